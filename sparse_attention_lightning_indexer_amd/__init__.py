@@ -515,9 +515,13 @@ def score_topk_fused_decode_noalloc(q, k_cache, block_table, seq_lens, query_len
     return idx, val
 
 
+from .mx4 import (MX4_EXPORTS, mx4_attend_selected, mx4_attend_window,  # noqa: E402
+                  mx4_attend_workspace_bytes, mx4_cache_read, mx4_cache_write)
+
 __all__ = [
     "score_prefill", "score_decode", "topk", "score_topk_fused_prefill",
     "score_topk_fused_decode", "score_topk_fused_decode_noalloc", "score_topk_fused_decode_blocks",
     "topk_blocks", "pool_keys", "score_topk_stream_prefill", "workspace_bytes", "load_library", "IndexerError",
-    "EXPORTS", "MAX_K_TOP",
+    "EXPORTS", "MAX_K_TOP", "mx4_cache_write", "mx4_cache_read", "mx4_attend_selected", "mx4_attend_window",
+    "mx4_attend_workspace_bytes", "MX4_EXPORTS",
 ]

@@ -19,7 +19,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libindexer.so")
-SOURCES = ["indexer_api.hip", "score_kernel.hip", "decode_kernel.hip", "topk_kernel.hip", "pool_kernel.hip", "stream_topk.hip"]
+SOURCES = ["indexer_api.hip", "score_kernel.hip", "decode_kernel.hip", "topk_kernel.hip", "pool_kernel.hip", "stream_topk.hip",
+           "mx4_api.hip", "mx4_cache.hip", "mx4_attend_f16.hip", "mx4_attend_bf16.hip"]
 PROBE_SOURCES = ["peak_probe.hip"]
 PROBE_LIB = os.path.join(PKG, "libpeak_probe.so")
 ARCH = os.environ.get("INDEXER_OFFLOAD_ARCH", "gfx950")

@@ -332,6 +332,16 @@ int device_cu_count() {
     return cached[dev];
 }
 
+int api_error(int status, const char *fmt, ...) {
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(g_last_error, sizeof g_last_error, fmt, ap);
+    va_end(ap);
+    return status;
+}
+
+int api_launch(hipError_t e, const char *what) { return hip_status(e, what); }
+
 }  // namespace lidx
 
 extern "C" {

@@ -135,4 +135,10 @@ hipError_t launch_pool(const _Float16 *k, int64_t k_ss, int n_keys, int head_dim
 // Number of compute units of the current device (cached per device).
 int device_cu_count();
 
+// The calling thread's last error (indexer_api.hip), for entry points declared
+// in other files.  Both return the status: api_error the one given, api_launch
+// that of a launch (clearing the message when it succeeded).
+int api_error(int status, const char *fmt, ...);
+int api_launch(hipError_t e, const char *what);
+
 }  // namespace lidx

@@ -1,0 +1,341 @@
+// C-ABI of the 4-bit cache operators (declared in include/indexer_mx4.h).
+// As in indexer_api.hip: every argument is checked on the host, without
+// touching device memory or calling HIP, before anything is enqueued.
+#include <math.h>
+
+#include "../../include/indexer_mx4.h"
+#include "internal.h"
+#include "mx4_internal.h"
+
+namespace {
+
+using lidx::api_error;
+
+bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
+constexpr int32_t kMaxKeys = INT32_MAX - 1023;  // room for positions of a last, partly filled tile
+
+#define MX4_FAIL(st, ...) return (indexer_status)api_error(st, __VA_ARGS__)
+#define MX4_TRY(expr)                                \
+    do {                                             \
+        const indexer_status st_ = (expr);           \
+        if (st_ != INDEXER_OK) return st_;           \
+    } while (0)
+
+indexer_status done(hipError_t e, const char *what) { return (indexer_status)lidx::api_launch(e, what); }
+
+indexer_status check_type(int32_t type) {
+    if (type != INDEXER_MX4_F16 && type != INDEXER_MX4_BF16)
+        MX4_FAIL(INDEXER_EINVAL, "type=%d is neither INDEXER_MX4_F16 nor INDEXER_MX4_BF16", type);
+    return INDEXER_OK;
+}
+
+indexer_status check_rows(const char *name, const void *p, int64_t st, int64_t sh, int32_t n_heads, int32_t head_dim) {
+    if (!p) MX4_FAIL(INDEXER_EINVAL, "%s is NULL", name);
+    if (!aligned(p, 16)) MX4_FAIL(INDEXER_EINVAL, "%s must be 16-byte aligned", name);
+    if (sh % 8 || (n_heads > 1 && sh < head_dim))
+        MX4_FAIL(INDEXER_EINVAL, "%s's head stride %lld must be >= head_dim and a multiple of 8", name, (long long)sh);
+    if (st % 8 || st < head_dim)
+        MX4_FAIL(INDEXER_EINVAL, "%s's row stride %lld must be >= head_dim and a multiple of 8", name, (long long)st);
+    return INDEXER_OK;
+}
+
+// Strides of the pages: no two rows may share bytes along one dimension.
+indexer_status check_pages(int32_t n_blocks, int32_t block_size, int32_t n_heads, int32_t head_dim,
+                           int64_t d_sb, int64_t d_ss, int64_t d_sh, int64_t s_sb, int64_t s_ss, int64_t s_sh,
+                           lidx::Mx4Pages *out) {
+    if (n_blocks < 0) MX4_FAIL(INDEXER_EINVAL, "n_blocks=%d must be >= 0", n_blocks);
+    if (block_size < 1) MX4_FAIL(INDEXER_EINVAL, "block_size=%d must be >= 1", block_size);
+    const int64_t row = head_dim / 2, srow = head_dim / 32;
+    if (d_sb % 16 || d_ss % 16 || d_sh % 16)
+        MX4_FAIL(INDEXER_EINVAL, "data strides %lld, %lld, %lld must be multiples of 16 bytes", (long long)d_sb,
+                 (long long)d_ss, (long long)d_sh);
+    if ((n_blocks > 1 && d_sb < row) || (block_size > 1 && d_ss < row) || (n_heads > 1 && d_sh < row))
+        MX4_FAIL(INDEXER_EINVAL, "data strides %lld, %lld, %lld must be >= head_dim/2 = %lld", (long long)d_sb,
+                 (long long)d_ss, (long long)d_sh, (long long)row);
+    if ((n_blocks > 1 && s_sb < srow) || (block_size > 1 && s_ss < srow) || (n_heads > 1 && s_sh < srow))
+        MX4_FAIL(INDEXER_EINVAL, "scale strides %lld, %lld, %lld must be >= head_dim/32 = %lld", (long long)s_sb,
+                 (long long)s_ss, (long long)s_sh, (long long)srow);
+    *out = lidx::Mx4Pages{d_sb, d_ss, d_sh, s_sb, s_ss, s_sh, n_blocks, block_size,
+                          lidx::fast_div((uint32_t)block_size), (int64_t)n_blocks * block_size};
+    return INDEXER_OK;
+}
+
+indexer_status check_cache(const char *name, const void *data, const void *scale) {
+    if (!data) MX4_FAIL(INDEXER_EINVAL, "%s_data is NULL", name);
+    if (!scale) MX4_FAIL(INDEXER_EINVAL, "%s_scale is NULL", name);
+    if (!aligned(data, 16)) MX4_FAIL(INDEXER_EINVAL, "%s_data must be 16-byte aligned", name);
+    return INDEXER_OK;
+}
+
+indexer_status check_row_shape(int32_t n_heads, int32_t head_dim) {
+    if (n_heads < 1 || n_heads > lidx::kMaxHeads || head_dim < 32 || head_dim > 1024 || head_dim % 32)
+        MX4_FAIL(INDEXER_ENOTSUP, "n_heads=%d head_dim=%d not supported (n_heads in 1..%d, head_dim a multiple of 32 "
+                 "in 32..1024)", n_heads, head_dim, lidx::kMaxHeads);
+    return INDEXER_OK;
+}
+
+bool attend_dim(int32_t d) { return d == 64 || d == 96 || d == 128 || d == 192 || d == 256; }
+
+// Everything the two attentions share; fills all of `a` but the selection or
+// window, and the launch fields.
+indexer_status check_attend(const void *q, int64_t q_st, int64_t q_sh, int32_t type, const void *kd, const void *ks,
+                            const void *vd, const void *vs, int32_t n_blocks, int32_t block_size, int64_t d_sb,
+                            int64_t d_ss, int64_t d_sh, int64_t s_sb, int64_t s_ss, int64_t s_sh,
+                            const int32_t *block_table, int64_t bt_stride, const int32_t *seq_lens,
+                            int32_t n_requests, int32_t query_len, int32_t max_seq_len, int32_t n_heads,
+                            int32_t n_kv, int32_t head_dim, float sm_scale, void *out, int64_t out_st,
+                            int64_t out_sh, float *lse, lidx::Mx4Attend *a) {
+    MX4_TRY(check_type(type));
+    if (n_requests < 0 || max_seq_len < 0)
+        MX4_FAIL(INDEXER_EINVAL, "n_requests=%d max_seq_len=%d must be >= 0", n_requests, max_seq_len);
+    if (query_len < 1) MX4_FAIL(INDEXER_EINVAL, "query_len=%d must be >= 1", query_len);
+    if (max_seq_len > kMaxKeys) MX4_FAIL(INDEXER_ENOTSUP, "max_seq_len=%d exceeds %d", max_seq_len, kMaxKeys);
+    if (n_heads < 1 || n_heads > lidx::kMaxHeads || n_kv < 1 || n_heads % n_kv || !attend_dim(head_dim))
+        MX4_FAIL(INDEXER_ENOTSUP, "n_heads=%d n_kv_heads=%d head_dim=%d not supported (n_heads in 1..%d, a multiple of "
+                 "n_kv_heads; head_dim 64, 96, 128, 192 or 256)", n_heads, n_kv, head_dim, lidx::kMaxHeads);
+    if ((int64_t)n_requests * query_len * n_heads > INT32_MAX)
+        MX4_FAIL(INDEXER_EINVAL, "n_requests*query_len*n_heads exceeds the int32 range");
+    if (!(sm_scale > 0.0f) || !isfinite(sm_scale) || !isfinite(sm_scale * 1.44269504f))
+        MX4_FAIL(INDEXER_EINVAL, "sm_scale=%g must be positive and finite", (double)sm_scale);
+    lidx::Mx4Pages pages;
+    MX4_TRY(check_pages(n_blocks, block_size, n_kv, head_dim, d_sb, d_ss, d_sh, s_sb, s_ss, s_sh, &pages));
+    MX4_TRY(check_rows("q", q, q_st, q_sh, n_heads, head_dim));
+    MX4_TRY(check_rows("out", out, out_st, out_sh, n_heads, head_dim));
+    if (n_blocks > 0) {
+        MX4_TRY(check_cache("k", kd, ks));
+        MX4_TRY(check_cache("v", vd, vs));
+    }
+    if (!seq_lens) MX4_FAIL(INDEXER_EINVAL, "seq_lens is NULL");
+    if (!aligned(seq_lens, 4) || !aligned(block_table, 4))
+        MX4_FAIL(INDEXER_EINVAL, "block_table and seq_lens must be 4-byte aligned");
+    if (lse && !aligned(lse, 4)) MX4_FAIL(INDEXER_EINVAL, "lse must be 4-byte aligned");
+    if (max_seq_len > 0) {
+        if (!block_table) MX4_FAIL(INDEXER_EINVAL, "block_table is NULL");
+        const int64_t need = ((int64_t)max_seq_len + block_size - 1) / block_size;
+        if (bt_stride < need)
+            MX4_FAIL(INDEXER_EINVAL, "bt_stride=%lld < ceil(max_seq_len/block_size)=%lld", (long long)bt_stride,
+                     (long long)need);
+    }
+    *a = lidx::Mx4Attend{};
+    a->q = q;
+    a->q_st = q_st;
+    a->q_sh = q_sh;
+    a->kd = (const uint8_t *)kd;
+    a->ks = (const uint8_t *)ks;
+    a->vd = (const uint8_t *)vd;
+    a->vs = (const uint8_t *)vs;
+    a->pages = pages;
+    a->block_table = block_table;
+    a->bt_stride = bt_stride;
+    a->seq_lens = seq_lens;
+    a->n_requests = n_requests;
+    a->q_len = query_len;
+    a->max_seq_len = max_seq_len;
+    a->n_heads = n_heads;
+    a->n_kv = n_kv;
+    a->group = n_heads / n_kv;
+    a->scale_log2 = (float)((double)sm_scale * 1.4426950408889634);
+    a->out = out;
+    a->out_st = out_st;
+    a->out_sh = out_sh;
+    a->lse = lse;
+    a->rows = n_requests * query_len;
+    a->div_group = lidx::fast_div((uint32_t)a->group);
+    a->div_kv = lidx::fast_div((uint32_t)n_kv);
+    a->div_pool = lidx::fast_div(1);
+    return INDEXER_OK;
+}
+
+indexer_status run_attend(lidx::Mx4Attend &a, int32_t type, int32_t head_dim, int64_t max_keys, void *workspace,
+                          size_t workspace_bytes, hipStream_t stream) {
+    const bool selected = a.idx != nullptr;
+    const lidx::Mx4Plan p = lidx::plan_mx4_attend(a.n_requests, a.q_len, max_keys, selected, a.n_heads, a.n_kv,
+                                                  head_dim);
+    if (p.workgroups > INT32_MAX) MX4_FAIL(INDEXER_EINVAL, "problem too large for one launch");
+    if (p.workspace_bytes && (!workspace || workspace_bytes < p.workspace_bytes || !aligned(workspace, 256)))
+        MX4_FAIL(INDEXER_EWORKSPACE, "attention needs %zu bytes of 256-byte aligned workspace, got %zu",
+                 p.workspace_bytes, workspace ? workspace_bytes : (size_t)0);
+    if (a.rows == 0) return done(hipSuccess, "");
+    a.units = p.units;
+    a.m_tiles = p.m_tiles;
+    a.n_splits = p.n_splits;
+    a.div_items = lidx::fast_div((uint32_t)(p.m_tiles * p.n_splits));
+    a.part_o = (float *)workspace;
+    a.part_ml = (float *)((char *)workspace + p.part_o_bytes);
+    return done(type == INDEXER_MX4_BF16 ? lidx::launch_mx4_attend_bf16(a, p, head_dim, stream)
+                                         : lidx::launch_mx4_attend_f16(a, p, head_dim, stream),
+                "attention kernel launch");
+}
+
+int64_t window_keys(int32_t max_seq_len, int32_t window, int32_t sinks) {
+    const int64_t w = (int64_t)window + sinks;
+    return window == 0 || w > max_seq_len ? max_seq_len : w;
+}
+
+}  // namespace
+
+namespace lidx {
+
+// A wave holds one tile of 16 query rows, or two where a unit has more rows.
+// Keys are shared among workgroups until there are about two per compute unit
+// (a workgroup's waves then still get a tile of 32 keys each).
+Mx4Plan plan_mx4_attend(int n_requests, int q_len, int64_t max_keys, bool selected, int n_heads, int n_kv,
+                        int head_dim) {
+    Mx4Plan p{};
+    const int group = n_heads / n_kv;
+    const int64_t rows = (int64_t)n_requests * q_len;
+    const int64_t n_m = selected ? group : (int64_t)q_len * group;
+    p.units = selected ? (int)rows : n_requests;
+    p.mt = n_m > 16 ? 2 : 1;
+    p.m_tiles = (int)((n_m + 16 * p.mt - 1) / (16 * p.mt));
+    const int waves = head_dim <= 128 ? 8 : 4;
+    const int64_t items = (int64_t)p.units * p.m_tiles * n_kv;
+    const int64_t most = (max_keys + 32 * waves - 1) / (32 * waves);
+    int64_t splits = items > 0 ? 512 / items : 1;
+    if (splits > most) splits = most;
+    if (splits > 64) splits = 64;
+    p.n_splits = splits < 1 ? 1 : (int)splits;
+    const int64_t pieces = (int64_t)p.units * p.m_tiles * p.n_splits;
+    p.workgroups = (pieces + 7) / 8 * 8 * n_kv;
+    if (p.n_splits > 1) {
+        const size_t parts = (size_t)rows * n_heads * p.n_splits;
+        p.part_o_bytes = (parts * head_dim * 4 + 255) / 256 * 256;
+        p.workspace_bytes = p.part_o_bytes + (parts * 8 + 255) / 256 * 256;
+    }
+    return p;
+}
+
+}  // namespace lidx
+
+extern "C" {
+
+indexer_status indexer_mx4_cache_write(const void *k, int64_t k_st, int64_t k_sh, const void *v, int64_t v_st,
+                                       int64_t v_sh, int32_t type, int32_t n_tokens, int32_t n_heads,
+                                       int32_t head_dim, const int64_t *slots, void *k_data, void *k_scale,
+                                       void *v_data, void *v_scale, int32_t n_blocks, int32_t block_size,
+                                       int64_t d_sb, int64_t d_ss, int64_t d_sh, int64_t s_sb, int64_t s_ss,
+                                       int64_t s_sh, void *stream) {
+    MX4_TRY(check_type(type));
+    if (n_tokens < 0) MX4_FAIL(INDEXER_EINVAL, "n_tokens=%d must be >= 0", n_tokens);
+    MX4_TRY(check_row_shape(n_heads, head_dim));
+    lidx::Mx4Write a{};
+    MX4_TRY(check_pages(n_blocks, block_size, n_heads, head_dim, d_sb, d_ss, d_sh, s_sb, s_ss, s_sh, &a.pages));
+    MX4_TRY(check_rows("k", k, k_st, k_sh, n_heads, head_dim));
+    if (n_blocks > 0) MX4_TRY(check_cache("k", k_data, k_scale));
+    if (v) {
+        MX4_TRY(check_rows("v", v, v_st, v_sh, n_heads, head_dim));
+        if (n_blocks > 0) MX4_TRY(check_cache("v", v_data, v_scale));
+    }
+    if (!slots) MX4_FAIL(INDEXER_EINVAL, "slots is NULL");
+    if (!aligned(slots, 8)) MX4_FAIL(INDEXER_EINVAL, "slots must be 8-byte aligned");
+    if (n_tokens == 0 || n_blocks == 0) return done(hipSuccess, "");
+    a.x[0] = k;
+    a.x[1] = v;
+    a.st[0] = k_st;
+    a.st[1] = v_st;
+    a.sh[0] = k_sh;
+    a.sh[1] = v_sh;
+    a.data[0] = (uint8_t *)k_data;
+    a.data[1] = (uint8_t *)v_data;
+    a.scale[0] = (uint8_t *)k_scale;
+    a.scale[1] = (uint8_t *)v_scale;
+    a.slots = slots;
+    a.n_tokens = n_tokens;
+    a.n_heads = n_heads;
+    a.head_dim = head_dim;
+    a.n_tensors = v ? 2 : 1;
+    a.div_e = lidx::fast_div((uint32_t)(n_heads * (head_dim / 8)));
+    a.div_c = lidx::fast_div((uint32_t)(head_dim / 8));
+    a.bf16 = type == INDEXER_MX4_BF16;
+    return done(lidx::launch_mx4_write(a, (hipStream_t)stream), "cache write launch");
+}
+
+indexer_status indexer_mx4_cache_read(const void *data, const void *scale, int32_t n_blocks, int32_t block_size,
+                                      int64_t d_sb, int64_t d_ss, int64_t d_sh, int64_t s_sb, int64_t s_ss,
+                                      int64_t s_sh, const int64_t *slots, int32_t n_rows, int32_t n_heads,
+                                      int32_t head_dim, void *out, int64_t out_st, int64_t out_sh, int32_t type,
+                                      void *stream) {
+    MX4_TRY(check_type(type));
+    if (n_rows < 0) MX4_FAIL(INDEXER_EINVAL, "n_rows=%d must be >= 0", n_rows);
+    MX4_TRY(check_row_shape(n_heads, head_dim));
+    lidx::Mx4Read a{};
+    MX4_TRY(check_pages(n_blocks, block_size, n_heads, head_dim, d_sb, d_ss, d_sh, s_sb, s_ss, s_sh, &a.pages));
+    if (n_blocks > 0) MX4_TRY(check_cache("the cache's", data, scale));
+    MX4_TRY(check_rows("out", out, out_st, out_sh, n_heads, head_dim));
+    if (!slots) MX4_FAIL(INDEXER_EINVAL, "slots is NULL");
+    if (!aligned(slots, 8)) MX4_FAIL(INDEXER_EINVAL, "slots must be 8-byte aligned");
+    if (n_rows == 0) return done(hipSuccess, "");
+    a.data = (const uint8_t *)data;
+    a.scale = (const uint8_t *)scale;
+    a.slots = slots;
+    a.out = out;
+    a.st = out_st;
+    a.sh = out_sh;
+    a.n_rows = n_rows;
+    a.n_heads = n_heads;
+    a.head_dim = head_dim;
+    a.div_e = lidx::fast_div((uint32_t)(n_heads * (head_dim / 8)));
+    a.div_c = lidx::fast_div((uint32_t)(head_dim / 8));
+    a.bf16 = type == INDEXER_MX4_BF16;
+    return done(lidx::launch_mx4_read(a, (hipStream_t)stream), "cache read launch");
+}
+
+indexer_status indexer_mx4_attend_selected(
+    const void *q, int64_t q_st, int64_t q_sh, int32_t type, const void *k_data, const void *k_scale,
+    const void *v_data, const void *v_scale, int32_t n_blocks, int32_t block_size, int64_t d_sb, int64_t d_ss,
+    int64_t d_sh, int64_t s_sb, int64_t s_ss, int64_t s_sh, const int32_t *block_table, int64_t bt_stride,
+    const int32_t *seq_lens, int32_t n_requests, int32_t query_len, int32_t max_seq_len, int32_t n_heads,
+    int32_t n_kv_heads, int32_t head_dim, float sm_scale, const int32_t *idx, int64_t idx_stride, int32_t n_sel,
+    int32_t pool_size, void *out, int64_t out_st, int64_t out_sh, float *lse, void *workspace,
+    size_t workspace_bytes, void *stream) {
+    lidx::Mx4Attend a;
+    MX4_TRY(check_attend(q, q_st, q_sh, type, k_data, k_scale, v_data, v_scale, n_blocks, block_size, d_sb, d_ss, d_sh,
+                         s_sb, s_ss, s_sh, block_table, bt_stride, seq_lens, n_requests, query_len, max_seq_len,
+                         n_heads, n_kv_heads, head_dim, sm_scale, out, out_st, out_sh, lse, &a));
+    if (n_sel < 0) MX4_FAIL(INDEXER_EINVAL, "n_sel=%d must be >= 0", n_sel);
+    if (pool_size < 1) MX4_FAIL(INDEXER_EINVAL, "pool_size=%d must be >= 1", pool_size);
+    if (pool_size > lidx::kMaxPool) MX4_FAIL(INDEXER_ENOTSUP, "pool_size=%d exceeds %d", pool_size, lidx::kMaxPool);
+    if ((int64_t)n_sel * pool_size > kMaxKeys)
+        MX4_FAIL(INDEXER_ENOTSUP, "n_sel*pool_size=%lld exceeds %d", (long long)n_sel * pool_size, kMaxKeys);
+    if (!idx) MX4_FAIL(INDEXER_EINVAL, "idx is NULL");
+    if (!aligned(idx, 4)) MX4_FAIL(INDEXER_EINVAL, "idx must be 4-byte aligned");
+    if (idx_stride < n_sel)
+        MX4_FAIL(INDEXER_EINVAL, "idx_stride=%lld < n_sel=%d", (long long)idx_stride, n_sel);
+    a.idx = idx;
+    a.idx_st = idx_stride;
+    a.n_sel = n_sel;
+    a.pool = pool_size;
+    a.div_pool = lidx::fast_div((uint32_t)pool_size);
+    return run_attend(a, type, head_dim, (int64_t)n_sel * pool_size, workspace, workspace_bytes, (hipStream_t)stream);
+}
+
+indexer_status indexer_mx4_attend_window(
+    const void *q, int64_t q_st, int64_t q_sh, int32_t type, const void *k_data, const void *k_scale,
+    const void *v_data, const void *v_scale, int32_t n_blocks, int32_t block_size, int64_t d_sb, int64_t d_ss,
+    int64_t d_sh, int64_t s_sb, int64_t s_ss, int64_t s_sh, const int32_t *block_table, int64_t bt_stride,
+    const int32_t *seq_lens, int32_t n_requests, int32_t query_len, int32_t max_seq_len, int32_t n_heads,
+    int32_t n_kv_heads, int32_t head_dim, float sm_scale, int32_t window, int32_t sinks, void *out, int64_t out_st,
+    int64_t out_sh, float *lse, void *workspace, size_t workspace_bytes, void *stream) {
+    lidx::Mx4Attend a;
+    MX4_TRY(check_attend(q, q_st, q_sh, type, k_data, k_scale, v_data, v_scale, n_blocks, block_size, d_sb, d_ss, d_sh,
+                         s_sb, s_ss, s_sh, block_table, bt_stride, seq_lens, n_requests, query_len, max_seq_len,
+                         n_heads, n_kv_heads, head_dim, sm_scale, out, out_st, out_sh, lse, &a));
+    if (window < 0 || sinks < 0) MX4_FAIL(INDEXER_EINVAL, "window=%d sinks=%d must be >= 0", window, sinks);
+    a.window = window;
+    a.sinks = window ? sinks : 0;
+    return run_attend(a, type, head_dim, window_keys(max_seq_len, window, sinks), workspace, workspace_bytes,
+                      (hipStream_t)stream);
+}
+
+size_t indexer_mx4_attend_workspace_bytes(int32_t n_requests, int32_t query_len, int32_t max_keys, int32_t selected,
+                                          int32_t n_heads, int32_t n_kv_heads, int32_t head_dim) {
+    if (n_requests < 0 || query_len < 1 || max_keys < 0 || n_heads < 1 || n_heads > lidx::kMaxHeads ||
+        n_kv_heads < 1 || n_heads % n_kv_heads || !attend_dim(head_dim) ||
+        (int64_t)n_requests * query_len * n_heads > INT32_MAX)
+        return (size_t)-1;
+    return lidx::plan_mx4_attend(n_requests, query_len, max_keys, selected != 0, n_heads, n_kv_heads, head_dim)
+        .workspace_bytes;
+}
+
+}  // extern "C"

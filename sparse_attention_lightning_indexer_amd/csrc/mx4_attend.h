@@ -1,0 +1,577 @@
+// Attention over the 4-bit cache for gfx950: the kernel, shared by its f16 and
+// bf16 instances (mx4_attend_f16.hip, mx4_attend_bf16.hip).
+//
+// For a query row (token, head) and the positions p it attends to,
+//   z[p] = c * q . K[p]   (c = sm_scale * log2 e),  out = sum 2^(z[p] - L) V[p],
+//   L = log2 sum 2^z[p];  one pass with the running maximum m and sum l of a
+// softmax, the accumulated product rescaled by 2^(m_old - m_new).
+//
+// A wave holds MT tiles of 16 query rows that share a K/V head and walks tiles
+// of 32 keys of its own; the waves of a workgroup take the tiles of a row's
+// keys in turn and join their (m, l, product) through LDS at the end, and rows
+// with too few workgroups share their keys among several, joined by a second
+// kernel.  Nothing in the loop waits for another wave.
+//
+//  - Scores: S^T = K Q^T on 16x16x32 MFMAs.  The contraction runs over the
+//    head dimension in any order both operands agree on, so a lane takes
+//    head_dim / 4 consecutive values of its key (l & 15): one wide load of
+//    codes and one scale byte (at head dimension 128, exactly one block).
+//  - The conversion from 4 bits applies the scale and gives the query's type
+//    exactly (caches written from it), two values an instruction.
+//  - A lane then holds 8 scores of one query row, (l & 15), which is the
+//    layout the product's P operand wants: P never leaves its lane, and
+//    neither do m, l and the rescaling of O^T = V^T P^T.
+//  - V's rows are converted like K's, stored to the wave's own LDS rows and
+//    read back transposed (ds_read_b64_tr_b16), 16 dimensions by 4 keys each.
+//    Rows are padded by 32 bytes: the 16 rows one read touches then cover all
+//    banks twice, the least 512 bytes can take.
+//  - Key (l >> 4) + 4 i + 16 u stands in row 4 (l >> 4) + i of score tile u, so
+//    one transposed read takes 16 consecutive LDS rows.
+//  - Loads run ahead: a tile's codes while the one before computes, its page
+//    ids one further, the selected indices one more.
+//
+// Masked positions: their scores become -inf by selection, so K's NaN there
+// never spreads; V's blocks of NaN are replaced by zeros in the product, and
+// the rows that do attend to such a key get their NaN by a mask of blocks
+// (0 * NaN would otherwise reach rows that must not see the key).
+#pragma once
+
+#include <math.h>
+
+#include "device_common.h"
+#include "mx4_internal.h"
+
+namespace lidx {
+namespace mx4 {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+template <bool BF16>
+struct Type;
+template <>
+struct Type<false> {
+    typedef half8 vec8;
+    typedef _Float16 one;
+    static __device__ __forceinline__ f32x4 mfma(vec8 a, vec8 b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+    }
+    // 8 codes of one word under a scale
+    static __device__ __forceinline__ vec8 from4(uint32_t w, float f) {
+        u32x4 r;
+        r.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, f, 0));
+        r.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, f, 1));
+        r.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, f, 2));
+        r.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, f, 3));
+        return __builtin_bit_cast(vec8, r);
+    }
+};
+template <>
+struct Type<true> {
+    typedef bf8 vec8;
+    typedef __bf16 one;
+    static __device__ __forceinline__ f32x4 mfma(vec8 a, vec8 b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ vec8 from4(uint32_t w, float f) {
+        u32x4 r;
+        r.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, f, 0));
+        r.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, f, 1));
+        r.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, f, 2));
+        r.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, f, 3));
+        return __builtin_bit_cast(vec8, r);
+    }
+};
+
+// Over the four lanes that share l & 15.
+__device__ __forceinline__ float quarter_max(float v) {
+    const unsigned u = __builtin_bit_cast(unsigned, v);
+    auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    const unsigned w = __builtin_bit_cast(
+        unsigned, fmaxf(__builtin_bit_cast(float, (unsigned)a[0]), __builtin_bit_cast(float, (unsigned)a[1])));
+    auto b = __builtin_amdgcn_permlane16_swap(w, w, false, false);
+    return fmaxf(__builtin_bit_cast(float, (unsigned)b[0]), __builtin_bit_cast(float, (unsigned)b[1]));
+}
+__device__ __forceinline__ float quarter_sum(float v) {
+    const unsigned u = __builtin_bit_cast(unsigned, v);
+    auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    const unsigned w = __builtin_bit_cast(
+        unsigned, __builtin_bit_cast(float, (unsigned)a[0]) + __builtin_bit_cast(float, (unsigned)a[1]));
+    auto b = __builtin_amdgcn_permlane16_swap(w, w, false, false);
+    return __builtin_bit_cast(float, (unsigned)b[0]) + __builtin_bit_cast(float, (unsigned)b[1]);
+}
+
+constexpr float kNegInf = -__builtin_huge_valf();
+
+template <int D>
+struct Shape {
+    static constexpr int KS = D / 32;               // MFMA steps over the head dimension
+    static constexpr int NT = D / 16;               // 16-dimension tiles of the product
+    static constexpr int ROW = 2 * D + 32;          // bytes of a V row in LDS
+    static constexpr int WAVES = D <= 128 ? 8 : 4;
+    static constexpr int OROW = D + 4;              // floats of a row of the join (padded)
+    static constexpr int JOIN = WAVES * 16 * OROW * 4;
+    static constexpr int STAGE = WAVES * 32 * ROW;
+    static constexpr int LDS = (STAGE > JOIN ? STAGE : JOIN) + WAVES * 16 * 8;
+};
+
+// One workgroup's share of the work.
+struct Item {
+    int unit, kv, split, m0;  // row unit, K/V head, key share, first query row of its tile
+};
+
+__device__ __forceinline__ Item item_of(const Mx4Attend &a, int mt) {
+    // Workgroups b, b + 8, b + 16, ... run on one XCD.  Piece w = (unit, row
+    // tile, key share) runs on XCD w mod 8 for all its K/V heads, one after the
+    // other, so the 128-byte lines the heads of a token share are fetched into
+    // one L2.
+    Item it;
+    const uint32_t b = blockIdx.x >> 3;
+    const uint32_t r = quotient(b, a.div_kv);
+    it.kv = (int)(b - r * a.div_kv.d);
+    const uint32_t w = r * 8u + (blockIdx.x & 7u);
+    it.unit = (int)quotient(w, a.div_items);  // row tiles * key shares of a unit
+    const uint32_t rest = w - (uint32_t)it.unit * a.div_items.d;
+    const uint32_t tile = rest / (uint32_t)a.n_splits;
+    it.split = (int)(rest - tile * (uint32_t)a.n_splits);
+    it.m0 = (int)tile * 16 * mt;
+    return it;
+}
+
+template <bool BF16, int D, int MT, bool SELECTED>
+__global__ void __launch_bounds__(Shape<D>::WAVES * 64) mx4_attend_kernel(Mx4Attend a) {
+    using T = Type<BF16>;
+    using S = Shape<D>;
+    typedef typename T::vec8 vec8;
+    constexpr int KS = S::KS, NT = S::NT, W = S::WAVES;
+    __shared__ __attribute__((aligned(16))) unsigned char smem[S::LDS];
+
+    const Item it = item_of(a, MT);
+    if (it.unit >= a.units) return;
+    const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
+    const int col = lane & 15, qd = lane >> 4;
+
+    // the unit's request, query rows and visible keys
+    const int req = SELECTED ? it.unit / a.q_len : it.unit;
+    const int seq = a.seq_lens[req];
+    const int n_m = SELECTED ? a.group : a.q_len * a.group;  // query rows of the unit at this K/V head
+    auto token_of = [&](int m) { return SELECTED ? it.unit : req * a.q_len + (int)quotient((uint32_t)m, a.div_group); };
+    auto head_of = [&](int m) {
+        return it.kv * a.group + (SELECTED ? m : m - (int)quotient((uint32_t)m, a.div_group) * a.group);
+    };
+    // keys a token sees, before the cap by max_seq_len
+    auto seen_of = [&](int token) { return (int64_t)seq - a.q_len + 1 + (token - req * a.q_len); };
+    const int64_t first_seen = seen_of(token_of(it.m0));
+    const int64_t last_seen = seen_of(token_of(min(it.m0 + 16 * MT, n_m) - 1));
+    const int cap_first = (int)max((int64_t)0, min(first_seen, (int64_t)a.max_seq_len));
+    const int cap_last = (int)max((int64_t)0, min(last_seen, (int64_t)a.max_seq_len));
+
+    // tiles of 32 keys: selected entries in order; or the first tokens, then the window
+    int n_tiles, sink_tiles = 0, base = 0;
+    if (SELECTED) {
+        n_tiles = cap_last > 0 ? (int)(((int64_t)a.n_sel * a.pool + 31) / 32) : 0;
+    } else {
+        int64_t lo = a.window ? first_seen - a.window : 0;
+        base = lo > 0 ? (int)min(lo, (int64_t)cap_last) & ~31 : 0;
+        sink_tiles = (min(a.sinks, base) + 31) / 32;
+        if (!a.window) sink_tiles = 0;
+        n_tiles = sink_tiles + (cap_last - base + 31) / 32;
+    }
+    if (a.pages.n_blocks == 0) n_tiles = 0;
+    const int per = (n_tiles + a.n_splits - 1) / a.n_splits;
+    const int t_end = min(n_tiles, (it.split + 1) * per);
+    const int t_begin = it.split * per + wave;
+
+    // per query-row tile: this lane's column of Q (its row's values in the
+    // order of the lane's part of the contraction), and the row's window
+    vec8 q[MT][KS];
+    int row_end[MT], row_start[MT];
+    float mx[MT], ls[MT];
+    f32x4 o[MT][NT];
+    uint32_t nan_blocks[MT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        const int m = it.m0 + mt * 16 + col;
+        const int mc = min(m, n_m - 1);
+        const int token = token_of(mc);
+        const uint4 *src = reinterpret_cast<const uint4 *>((const uint16_t *)a.q + (int64_t)token * a.q_st +
+                                                           (int64_t)head_of(mc) * a.q_sh + qd * (KS * 8));
+#pragma unroll
+        for (int s = 0; s < KS; ++s) q[mt][s] = __builtin_bit_cast(vec8, src[s]);
+        const int64_t seen = seen_of(token);
+        row_end[mt] = (int)max((int64_t)0, min(seen, (int64_t)a.max_seq_len));
+        row_start[mt] = a.window ? (int)min(max((int64_t)0, seen - a.window), (int64_t)row_end[mt]) : 0;
+        mx[mt] = kNegInf;
+        ls[mt] = 0.0f;
+        nan_blocks[mt] = 0u;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) o[mt][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+
+    // this lane's two keys of a tile: rows col of score tiles 0 and 1
+    const int key0 = (col >> 2) + 4 * (col & 3);
+    const int64_t head_d = (int64_t)it.kv * a.pages.d_sh + qd * (KS * 4);
+    const int64_t head_s = (int64_t)it.kv * a.pages.s_sh;
+    const int32_t *table = a.block_table + (int64_t)req * a.bt_stride;
+    const int32_t *sel = SELECTED ? a.idx + (int64_t)it.unit * a.idx_st : nullptr;
+    const int n_entries = SELECTED ? a.n_sel * a.pool : 0;
+
+    // stage 1: the entry's selected index
+    auto load_index = [&](int tile, int u) -> int {
+        const int e = tile * 32 + u * 16 + key0;
+        if (tile >= t_end || e >= n_entries) return -1;
+        return sel[a.pool == 1 ? e : (int)quotient((uint32_t)e, a.div_pool)];
+    };
+    // stage 2: the position (-1: none), and its page's id
+    auto position = [&](int tile, int u, int id) -> int {
+        if (tile >= t_end) return -1;
+        if (SELECTED) {
+            if (id < 0) return -1;
+            if (a.pool == 1) return id < cap_last ? id : -1;
+            const int e = tile * 32 + u * 16 + key0;
+            const int64_t p = (int64_t)id * a.pool + (e - (int)quotient((uint32_t)e, a.div_pool) * a.pool);
+            return p < cap_last ? (int)p : -1;
+        }
+        const int p = (tile < sink_tiles ? tile * 32 : base + (tile - sink_tiles) * 32) + u * 16 + key0;
+        return p < cap_last ? p : -1;
+    };
+    auto load_page = [&](int p) -> int {
+        return p < 0 ? -1 : table[quotient((uint32_t)p, a.pages.div_bs)];
+    };
+    // a lane's KS words (8 values each) lie in blocks (qd * KS + s) / 4: at most NB
+    constexpr int NB = KS % 4 == 0 ? KS / 4 : (KS == 2 ? 1 : 2);
+    struct Raw {
+        uint32_t k[KS], v[KS];
+        uint32_t sk[NB], sv[NB];
+        bool ok;
+    };
+    const int blk0 = qd * KS / 4;
+    auto load_rows = [&](int p, int page) {
+        Raw r;
+        r.ok = p >= 0 && (uint32_t)page < (uint32_t)a.pages.n_blocks;
+        const int64_t pg = r.ok ? page : 0;
+        const int64_t off = r.ok ? p - (int)quotient((uint32_t)p, a.pages.div_bs) * a.pages.block_size : 0;
+        const int64_t at = pg * a.pages.d_sb + off * a.pages.d_ss + head_d;
+        const uint32_t *kd = reinterpret_cast<const uint32_t *>(a.kd + at);
+        const uint32_t *vd = reinterpret_cast<const uint32_t *>(a.vd + at);
+        __builtin_memcpy(r.k, __builtin_assume_aligned(kd, KS % 4 == 0 ? 16 : (KS % 2 == 0 ? 8 : 4)), KS * 4);
+        __builtin_memcpy(r.v, __builtin_assume_aligned(vd, KS % 4 == 0 ? 16 : (KS % 2 == 0 ? 8 : 4)), KS * 4);
+        const int64_t sat = pg * a.pages.s_sb + off * a.pages.s_ss + head_s;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const int blk = min(blk0 + b, D / 32 - 1);
+            r.sk[b] = a.ks[sat + blk];
+            r.sv[b] = a.vs[sat + blk];
+        }
+        return r;
+    };
+    // which of the lane's blocks its word s belongs to
+    auto block_of = [&](int s) { return KS % 4 == 0 ? s / 4 : (KS == 2 ? 0 : (qd * KS + s) / 4 - blk0); };
+
+    typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+    typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
+    lds_u8 *stage = (lds_u8 *)smem + wave * (32 * S::ROW);
+
+    int id[2] = {-1, -1}, pos[2], page[2];
+    Raw raw[2], nxt[2];
+    int npos[2];
+    if (t_begin < t_end) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            if (SELECTED) id[u] = load_index(t_begin, u);
+            pos[u] = position(t_begin, u, id[u]);
+            page[u] = load_page(pos[u]);
+            raw[u] = load_rows(pos[u], page[u]);
+            if (SELECTED) id[u] = load_index(t_begin + W, u);
+            npos[u] = position(t_begin + W, u, id[u]);
+            page[u] = load_page(npos[u]);
+            if (SELECTED) id[u] = load_index(t_begin + 2 * W, u);
+        }
+    }
+
+    for (int tile = t_begin; tile < t_end; tile += W) {
+        // loads for the tiles ahead
+        int after[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            nxt[u] = load_rows(npos[u], page[u]);
+            after[u] = position(tile + 2 * W, u, id[u]);
+            page[u] = load_page(after[u]);
+            if (SELECTED) id[u] = load_index(tile + 3 * W, u);
+        }
+
+        // scores
+        f32x4 s[MT][2];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) s[mt][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int st = 0; st < KS; ++st) {
+                uint32_t sb = raw[u].sk[0];
+#pragma unroll
+                for (int b = 1; b < NB; ++b) sb = block_of(st) == b ? raw[u].sk[b] : sb;
+                const vec8 kv = T::from4(raw[u].k[st], __builtin_bit_cast(float, sb << 23));
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) s[mt][u] = T::mfma(kv, q[mt][st], s[mt][u]);
+            }
+
+        // V's rows into the wave's LDS, blocks of NaN as zeros
+        uint64_t valid[2];
+        bool has_nan = false;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            valid[u] = __ballot(raw[u].ok);
+            uint32_t sv[NB];
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const bool bad = raw[u].sv[b] == 255u;
+                has_nan |= raw[u].ok && bad;
+                sv[b] = raw[u].ok && !bad ? raw[u].sv[b] : 0u;
+            }
+#pragma unroll
+            for (int st = 0; st < KS; ++st) {
+                uint32_t sb = sv[0];
+#pragma unroll
+                for (int b = 1; b < NB; ++b) sb = block_of(st) == b ? sv[b] : sb;
+                const vec8 vv = T::from4(raw[u].v[st], __builtin_bit_cast(float, sb << 23));
+                *(lds_u32x4 *)(stage + (u * 16 + key0) * S::ROW + (qd * KS + st) * 16) = __builtin_bit_cast(u32x4, vv);
+            }
+        }
+
+        // which scores count: bit 4 * qd + i of valid[u] is this lane's score i of tile u
+        const int p0 = SELECTED ? 0 : (tile < sink_tiles ? tile * 32 : base + (tile - sink_tiles) * 32);
+        bool whole = (valid[0] & valid[1] & 0xffffull) == 0xffffull;
+        if (!SELECTED) {
+            whole = whole && p0 + 32 <= cap_first &&
+                    (!a.window || p0 + 32 <= a.sinks || (int64_t)p0 >= last_seen - a.window);
+        }
+        auto counts = [&](int mt, int u, int i) -> bool {
+            bool in = (valid[u] >> (4 * qd + i)) & 1ull;
+            if (!SELECTED) {
+                const int p = p0 + u * 16 + 4 * i + qd;
+                in = in && p < row_end[mt] && (p >= row_start[mt] || p < a.sinks);
+            }
+            return in;
+        };
+        if (!whole) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s[mt][u][i] = counts(mt, u, i) ? s[mt][u][i] : kNegInf;
+        }
+        if (__ballot(has_nan)) {
+            // rare: mark, for each row, the blocks of V whose sum is NaN
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+                for (int kk = 0; kk < 16; ++kk) {  // row of score tile u
+                    uint32_t blocks = 0;
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        const uint64_t who = __ballot(raw[u].ok && raw[u].sv[b] == 255u && col == kk);
+#pragma unroll
+                        for (int g = 0; g < 4; ++g)
+                            if ((who >> (16 * g)) & 0xffffull) {
+                                const int blk = min(g * KS / 4 + b, D / 32 - 1);
+                                blocks |= 1u << blk;
+                            }
+                    }
+                    if (!blocks) continue;
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        bool in = (valid[u] >> kk) & 1ull;
+                        if (!SELECTED) {
+                            const int p = p0 + u * 16 + 4 * (kk & 3) + (kk >> 2);
+                            in = in && p < row_end[mt] && (p >= row_start[mt] || p < a.sinks);
+                        }
+                        if (in) nan_blocks[mt] |= blocks;
+                    }
+                }
+        }
+
+        // softmax: the maximum over the tile, the sum of this lane's part
+        vec8 p[MT];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            float top = fmaxf(fmaxf(fmaxf(s[mt][0][0], s[mt][0][1]), fmaxf(s[mt][0][2], s[mt][0][3])),
+                              fmaxf(fmaxf(s[mt][1][0], s[mt][1][1]), fmaxf(s[mt][1][2], s[mt][1][3])));
+            top = quarter_max(top) * a.scale_log2;
+            if (__ballot(top > mx[mt])) {
+                const float m_new = fmaxf(mx[mt], top);
+                const float f = m_new > mx[mt] ? __builtin_amdgcn_exp2f(mx[mt] - m_new) : 1.0f;
+                mx[mt] = m_new;
+                ls[mt] *= f;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[mt][n][i] *= f;
+            }
+            const float sub = mx[mt] == kNegInf ? 0.0f : mx[mt];
+            float sum = 0.0f;
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[mt][u][i], a.scale_log2, -sub));
+                    sum += e;
+                    p[mt][u * 4 + i] = (typename T::one)e;
+                }
+            ls[mt] += sum;
+        }
+
+        // O^T += V^T P^T
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            lds_u8 *src = stage + (4 * (col >> 2) + qd) * S::ROW + n * 32 + (col & 3) * 8;
+            union {
+                s16x4 h[2];
+                vec8 v;
+            } vt;
+            vt.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)src);
+            vt.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(src + 16 * S::ROW));
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) o[mt][n] = T::mfma(vt.v, p[mt], o[mt][n]);
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            raw[u] = nxt[u];
+            npos[u] = after[u];
+        }
+    }
+
+    // join the waves: each writes its product, m and l; every thread then adds
+    // up a share of the outputs
+    float *jo = reinterpret_cast<float *>(smem);
+    float *jml = reinterpret_cast<float *>(smem + (S::STAGE > S::JOIN ? S::STAGE : S::JOIN));
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        const float l = quarter_sum(ls[mt]);
+        __syncthreads();  // the staging rows, or the last tile's join, are no longer read
+        float *dst = jo + (wave * 16 + col) * S::OROW;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            f32x4 v = o[mt][n];
+            if ((nan_blocks[mt] >> (n / 2)) & 1u) v = f32x4{NAN, NAN, NAN, NAN};
+            *reinterpret_cast<f32x4 *>(dst + n * 16 + qd * 4) = v;
+        }
+        if (qd == 0) {
+            jml[(wave * 16 + col) * 2] = mx[mt];
+            jml[(wave * 16 + col) * 2 + 1] = l;
+        }
+        __syncthreads();
+        for (int e = threadIdx.x; e < 16 * (D / 8); e += W * 64) {
+            const int row = e / (D / 8), c = e - row * (D / 8);
+            const int m = it.m0 + mt * 16 + row;
+            if (m >= n_m) continue;
+            float m_all = kNegInf;
+#pragma unroll
+            for (int w = 0; w < W; ++w) m_all = fmaxf(m_all, jml[(w * 16 + row) * 2]);
+            const float sub = m_all == kNegInf ? 0.0f : m_all;
+            float l_all = 0.0f, acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                const float f = __builtin_amdgcn_exp2f(jml[(w * 16 + row) * 2] - sub);
+                l_all += f * jml[(w * 16 + row) * 2 + 1];
+                const float *src = jo + (w * 16 + row) * S::OROW + c * 8;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) acc[i] += f * src[i];
+            }
+            const int token = token_of(m), head = head_of(m);
+            const int64_t th = (int64_t)token * a.n_heads + head;
+            if (a.n_splits > 1) {
+                float *dst2 = a.part_o + (th * a.n_splits + it.split) * D + c * 8;
+                *reinterpret_cast<f32x4 *>(dst2) = f32x4{acc[0], acc[1], acc[2], acc[3]};
+                *reinterpret_cast<f32x4 *>(dst2 + 4) = f32x4{acc[4], acc[5], acc[6], acc[7]};
+                if (c == 0) {
+                    a.part_ml[(th * a.n_splits + it.split) * 2] = m_all;
+                    a.part_ml[(th * a.n_splits + it.split) * 2 + 1] = l_all;
+                }
+            } else {
+                const float inv = l_all == 0.0f ? 0.0f : 1.0f / l_all;
+                vec8 r;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) r[i] = (typename T::one)(acc[i] * inv);
+                *reinterpret_cast<vec8 *>((uint16_t *)a.out + (int64_t)token * a.out_st + (int64_t)head * a.out_sh +
+                                          c * 8) = r;
+                if (c == 0 && a.lse)
+                    a.lse[th] = l_all == 0.0f ? kNegInf : (m_all + log2f(l_all)) * 0.69314718055994530942f;
+            }
+        }
+    }
+}
+
+// Joins the shares of rows whose keys were split: one thread per 8 outputs.
+template <bool BF16, int D>
+__global__ void __launch_bounds__(256) mx4_join_kernel(Mx4Attend a) {
+    using T = Type<BF16>;
+    typedef typename T::vec8 vec8;
+    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t th = e / (D / 8);
+    const int c = (int)(e - th * (D / 8));
+    if (th >= (int64_t)a.rows * a.n_heads) return;
+    const float *ml = a.part_ml + th * a.n_splits * 2;
+    float m_all = kNegInf;
+    for (int s = 0; s < a.n_splits; ++s) m_all = fmaxf(m_all, ml[2 * s]);
+    const float sub = m_all == kNegInf ? 0.0f : m_all;
+    float l_all = 0.0f, acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    for (int s = 0; s < a.n_splits; ++s) {
+        const float f = __builtin_amdgcn_exp2f(ml[2 * s] - sub);
+        l_all += f * ml[2 * s + 1];
+        const f32x4 *src = reinterpret_cast<const f32x4 *>(a.part_o + (th * a.n_splits + s) * D + c * 8);
+        const f32x4 x = src[0], y = src[1];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            acc[i] += f * x[i];
+            acc[4 + i] += f * y[i];
+        }
+    }
+    const int64_t token = th / a.n_heads;
+    const int head = (int)(th - token * a.n_heads);
+    const float inv = l_all == 0.0f ? 0.0f : 1.0f / l_all;
+    vec8 r;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = (typename T::one)(acc[i] * inv);
+    *reinterpret_cast<vec8 *>((uint16_t *)a.out + token * a.out_st + (int64_t)head * a.out_sh + c * 8) = r;
+    if (c == 0 && a.lse) a.lse[th] = l_all == 0.0f ? kNegInf : (m_all + log2f(l_all)) * 0.69314718055994530942f;
+}
+
+template <bool BF16, int D, int MT>
+hipError_t launch_tiles(const Mx4Attend &a, const Mx4Plan &p, hipStream_t stream) {
+    const dim3 grid((unsigned)p.workgroups), block(Shape<D>::WAVES * 64);
+    if (a.idx)
+        hipLaunchKernelGGL((mx4_attend_kernel<BF16, D, MT, true>), grid, block, 0, stream, a);
+    else
+        hipLaunchKernelGGL((mx4_attend_kernel<BF16, D, MT, false>), grid, block, 0, stream, a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.n_splits == 1) return e;
+    const int64_t threads = (int64_t)a.rows * a.n_heads * (D / 8);
+    hipLaunchKernelGGL((mx4_join_kernel<BF16, D>), dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, stream, a);
+    return hipGetLastError();
+}
+
+template <bool BF16, int D>
+hipError_t launch_dim(const Mx4Attend &a, const Mx4Plan &p, hipStream_t stream) {
+    if (p.mt == 1) return launch_tiles<BF16, D, 1>(a, p, stream);
+    return launch_tiles<BF16, D, 2>(a, p, stream);
+}
+
+template <bool BF16>
+hipError_t launch_attend(const Mx4Attend &a, const Mx4Plan &p, int head_dim, hipStream_t stream) {
+    switch (head_dim) {
+        case 64: return launch_dim<BF16, 64>(a, p, stream);
+        case 96: return launch_dim<BF16, 96>(a, p, stream);
+        case 128: return launch_dim<BF16, 128>(a, p, stream);
+        case 192: return launch_dim<BF16, 192>(a, p, stream);
+        case 256: return launch_dim<BF16, 256>(a, p, stream);
+        default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace mx4
+}  // namespace lidx

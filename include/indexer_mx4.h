@@ -18,7 +18,11 @@
  *   data   [n_blocks][block_size][n_heads][head_dim / 2]
  *   scale  [n_blocks][block_size][n_heads][head_dim / 32]
  * with any block, slot and head strides (so [block][head][slot] orders too);
- * a row's bytes are contiguous.  A slot is block * block_size + offset.
+ * a row's bytes are contiguous.  A slot is block * block_size + offset.  Data
+ * pointers and strides are multiples of 16 bytes, and every stride is at least
+ * a row; block_size and slot strides are below 2^24, block strides and a
+ * block's extent below 2^32 (else INDEXER_ENOTSUP).  The cache as a whole may
+ * be of any size.
  * Each 32 consecutive values of a row share a scale byte s, a factor
  * 2^(s - 127) (255: the 32 values are NaN), and hold 4 bits each: a sign and
  * a magnitude out of 0, .5, 1, 1.5, 2, 3, 4, 6 in code order; the even

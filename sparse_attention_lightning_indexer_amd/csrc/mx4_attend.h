@@ -27,8 +27,8 @@
 //    banks twice, the least 512 bytes can take.
 //  - Key (l >> 4) + 4 i + 16 u stands in row 4 (l >> 4) + i of score tile u, so
 //    one transposed read takes 16 consecutive LDS rows.
-//  - Loads run ahead: a tile's codes while the one before computes, its page
-//    ids one further, the selected indices one more.
+//  - Loads run ahead: a tile's codes from when the one before is converted,
+//    its page ids one tile further, the selected indices one more.
 //
 // Masked positions: their scores become -inf by selection, so K's NaN there
 // never spreads; V's blocks of NaN are replaced by zeros in the product, and
@@ -140,12 +140,17 @@ __device__ __forceinline__ Item item_of(const Mx4Attend &a, int mt) {
     return it;
 }
 
-template <bool BF16, int D, int MT, bool SELECTED>
-__global__ void __launch_bounds__(Shape<D>::WAVES * 64) mx4_attend_kernel(Mx4Attend a) {
+// What a row attends to: a window (or everything), selected keys, selected
+// runs of `pool` keys.
+enum Mode { kWindow = 0, kKeys = 1, kPools = 2 };
+
+template <bool BF16, int D, int MT, int MODE>
+__global__ void __launch_bounds__(Shape<D>::WAVES * 64, (MT == 1 && D <= 128 ? 4 : (MT == 2 && D == 256 ? 1 : 2))) mx4_attend_kernel(Mx4Attend a) {
     using T = Type<BF16>;
     using S = Shape<D>;
     typedef typename T::vec8 vec8;
     constexpr int KS = S::KS, NT = S::NT, W = S::WAVES;
+    constexpr bool SELECTED = MODE != kWindow;
     __shared__ __attribute__((aligned(16))) unsigned char smem[S::LDS];
 
     const Item it = item_of(a, MT);
@@ -212,36 +217,38 @@ __global__ void __launch_bounds__(Shape<D>::WAVES * 64) mx4_attend_kernel(Mx4Att
 
     // this lane's two keys of a tile: rows col of score tiles 0 and 1
     const int key0 = (col >> 2) + 4 * (col & 3);
-    const int64_t head_d = (int64_t)it.kv * a.pages.d_sh + qd * (KS * 4);
-    const int64_t head_s = (int64_t)it.kv * a.pages.s_sh;
+    const uint32_t head_d = (uint32_t)it.kv * (uint32_t)a.pages.d_sh + qd * (KS * 4);
+    const uint32_t head_s = (uint32_t)it.kv * (uint32_t)a.pages.s_sh + qd * KS / 4;
     const int32_t *table = a.block_table + (int64_t)req * a.bt_stride;
     const int32_t *sel = SELECTED ? a.idx + (int64_t)it.unit * a.idx_st : nullptr;
-    const int n_entries = SELECTED ? a.n_sel * a.pool : 0;
+    const uint32_t end_entry = SELECTED ? (uint32_t)min(a.n_sel * a.pool, t_end * 32) : 0u;
+    const uint32_t end_unit = MODE == kPools ? (uint32_t)(cap_last + a.pool - 1) / (uint32_t)a.pool : 0u;
 
-    // stage 1: the entry's selected index
+    // The three steps from a tile to its codes.  Each loads from a place that
+    // exists whatever the lane's key (a clamped entry, page 0 of the table,
+    // slot 0 of the cache), so none branches and the loads of a step overlap;
+    // `pos` = -1 and Raw::ok say what counts.
+    // 1: the entry's selected index
     auto load_index = [&](int tile, int u) -> int {
-        const int e = tile * 32 + u * 16 + key0;
-        if (tile >= t_end || e >= n_entries) return -1;
-        return sel[a.pool == 1 ? e : (int)quotient((uint32_t)e, a.div_pool)];
+        const uint32_t e = (uint32_t)(tile * 32 + u * 16 + key0);
+        return sel[min(MODE == kPools ? quotient(e, a.div_pool) : e, (uint32_t)a.n_sel - 1u)];
     };
-    // stage 2: the position (-1: none), and its page's id
+    // 2: the position (-1: none), and its page's id
     auto position = [&](int tile, int u, int id) -> int {
-        if (tile >= t_end) return -1;
-        if (SELECTED) {
-            if (id < 0) return -1;
-            if (a.pool == 1) return id < cap_last ? id : -1;
-            const int e = tile * 32 + u * 16 + key0;
-            const int64_t p = (int64_t)id * a.pool + (e - (int)quotient((uint32_t)e, a.div_pool) * a.pool);
-            return p < cap_last ? (int)p : -1;
+        const uint32_t e = (uint32_t)(tile * 32 + u * 16 + key0);
+        if (MODE == kKeys) return e < end_entry && (uint32_t)id < (uint32_t)cap_last ? id : -1;
+        if (MODE == kPools) {
+            const uint32_t p = (uint32_t)id * (uint32_t)a.pool + (e - quotient(e, a.div_pool) * (uint32_t)a.pool);
+            return e < end_entry && (uint32_t)id < end_unit && p < (uint32_t)cap_last ? (int)p : -1;
         }
         const int p = (tile < sink_tiles ? tile * 32 : base + (tile - sink_tiles) * 32) + u * 16 + key0;
-        return p < cap_last ? p : -1;
+        return tile < t_end && p < cap_last ? p : -1;
     };
-    auto load_page = [&](int p) -> int {
-        return p < 0 ? -1 : table[quotient((uint32_t)p, a.pages.div_bs)];
-    };
-    // a lane's KS words (8 values each) lie in blocks (qd * KS + s) / 4: at most NB
+    auto load_page = [&](int p) -> int { return table[quotient((uint32_t)max(p, 0), a.pages.div_bs)]; };
+    // 3: the codes and scales.  A lane's KS words (8 values each) lie in blocks
+    // (qd * KS + s) / 4: at most NB of them
     constexpr int NB = KS % 4 == 0 ? KS / 4 : (KS == 2 ? 1 : 2);
+    constexpr int ALIGN = KS % 4 == 0 ? 16 : (KS % 2 == 0 ? 8 : 4);
     struct Raw {
         uint32_t k[KS], v[KS];
         uint32_t sk[NB], sv[NB];
@@ -251,19 +258,19 @@ __global__ void __launch_bounds__(Shape<D>::WAVES * 64) mx4_attend_kernel(Mx4Att
     auto load_rows = [&](int p, int page) {
         Raw r;
         r.ok = p >= 0 && (uint32_t)page < (uint32_t)a.pages.n_blocks;
-        const int64_t pg = r.ok ? page : 0;
-        const int64_t off = r.ok ? p - (int)quotient((uint32_t)p, a.pages.div_bs) * a.pages.block_size : 0;
-        const int64_t at = pg * a.pages.d_sb + off * a.pages.d_ss + head_d;
-        const uint32_t *kd = reinterpret_cast<const uint32_t *>(a.kd + at);
-        const uint32_t *vd = reinterpret_cast<const uint32_t *>(a.vd + at);
-        __builtin_memcpy(r.k, __builtin_assume_aligned(kd, KS % 4 == 0 ? 16 : (KS % 2 == 0 ? 8 : 4)), KS * 4);
-        __builtin_memcpy(r.v, __builtin_assume_aligned(vd, KS % 4 == 0 ? 16 : (KS % 2 == 0 ? 8 : 4)), KS * 4);
-        const int64_t sat = pg * a.pages.s_sb + off * a.pages.s_ss + head_s;
+        const uint32_t q = (uint32_t)max(p, 0);
+        const uint32_t off = r.ok ? q - __umul24(quotient(q, a.pages.div_bs), (uint32_t)a.pages.block_size) : 0u;
+        const uint32_t pg = r.ok ? (uint32_t)page : 0u;
+        const uint64_t at = (uint64_t)pg * (uint32_t)a.pages.d_sb + (__umul24(off, (uint32_t)a.pages.d_ss) + head_d);
+        __builtin_memcpy(r.k, __builtin_assume_aligned(a.kd + at, ALIGN), KS * 4);
+        __builtin_memcpy(r.v, __builtin_assume_aligned(a.vd + at, ALIGN), KS * 4);
+        const uint64_t sat = (uint64_t)pg * (uint32_t)a.pages.s_sb + (__umul24(off, (uint32_t)a.pages.s_ss) + head_s);
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-            const int blk = min(blk0 + b, D / 32 - 1);
-            r.sk[b] = a.ks[sat + blk];
-            r.sv[b] = a.vs[sat + blk];
+            // the last block of a row again where the lane has fewer than NB
+            const uint32_t more = NB * 4 == KS || NB == 1 ? (uint32_t)b : (uint32_t)(min(blk0 + b, D / 32 - 1) - blk0);
+            r.sk[b] = a.ks[sat + more];
+            r.sv[b] = a.vs[sat + more];
         }
         return r;
     };
@@ -275,8 +282,7 @@ __global__ void __launch_bounds__(Shape<D>::WAVES * 64) mx4_attend_kernel(Mx4Att
     lds_u8 *stage = (lds_u8 *)smem + wave * (32 * S::ROW);
 
     int id[2] = {-1, -1}, pos[2], page[2];
-    Raw raw[2], nxt[2];
-    int npos[2];
+    Raw raw[2];
     if (t_begin < t_end) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
@@ -285,23 +291,13 @@ __global__ void __launch_bounds__(Shape<D>::WAVES * 64) mx4_attend_kernel(Mx4Att
             page[u] = load_page(pos[u]);
             raw[u] = load_rows(pos[u], page[u]);
             if (SELECTED) id[u] = load_index(t_begin + W, u);
-            npos[u] = position(t_begin + W, u, id[u]);
-            page[u] = load_page(npos[u]);
+            pos[u] = position(t_begin + W, u, id[u]);
+            page[u] = load_page(pos[u]);
             if (SELECTED) id[u] = load_index(t_begin + 2 * W, u);
         }
     }
 
     for (int tile = t_begin; tile < t_end; tile += W) {
-        // loads for the tiles ahead
-        int after[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            nxt[u] = load_rows(npos[u], page[u]);
-            after[u] = position(tile + 2 * W, u, id[u]);
-            page[u] = load_page(after[u]);
-            if (SELECTED) id[u] = load_index(tile + 3 * W, u);
-        }
-
         // scores
         f32x4 s[MT][2];
 #pragma unroll
@@ -395,6 +391,16 @@ __global__ void __launch_bounds__(Shape<D>::WAVES * 64) mx4_attend_kernel(Mx4Att
                 }
         }
 
+        // the next tile's codes, into the registers this one's came from; the
+        // page ids of the one after, and the indices of the one after that
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            raw[u] = load_rows(pos[u], page[u]);
+            pos[u] = position(tile + 2 * W, u, id[u]);
+            page[u] = load_page(pos[u]);
+            if (SELECTED) id[u] = load_index(tile + 3 * W, u);
+        }
+
         // softmax: the maximum over the tile, the sum of this lane's part
         vec8 p[MT];
 #pragma unroll
@@ -437,11 +443,6 @@ __global__ void __launch_bounds__(Shape<D>::WAVES * 64) mx4_attend_kernel(Mx4Att
             vt.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(src + 16 * S::ROW));
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) o[mt][n] = T::mfma(vt.v, p[mt], o[mt][n]);
-        }
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            raw[u] = nxt[u];
-            npos[u] = after[u];
         }
     }
 
@@ -544,10 +545,12 @@ __global__ void __launch_bounds__(256) mx4_join_kernel(Mx4Attend a) {
 template <bool BF16, int D, int MT>
 hipError_t launch_tiles(const Mx4Attend &a, const Mx4Plan &p, hipStream_t stream) {
     const dim3 grid((unsigned)p.workgroups), block(Shape<D>::WAVES * 64);
-    if (a.idx)
-        hipLaunchKernelGGL((mx4_attend_kernel<BF16, D, MT, true>), grid, block, 0, stream, a);
+    if (!a.idx)
+        hipLaunchKernelGGL((mx4_attend_kernel<BF16, D, MT, kWindow>), grid, block, 0, stream, a);
+    else if (a.pool == 1)
+        hipLaunchKernelGGL((mx4_attend_kernel<BF16, D, MT, kKeys>), grid, block, 0, stream, a);
     else
-        hipLaunchKernelGGL((mx4_attend_kernel<BF16, D, MT, false>), grid, block, 0, stream, a);
+        hipLaunchKernelGGL((mx4_attend_kernel<BF16, D, MT, kPools>), grid, block, 0, stream, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.n_splits == 1) return e;
     const int64_t threads = (int64_t)a.rows * a.n_heads * (D / 8);

@@ -54,6 +54,12 @@ PAGE_REFUSALS = [
     (dict(dsb=-1024), li.EINVAL, b"data strides"),
     (dict(ssh=3), li.EINVAL, b"scale strides"),
     (dict(sss=0), li.EINVAL, b"scale strides"),
+    (dict(bs=1 << 24), li.ENOTSUP, b"pages not supported"),
+    (dict(dss=1 << 24), li.ENOTSUP, b"pages not supported"),
+    (dict(sss=1 << 24), li.ENOTSUP, b"pages not supported"),
+    (dict(dsh=1 << 30), li.ENOTSUP, b"pages not supported"),
+    (dict(dsb=1 << 32), li.ENOTSUP, b"pages not supported"),
+    (dict(ssb=1 << 32), li.ENOTSUP, b"pages not supported"),
 ]
 
 

@@ -23,10 +23,8 @@
 //    neither do m, l and the rescaling of O^T = V^T P^T.
 //  - V's rows are converted like K's, stored to the wave's own LDS rows and
 //    read back transposed (ds_read_b64_tr_b16), 16 dimensions by 4 keys each.
-//    Rows are padded by 32 bytes: the 16 rows one read touches then cover all
-//    banks twice, the least 512 bytes can take.
-//  - Key (l >> 4) + 4 i + 16 u stands in row 4 (l >> 4) + i of score tile u, so
-//    one transposed read takes 16 consecutive LDS rows.
+//    Rows are padded by 32 bytes: the 8 consecutive rows that half a wave reads
+//    32 bytes of, or writes 16 bytes of, then lie in different banks.
 //  - Loads run ahead: a tile's codes from when the one before is converted,
 //    its page ids one tile further, the selected indices one more.
 //
@@ -215,8 +213,8 @@ __global__ void __launch_bounds__(Shape<D>::WAVES * 64, (MT == 1 && D <= 128 ? 4
         for (int n = 0; n < NT; ++n) o[mt][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
 
-    // this lane's two keys of a tile: rows col of score tiles 0 and 1
-    const int key0 = (col >> 2) + 4 * (col & 3);
+    // this lane's two keys of a tile: rows col of score tiles 0 and 1, keys col
+    // and 16 + col
     const uint32_t head_d = (uint32_t)it.kv * (uint32_t)a.pages.d_sh + qd * (KS * 4);
     const uint32_t head_s = (uint32_t)it.kv * (uint32_t)a.pages.s_sh + qd * KS / 4;
     const int32_t *table = a.block_table + (int64_t)req * a.bt_stride;
@@ -230,18 +228,18 @@ __global__ void __launch_bounds__(Shape<D>::WAVES * 64, (MT == 1 && D <= 128 ? 4
     // `pos` = -1 and Raw::ok say what counts.
     // 1: the entry's selected index
     auto load_index = [&](int tile, int u) -> int {
-        const uint32_t e = (uint32_t)(tile * 32 + u * 16 + key0);
+        const uint32_t e = (uint32_t)(tile * 32 + u * 16 + col);
         return sel[min(MODE == kPools ? quotient(e, a.div_pool) : e, (uint32_t)a.n_sel - 1u)];
     };
     // 2: the position (-1: none), and its page's id
     auto position = [&](int tile, int u, int id) -> int {
-        const uint32_t e = (uint32_t)(tile * 32 + u * 16 + key0);
+        const uint32_t e = (uint32_t)(tile * 32 + u * 16 + col);
         if (MODE == kKeys) return e < end_entry && (uint32_t)id < (uint32_t)cap_last ? id : -1;
         if (MODE == kPools) {
             const uint32_t p = (uint32_t)id * (uint32_t)a.pool + (e - quotient(e, a.div_pool) * (uint32_t)a.pool);
             return e < end_entry && (uint32_t)id < end_unit && p < (uint32_t)cap_last ? (int)p : -1;
         }
-        const int p = (tile < sink_tiles ? tile * 32 : base + (tile - sink_tiles) * 32) + u * 16 + key0;
+        const int p = (tile < sink_tiles ? tile * 32 : base + (tile - sink_tiles) * 32) + u * 16 + col;
         return tile < t_end && p < cap_last ? p : -1;
     };
     auto load_page = [&](int p) -> int { return table[quotient((uint32_t)max(p, 0), a.pages.div_bs)]; };
@@ -335,7 +333,7 @@ __global__ void __launch_bounds__(Shape<D>::WAVES * 64, (MT == 1 && D <= 128 ? 4
 #pragma unroll
                 for (int b = 1; b < NB; ++b) sb = block_of(st) == b ? sv[b] : sb;
                 const vec8 vv = T::from4(raw[u].v[st], __builtin_bit_cast(float, sb << 23));
-                *(lds_u32x4 *)(stage + (u * 16 + key0) * S::ROW + (qd * KS + st) * 16) = __builtin_bit_cast(u32x4, vv);
+                *(lds_u32x4 *)(stage + (u * 16 + col) * S::ROW + (qd * KS + st) * 16) = __builtin_bit_cast(u32x4, vv);
             }
         }
 
@@ -349,7 +347,7 @@ __global__ void __launch_bounds__(Shape<D>::WAVES * 64, (MT == 1 && D <= 128 ? 4
         auto counts = [&](int mt, int u, int i) -> bool {
             bool in = (valid[u] >> (4 * qd + i)) & 1ull;
             if (!SELECTED) {
-                const int p = p0 + u * 16 + 4 * i + qd;
+                const int p = p0 + u * 16 + 4 * qd + i;
                 in = in && p < row_end[mt] && (p >= row_start[mt] || p < a.sinks);
             }
             return in;
@@ -383,7 +381,7 @@ __global__ void __launch_bounds__(Shape<D>::WAVES * 64, (MT == 1 && D <= 128 ? 4
                     for (int mt = 0; mt < MT; ++mt) {
                         bool in = (valid[u] >> kk) & 1ull;
                         if (!SELECTED) {
-                            const int p = p0 + u * 16 + 4 * (kk & 3) + (kk >> 2);
+                            const int p = p0 + u * 16 + kk;
                             in = in && p < row_end[mt] && (p >= row_start[mt] || p < a.sinks);
                         }
                         if (in) nan_blocks[mt] |= blocks;
@@ -434,7 +432,7 @@ __global__ void __launch_bounds__(Shape<D>::WAVES * 64, (MT == 1 && D <= 128 ? 4
         // O^T += V^T P^T
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            lds_u8 *src = stage + (4 * (col >> 2) + qd) * S::ROW + n * 32 + (col & 3) * 8;
+            lds_u8 *src = stage + (4 * qd + (col >> 2)) * S::ROW + n * 32 + (col & 3) * 8;
             union {
                 s16x4 h[2];
                 vec8 v;

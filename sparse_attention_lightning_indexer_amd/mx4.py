@@ -28,14 +28,15 @@ MX4_EXPORTS = (
 MX4_F16, MX4_BF16 = 0, 1
 MAX_KEYS = 2**31 - 1024
 
-_ready = None
+_lib = None        # the library with these entry points' signatures declared
+_torch = None
+_types = {}        # torch dtype -> the library's type code
 
 
 def _library():
-    """The library with these entry points' signatures declared."""
-    global _ready
+    global _lib, _torch
     lib = _pkg.load_library()
-    if _ready is lib:
+    if _lib is lib:
         return lib
     p, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
     pages = [i32, i32] + [i64] * 6
@@ -50,76 +51,93 @@ def _library():
         f.restype = ctypes.c_int
     lib.indexer_mx4_attend_workspace_bytes.argtypes = [i32] * 7
     lib.indexer_mx4_attend_workspace_bytes.restype = sz
-    _ready = lib
+    if _torch is None:
+        _torch = _pkg._torch()
+        _types.update({_torch.float16: MX4_F16, _torch.bfloat16: MX4_BF16})
+    _lib = lib
     return lib
 
 
+# These calls are short, so the checks are: one test of everything that is
+# usually right, and the framework's own check, which names what is not.
+
+def _need(t, name, dtype, dev, dims):
+    if not (isinstance(t, _torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.dim() == dims):
+        _pkg._need(t, name, dtype, _torch.device("cuda", dev), dims)
+
+
+def _gpu(t, name):
+    """The index of the tensor's GPU."""
+    if not isinstance(t, _torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    return t.get_device()
+
+
 def _type_of(dtype) -> int:
-    torch = _pkg._torch()
-    if dtype == torch.float16:
-        return MX4_F16
-    if dtype == torch.bfloat16:
-        return MX4_BF16
-    raise TypeError(f"the 4-bit cache takes torch.float16 or torch.bfloat16, got {dtype}")
+    kind = _types.get(dtype)
+    if kind is None:
+        raise TypeError(f"the 4-bit cache takes torch.float16 or torch.bfloat16, got {dtype}")
+    return kind
 
 
-def _rows(t, name, dtype, device, shape=None):
-    """Rows [n, heads, d] with d contiguous."""
-    _pkg._need(t, name, dtype, device, 3)
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if t.shape[2] > 1 and t.stride(2) != 1:
+def _rows(t, name, dtype, dev, shape=None):
+    """Checks rows [n, heads, d] with d contiguous; their row and head strides
+    (a dimension of one entry has whatever stride is natural)."""
+    _need(t, name, dtype, dev, 3)
+    n, heads, d = t.shape
+    if shape is not None and (n, heads, d) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {[n, heads, d]}")
+    st, sh, sd = t.stride()
+    if sd != 1 and d > 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
+    if heads <= 1:
+        sh = d
+    return (st if n > 1 else heads * max(sh, d)), sh
 
 
-def _stride(t, dim, natural):
-    """A dimension's stride in elements; that of one entry says nothing."""
-    return t.stride(dim) if t.shape[dim] > 1 else natural
-
-
-def _row_strides(t):
-    """Row and head strides of [n, heads, d] rows."""
-    sh = _stride(t, 1, t.shape[2])
-    return _stride(t, 0, t.shape[1] * max(sh, t.shape[2])), sh
-
-
-def _cache(data, scale, name, device, heads, d):
+def _cache(data, scale, name, dev, heads, d):
     """Checks one cache; its (n_blocks, block_size, strides in bytes)."""
-    torch = _pkg._torch()
-    _pkg._need(data, f"{name}_data", torch.uint8, device, 4)
-    _pkg._need(scale, f"{name}_scale", torch.uint8, device, 4)
-    blocks, size = data.shape[0], data.shape[1]
-    if d % 32 or tuple(data.shape[2:]) != (heads, d // 2):
+    uint8 = _torch.uint8
+    _need(data, f"{name}_data", uint8, dev, 4)
+    _need(scale, f"{name}_scale", uint8, dev, 4)
+    blocks, size, h, w = data.shape
+    if d % 32 or h != heads or 2 * w != d:
         raise ValueError(f"{name}_data must be [n_blocks, block_size, {heads}, {d}/2] (head_dim a multiple of 32), got "
                          f"{list(data.shape)}")
-    if tuple(scale.shape) != (blocks, size, heads, d // 32):
+    if scale.shape != (blocks, size, heads, d // 32):
         raise ValueError(f"{name}_scale must be {[blocks, size, heads, d // 32]}, got {list(scale.shape)}")
-    if data.stride(3) != 1 or (scale.stride(3) != 1 and d > 32):
+    db, ds, dh, one = data.stride()
+    sb, ss, sh, sone = scale.stride()
+    if one != 1 or (sone != 1 and d > 32):
         raise ValueError(f"{name}_data's and {name}_scale's last dimension must be contiguous")
-    return (blocks, size) + tuple(_stride(t, i, t.shape[3]) for t in (data, scale) for i in range(3))
+    # a dimension of one entry: its stride says nothing
+    if heads == 1:
+        dh, sh = w, d // 32
+    if size <= 1:
+        ds, ss = w, d // 32
+    if blocks <= 1:
+        db, sb = w, d // 32
+    return blocks, size, db, ds, dh, sb, ss, sh
 
 
-def _slots(slots, n, device):
-    _pkg._need(slots, "slots", _pkg._torch().int64, device, 1)
+def _slots(slots, n, dev):
+    _need(slots, "slots", _torch.int64, dev, 1)
     if slots.shape[0] != n:
         raise ValueError(f"slots must have one entry per row ({n}), got {slots.shape[0]}")
     if n > 1 and slots.stride(0) != 1:
         raise ValueError("slots must be contiguous")
 
 
-def _on(device):
-    """Makes the tensors' device current for a launch, where it is not."""
-    torch = _pkg._torch()
-    return torch.cuda.device(device)
-
-
-def _call(device, status_of):
-    torch = _pkg._torch()
-    if device.index is None or device.index == torch.cuda.current_device():
-        _pkg._check(status_of())
+def _call(dev, entry, *args):
+    """Calls the library on torch's current stream of the tensors' device,
+    with that device current."""
+    if dev == _torch._C._cuda_getDevice():
+        status = entry(*args, _torch._C._cuda_getCurrentRawStream(dev))
     else:
-        with _on(device):
-            _pkg._check(status_of())
+        with _torch.cuda.device(dev):
+            status = entry(*args, _torch._C._cuda_getCurrentRawStream(dev))
+    if status:
+        _pkg._check(status)
 
 
 def mx4_cache_write(k, slots, k_data, k_scale, v=None, v_data=None, v_scale=None) -> None:
@@ -128,27 +146,24 @@ def mx4_cache_write(k, slots, k_data, k_scale, v=None, v_data=None, v_scale=None
     negative slot or one past the cache is skipped.  Slots that are not skipped
     must be distinct.  Every other slot keeps its bytes."""
     lib = _library()
-    torch = _pkg._torch()
-    if not isinstance(k, torch.Tensor) or not k.is_cuda:
-        raise ValueError("k must be a GPU tensor")
-    dev = k.device
+    dev = _gpu(k, "k")
     kind = _type_of(k.dtype)
-    _rows(k, "k", k.dtype, dev)
-    n, heads, d = k.shape
+    k_strides = _rows(k, "k", k.dtype, dev)
+    n, heads, d = shape = tuple(k.shape)
     pages = _cache(k_data, k_scale, "k", dev, heads, d)
     _slots(slots, n, dev)
-    if (v is None) != (v_data is None) or (v is None) != (v_scale is None):
-        raise ValueError("v, v_data and v_scale come together")
-    if v is not None:
-        _rows(v, "v", k.dtype, dev, k.shape)
+    v_args, v_strides = (None, None), (0, 0)
+    if v is not None and v_data is not None and v_scale is not None:
+        v_strides = _rows(v, "v", k.dtype, dev, shape)
         if _cache(v_data, v_scale, "v", dev, heads, d) != pages:
             raise ValueError("the K and V caches must have the same shape and strides")
+        v_args = (v_data.data_ptr(), v_scale.data_ptr())
+    elif v is not None or v_data is not None or v_scale is not None:
+        raise ValueError("v, v_data and v_scale come together")
     if n == 0 or pages[0] == 0:  # nothing to write, or nowhere (and empty tensors have no address)
         return
-    ptr = _pkg._ptr
-    _call(dev, lambda: lib.indexer_mx4_cache_write(
-        ptr(k), *_row_strides(k), ptr(v), *(_row_strides(v) if v is not None else (0, 0)), kind, n, heads, d, ptr(slots), ptr(k_data), ptr(k_scale), ptr(v_data),
-        ptr(v_scale), *pages, _pkg._stream(dev)))
+    _call(dev, lib.indexer_mx4_cache_write, k.data_ptr(), *k_strides, None if v is None else v.data_ptr(), *v_strides,
+          kind, n, heads, d, slots.data_ptr(), k_data.data_ptr(), k_scale.data_ptr(), *v_args, *pages)
 
 
 def mx4_cache_read(data, scale, slots, dtype=None, out=None):
@@ -156,32 +171,27 @@ def mx4_cache_read(data, scale, slots, dtype=None, out=None):
     (float16 unless given, or out's), row i from slot slots[i] (zeros where
     that is negative or past the cache; a slot may come again)."""
     lib = _library()
-    torch = _pkg._torch()
-    if not isinstance(data, torch.Tensor) or not data.is_cuda:
-        raise ValueError("data must be a GPU tensor")
-    dev = data.device
+    dev = _gpu(data, "data")
     if data.dim() != 4:
         raise ValueError(f"data must have 4 dims, got {data.dim()}")
     heads, d = data.shape[2], 2 * data.shape[3]
     if dtype is None:
-        dtype = torch.float16 if out is None else out.dtype
+        dtype = _torch.float16 if out is None else out.dtype
     kind = _type_of(dtype)
     pages = _cache(data, scale, "k", dev, heads, d)
-    if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
+    if not isinstance(slots, _torch.Tensor) or slots.dim() != 1:
         raise ValueError("slots must be a vector of slots")
     n = slots.shape[0]
     _slots(slots, n, dev)
     if out is None:
-        out = torch.empty((n, heads, d), dtype=dtype, device=dev)
-    _rows(out, "out", dtype, dev, (n, heads, d))
-    if out.numel() == 0:
+        out = _torch.empty((n, heads, d), dtype=dtype, device=data.device)
+    strides = _rows(out, "out", dtype, dev, (n, heads, d))
+    if n == 0 or heads == 0 or d == 0:
         return out
     if pages[0] == 0:  # an empty cache has no slot, and no address
         return out.zero_()
-    ptr = _pkg._ptr
-    _call(dev, lambda: lib.indexer_mx4_cache_read(
-        ptr(data), ptr(scale), *pages, ptr(slots), n, heads, d, ptr(out), *_row_strides(out), kind,
-        _pkg._stream(dev)))
+    _call(dev, lib.indexer_mx4_cache_read, data.data_ptr(), scale.data_ptr(), *pages, slots.data_ptr(), n, heads, d,
+          out.data_ptr(), *strides, kind)
     return out
 
 
@@ -194,56 +204,58 @@ def mx4_attend_workspace_bytes(n_requests: int, query_len: int, max_keys: int, s
 
 def _attend(entry, q, k_data, k_scale, v_data, v_scale, block_table, seq_lens, query_len, max_seq_len, sm_scale,
             selected, max_keys, form, out, lse, with_lse, workspace):
-    torch = _pkg._torch()
-    lib = _library()
-    if not isinstance(q, torch.Tensor) or not q.is_cuda:
-        raise ValueError("q must be a GPU tensor")
-    dev = q.device
-    kind = _type_of(q.dtype)
-    _rows(q, "q", q.dtype, dev)
-    rows, heads, d = q.shape
+    torch = _torch
+    dev = _gpu(q, "q")
+    dtype = q.dtype
+    kind = _type_of(dtype)
+    q_strides = _rows(q, "q", dtype, dev)
+    rows, heads, d = shape = tuple(q.shape)
     if not isinstance(k_data, torch.Tensor) or k_data.dim() != 4:
         raise ValueError("k_data must be [n_blocks, block_size, n_kv_heads, head_dim/2]")
     kv = k_data.shape[2]
     pages = _cache(k_data, k_scale, "k", dev, kv, d)
     if _cache(v_data, v_scale, "v", dev, kv, d) != pages:
         raise ValueError("the K and V caches must have the same shape and strides")
-    _pkg._need(block_table, "block_table", torch.int32, dev, 2)
-    _pkg._need(seq_lens, "seq_lens", torch.int32, dev, 1)
+    _need(block_table, "block_table", torch.int32, dev, 2)
+    _need(seq_lens, "seq_lens", torch.int32, dev, 1)
     requests = seq_lens.shape[0]
     if requests > 1 and seq_lens.stride(0) != 1:
         raise ValueError("seq_lens must be contiguous")
-    if block_table.shape[1] > 1 and block_table.stride(1) != 1:
+    bt_rows, bt_cols = block_table.shape
+    bt_stride, bt_one = block_table.stride()
+    if bt_cols > 1 and bt_one != 1:
         raise ValueError("block_table rows must be contiguous")
-    if block_table.shape[0] < requests or block_table.shape[1] * pages[1] < max_seq_len:
+    if bt_rows < requests or bt_cols * pages[1] < max_seq_len:
         raise ValueError(f"block_table must be at least [n_requests, ceil(max_seq_len/block_size)] = [{requests}, "
-                         f"{-(-max_seq_len // max(pages[1], 1))}], got {list(block_table.shape)}")
+                         f"{-(-max_seq_len // max(pages[1], 1))}], got {[bt_rows, bt_cols]}")
     if rows != requests * query_len:
         raise ValueError(f"q has {rows} rows, expected n_requests*query_len = {requests * query_len}")
     if out is None:
-        out = torch.empty((rows, heads, d), dtype=q.dtype, device=dev)
-    _rows(out, "out", q.dtype, dev, q.shape)
-    if lse is None and with_lse:
-        lse = torch.empty((rows, heads), dtype=torch.float32, device=dev)
+        out = torch.empty(shape, dtype=dtype, device=q.device)
+        out_strides = (heads * d, d)
+    else:
+        out_strides = _rows(out, "out", dtype, dev, shape)
     if lse is not None:
-        _pkg._need(lse, "lse", torch.float32, dev, 2)
-        if tuple(lse.shape) != (rows, heads) or not lse.is_contiguous():
+        _need(lse, "lse", torch.float32, dev, 2)
+        if lse.shape != (rows, heads) or not lse.is_contiguous():
             raise ValueError(f"lse must be contiguous [{rows}, {heads}]")
-    if rows == 0:  # nothing to compute
-        return out, lse
-    need = lib.indexer_mx4_attend_workspace_bytes(requests, query_len, max_keys, selected, heads, kv, d)
+    elif with_lse:
+        lse = torch.empty((rows, heads), dtype=torch.float32, device=q.device)
     if workspace is not None:
-        _pkg._need(workspace, "workspace", torch.uint8, dev, 1)
+        _need(workspace, "workspace", torch.uint8, dev, 1)
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
-    elif 0 < need < 2**63:  # sizes the library refuses have none: the call below names them
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    ptr = _pkg._ptr
-    _call(dev, lambda: getattr(lib, entry)(
-        ptr(q), *_row_strides(q), kind, ptr(k_data), ptr(k_scale), ptr(v_data), ptr(v_scale), *pages,
-        ptr(block_table), _stride(block_table, 0, block_table.shape[1]), ptr(seq_lens), requests, query_len, max_seq_len, heads, kv, d,
-        sm_scale, *form, ptr(out), *_row_strides(out), ptr(lse), ptr(workspace),
-        workspace.numel() if workspace is not None else 0, _pkg._stream(dev)))
+    if rows == 0:  # nothing to compute
+        return out, lse
+    if workspace is None:
+        need = _lib.indexer_mx4_attend_workspace_bytes(requests, query_len, max_keys, selected, heads, kv, d)
+        if 0 < need < 2**63:  # sizes the library refuses have none: the call below names them
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    _call(dev, entry, q.data_ptr(), *q_strides, kind, k_data.data_ptr(), k_scale.data_ptr(), v_data.data_ptr(),
+          v_scale.data_ptr(), *pages, block_table.data_ptr(), bt_stride if bt_rows > 1 else bt_cols,
+          seq_lens.data_ptr(), requests, query_len, max_seq_len, heads, kv, d, sm_scale, *form, out.data_ptr(),
+          *out_strides, None if lse is None else lse.data_ptr(), None if workspace is None else workspace.data_ptr(),
+          0 if workspace is None else workspace.numel())
     return out, lse
 
 
@@ -258,29 +270,30 @@ def mx4_attend_selected(q, k_data, k_scale, v_data, v_scale, block_table, seq_le
     cache's four tensors, block_table i32 [R, max_blocks], seq_lens i32 [R]
     -> (out like q, lse f32 [R*Q, n_heads] or None).  Keys past the block
     table's pages are not seen.  A row with no key has out 0 and lse -inf."""
-    torch = _pkg._torch()
-    if not isinstance(q, torch.Tensor) or not isinstance(idx, torch.Tensor):
-        raise TypeError("q and idx must be torch.Tensors")
-    _pkg._need(idx, "idx", torch.int32, q.device, 2)
-    if idx.shape[0] != q.shape[0]:
-        raise ValueError(f"idx must have one row per row of q ({q.shape[0]}), got {idx.shape[0]}")
-    if idx.shape[1] > 1 and idx.stride(1) != 1:
+    lib = _library()
+    if not isinstance(q, _torch.Tensor):
+        raise TypeError("q must be a torch.Tensor")
+    _need(idx, "idx", _torch.int32, _gpu(q, "q"), 2)
+    rows, n_sel = idx.shape
+    if rows != q.shape[0]:
+        raise ValueError(f"idx must have one row per row of q ({q.shape[0]}), got {rows}")
+    idx_stride, one = idx.stride()
+    if n_sel > 1 and one != 1:
         raise ValueError("idx rows must be contiguous")
-    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+    if not isinstance(block_table, _torch.Tensor) or block_table.dim() != 2:
         raise ValueError("block_table must be [n_requests, max_blocks]")
-    if not isinstance(k_data, torch.Tensor) or k_data.dim() != 4:
+    if not isinstance(k_data, _torch.Tensor) or k_data.dim() != 4:
         raise ValueError("k_data must be [n_blocks, block_size, n_kv_heads, head_dim/2]")
     if pool_size < 1:
         raise ValueError("pool_size must be >= 1")
-    max_seq_len = min(block_table.shape[1] * k_data.shape[1], MAX_KEYS)
-    n_sel = idx.shape[1]
-    # an empty selection has no address: one entry of -1 attends to as little
-    if n_sel == 0 and idx.shape[0] > 0:
-        idx = torch.full((idx.shape[0], 1), -1, dtype=torch.int32, device=q.device)
-        n_sel = 1
-    return _attend("indexer_mx4_attend_selected", q, k_data, k_scale, v_data, v_scale, block_table, seq_lens,
-                   query_len, max_seq_len, sm_scale, 1, min(n_sel * pool_size, 2**31 - 1),
-                   (_pkg._ptr(idx), _stride(idx, 0, n_sel), n_sel, pool_size), out, lse, with_lse, workspace)
+    if n_sel == 0 and rows > 0:  # an empty selection has no address: one entry of -1 attends to as little
+        idx = _torch.full((rows, 1), -1, dtype=_torch.int32, device=q.device)
+        n_sel = idx_stride = 1
+    return _attend(lib.indexer_mx4_attend_selected, q, k_data, k_scale, v_data, v_scale, block_table, seq_lens,
+                   query_len, min(block_table.shape[1] * k_data.shape[1], MAX_KEYS), sm_scale, 1,
+                   min(n_sel * pool_size, 2**31 - 1),
+                   (idx.data_ptr(), idx_stride if rows > 1 else n_sel, n_sel, pool_size), out, lse, with_lse,
+                   workspace)
 
 
 def mx4_attend_window(q, k_data, k_scale, v_data, v_scale, block_table, seq_lens, query_len: int, max_seq_len: int,
@@ -290,7 +303,8 @@ def mx4_attend_window(q, k_data, k_scale, v_data, v_scale, block_table, seq_lens
     `sinks` tokens (window 0: every key it sees): with v = seq_lens[r] - Q + 1
     + j, the keys s < min(v, max_seq_len) that have s >= v - window or
     s < sinks.  Other arguments and results as in mx4_attend_selected."""
+    lib = _library()
     keys = max_seq_len if window == 0 else min(max_seq_len, window + sinks)
-    return _attend("indexer_mx4_attend_window", q, k_data, k_scale, v_data, v_scale, block_table, seq_lens, query_len,
+    return _attend(lib.indexer_mx4_attend_window, q, k_data, k_scale, v_data, v_scale, block_table, seq_lens, query_len,
                    max_seq_len, sm_scale, 0, max(0, min(keys, 2**31 - 1)), (window, sinks), out, lse, with_lse,
                    workspace)

@@ -188,8 +188,13 @@ int64_t window_keys(int32_t max_seq_len, int32_t window, int32_t sinks) {
 namespace lidx {
 
 // A wave holds one tile of 16 query rows, or two where a unit has more rows.
-// Keys are shared among workgroups until there are about two per compute unit
-// (a workgroup's waves then still get a tile of 32 keys each).
+// Where there are fewer workgroups than compute units, several share a row's
+// keys, about one workgroup per compute unit: one row of 131072 keys on 8 K/V
+// heads takes 123, 67, 41 and 43 us with 8, 16, 32 and 64 shares (32 is one a
+// compute unit).  Joining the shares is a second launch, about 5 us, the time
+// of about 4 tiles of a wave; 32 rows of 512 keys on 8 heads, two tiles a
+// wave, take 9.3 us whole and 15.8 us in halves.  So keys are shared only
+// where that takes at least 4 tiles from every wave.
 Mx4Plan plan_mx4_attend(int n_requests, int q_len, int64_t max_keys, bool selected, int n_heads, int n_kv,
                         int head_dim) {
     Mx4Plan p{};
@@ -202,10 +207,12 @@ Mx4Plan plan_mx4_attend(int n_requests, int q_len, int64_t max_keys, bool select
     const int waves = head_dim <= 128 ? 8 : 4;
     const int64_t items = (int64_t)p.units * p.m_tiles * n_kv;
     const int64_t most = (max_keys + 32 * waves - 1) / (32 * waves);
-    int64_t splits = items > 0 ? 512 / items : 1;
+    int64_t splits = items > 0 ? 256 / items : 1;
     if (splits > most) splits = most;
-    if (splits > 64) splits = 64;
-    p.n_splits = splits < 1 ? 1 : (int)splits;
+    if (splits > kMx4MaxSplits) splits = kMx4MaxSplits;
+    // most: tiles of a wave that has a row's keys to itself
+    if (splits < 1 || most * (splits - 1) < 4 * splits) splits = 1;
+    p.n_splits = (int)splits;
     const int64_t pieces = (int64_t)p.units * p.m_tiles * p.n_splits;
     p.workgroups = (pieces + 7) / 8 * 8 * n_kv;
     if (p.n_splits > 1) {

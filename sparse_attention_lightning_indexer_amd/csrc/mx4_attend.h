@@ -505,39 +505,62 @@ __global__ void __launch_bounds__(Shape<D>::WAVES * 64, (MT == 1 && D <= 128 ? 4
     }
 }
 
-// Joins the shares of rows whose keys were split: one thread per 8 outputs.
+// Joins the shares of rows whose keys were split (at most kMx4MaxSplits): a workgroup per
+// query row and head.  Threads take 4 outputs of every 1024 / D-th share, so
+// the loads of a row's shares overlap, and add up through LDS.
 template <bool BF16, int D>
 __global__ void __launch_bounds__(256) mx4_join_kernel(Mx4Attend a) {
     using T = Type<BF16>;
     typedef typename T::vec8 vec8;
-    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t th = e / (D / 8);
-    const int c = (int)(e - th * (D / 8));
-    if (th >= (int64_t)a.rows * a.n_heads) return;
-    const float *ml = a.part_ml + th * a.n_splits * 2;
-    float m_all = kNegInf;
-    for (int s = 0; s < a.n_splits; ++s) m_all = fmaxf(m_all, ml[2 * s]);
-    const float sub = m_all == kNegInf ? 0.0f : m_all;
-    float l_all = 0.0f, acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    for (int s = 0; s < a.n_splits; ++s) {
-        const float f = __builtin_amdgcn_exp2f(ml[2 * s] - sub);
-        l_all += f * ml[2 * s + 1];
-        const f32x4 *src = reinterpret_cast<const f32x4 *>(a.part_o + (th * a.n_splits + s) * D + c * 8);
-        const f32x4 x = src[0], y = src[1];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            acc[i] += f * x[i];
-            acc[4 + i] += f * y[i];
+    constexpr int C = D / 4, G = 256 / C;  // chunks of 4 outputs, shares in flight
+    __shared__ float weight[kMx4MaxSplits], total[1];
+    static_assert(kMx4MaxSplits <= 64, "a lane per share");
+    __shared__ __attribute__((aligned(16))) float part[G][D];
+    const int64_t th = blockIdx.x;
+    const int c = threadIdx.x % C, g = threadIdx.x / C;
+    const float *po = a.part_o + th * a.n_splits * D + c * 4;
+    if (threadIdx.x < 64) {
+        const float *ml = a.part_ml + th * a.n_splits * 2;
+        const bool has = (int)threadIdx.x < a.n_splits;
+        const float m = has ? ml[2 * threadIdx.x] : kNegInf;
+        float l = has ? ml[2 * threadIdx.x + 1] : 0.0f;
+        float m_all = m;
+        for (int d = 32; d; d >>= 1) m_all = fmaxf(m_all, __shfl_xor(m_all, d));
+        const float f = __builtin_amdgcn_exp2f(m - (m_all == kNegInf ? 0.0f : m_all));
+        l *= f;
+        for (int d = 32; d; d >>= 1) l += __shfl_xor(l, d);
+        weight[threadIdx.x] = f;
+        if (threadIdx.x == 0) {
+            total[0] = l;
+            if (a.lse) a.lse[th] = l == 0.0f ? kNegInf : (m_all + log2f(l)) * 0.69314718055994530942f;
         }
+    }
+    __syncthreads();
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (g < G) {
+#pragma unroll 4
+        for (int s = g; s < a.n_splits; s += G) {
+            const f32x4 x = *reinterpret_cast<const f32x4 *>(po + (int64_t)s * D);
+            const float f = weight[s];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[i] += f * x[i];
+        }
+        *reinterpret_cast<f32x4 *>(&part[g][c * 4]) = acc;
+    }
+    __syncthreads();
+    if (threadIdx.x >= D / 8) return;
+    const float inv = total[0] == 0.0f ? 0.0f : 1.0f / total[0];
+    vec8 r;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float v = 0.0f;
+#pragma unroll
+        for (int k = 0; k < G; ++k) v += part[k][threadIdx.x * 8 + i];
+        r[i] = (typename T::one)(v * inv);
     }
     const int64_t token = th / a.n_heads;
     const int head = (int)(th - token * a.n_heads);
-    const float inv = l_all == 0.0f ? 0.0f : 1.0f / l_all;
-    vec8 r;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = (typename T::one)(acc[i] * inv);
-    *reinterpret_cast<vec8 *>((uint16_t *)a.out + token * a.out_st + (int64_t)head * a.out_sh + c * 8) = r;
-    if (c == 0 && a.lse) a.lse[th] = l_all == 0.0f ? kNegInf : (m_all + log2f(l_all)) * 0.69314718055994530942f;
+    *reinterpret_cast<vec8 *>((uint16_t *)a.out + token * a.out_st + (int64_t)head * a.out_sh + threadIdx.x * 8) = r;
 }
 
 template <bool BF16, int D, int MT>
@@ -551,8 +574,7 @@ hipError_t launch_tiles(const Mx4Attend &a, const Mx4Plan &p, hipStream_t stream
         hipLaunchKernelGGL((mx4_attend_kernel<BF16, D, MT, kPools>), grid, block, 0, stream, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.n_splits == 1) return e;
-    const int64_t threads = (int64_t)a.rows * a.n_heads * (D / 8);
-    hipLaunchKernelGGL((mx4_join_kernel<BF16, D>), dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((mx4_join_kernel<BF16, D>), dim3((unsigned)(a.rows * a.n_heads)), dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 

@@ -96,6 +96,8 @@ struct Mx4Attend {
     float *part_ml;     // [rows][n_heads][n_splits][2]
 };
 
+constexpr int kMx4MaxSplits = 64;
+
 // Launch geometry: how many 16-row tiles a wave holds and how many workgroups
 // share a row's keys; a function of sizes alone.
 struct Mx4Plan {

@@ -67,7 +67,7 @@ indexer_status check_pages(int32_t n_blocks, int32_t block_size, int32_t n_heads
     if (block_size == 1) d_ss = s_ss = 0;
     if (n_heads == 1) d_sh = s_sh = 0;
     *out = lidx::Mx4Pages{d_sb, d_ss, d_sh, s_sb, s_ss, s_sh, n_blocks, block_size,
-                          lidx::fast_div((uint32_t)block_size), (int64_t)n_blocks * block_size};
+                          lidx::fast_div((uint32_t)block_size), (int64_t)n_blocks * block_size, d_sb == 16 * s_sb && d_ss == 16 * s_ss};
     return INDEXER_OK;
 }
 

@@ -46,6 +46,7 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 template <bool BF16>
 struct Type;
@@ -83,6 +84,12 @@ struct Type<true> {
     }
 };
 
+// The larger of two numbers (a NaN is passed over): the middle of them and
+// infinity, one instruction where fmaxf takes three to quiet its operands.
+__device__ __forceinline__ float larger(float a, float b) {
+    return __builtin_amdgcn_fmed3f(a, b, __builtin_huge_valf());
+}
+
 // Over the four lanes that share l & 15.
 __device__ __forceinline__ float quarter_max(float v) {
     const unsigned u = __builtin_bit_cast(unsigned, v);
@@ -101,12 +108,43 @@ __device__ __forceinline__ float quarter_sum(float v) {
     return __builtin_bit_cast(float, (unsigned)b[0]) + __builtin_bit_cast(float, (unsigned)b[1]);
 }
 
+// N (1 to 4) consecutive words to and from LDS, 16-byte aligned.
+template <int N>
+__device__ __forceinline__ void put_words(lds_u8 *dst, const uint32_t (&w)[N]) {
+    typedef __attribute__((address_space(3))) u32x4 v4;
+    typedef __attribute__((address_space(3))) u32x2 v2;
+    typedef __attribute__((address_space(3))) uint32_t v1;
+    if constexpr (N == 4) {
+        *(v4 *)dst = u32x4{w[0], w[1], w[2], w[3]};
+    } else {
+        if constexpr (N >= 2) *(v2 *)dst = u32x2{w[0], w[1]};
+        if constexpr (N % 2 == 1) *(v1 *)(dst + (N - 1) * 4) = w[N - 1];
+    }
+}
+template <int N>
+__device__ __forceinline__ void get_words(const lds_u8 *src, uint32_t (&w)[N]) {
+    typedef const __attribute__((address_space(3))) u32x4 v4;
+    typedef const __attribute__((address_space(3))) u32x2 v2;
+    typedef const __attribute__((address_space(3))) uint32_t v1;
+    if constexpr (N == 4) {
+        const u32x4 v = *(v4 *)src;
+        w[0] = v[0], w[1] = v[1], w[2] = v[2], w[3] = v[3];
+    } else {
+        if constexpr (N >= 2) {
+            const u32x2 v = *(v2 *)src;
+            w[0] = v[0], w[1] = v[1];
+        }
+        if constexpr (N % 2 == 1) w[N - 1] = *(v1 *)(src + (N - 1) * 4);
+    }
+}
+
 constexpr float kNegInf = -__builtin_huge_valf();
 
 template <int D>
 struct Shape {
     static constexpr int KS = D / 32;               // MFMA steps over the head dimension
     static constexpr int NT = D / 16;               // 16-dimension tiles of the product
+    static constexpr int UNITS = D <= 128 ? 4 : 8;  // 16-byte units of a key's codes in LDS
     static constexpr int ROW = 2 * D + 32;          // bytes of a V row in LDS
     static constexpr int WAVES = D <= 128 ? 8 : 4;
     static constexpr int OROW = D + 4;              // floats of a row of the join (padded)
@@ -213,89 +251,207 @@ __global__ void __launch_bounds__(Shape<D>::WAVES * 64, (MT == 1 && D <= 128 ? 4
         for (int n = 0; n < NT; ++n) o[mt][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
 
-    // this lane's two keys of a tile: rows col of score tiles 0 and 1, keys col
-    // and 16 + col
-    const uint32_t head_d = (uint32_t)it.kv * (uint32_t)a.pages.d_sh + qd * (KS * 4);
-    const uint32_t head_s = (uint32_t)it.kv * (uint32_t)a.pages.s_sh + qd * KS / 4;
+    // A tile's 32 keys are the rows of score tiles 0 and 1 (keys `row` and 16 +
+    // row of the tile).  Four neighbouring lanes load a key's row, a quarter
+    // each, so that their 16-byte loads fall into one line; where the lanes of
+    // one row were 16 apart, as the products want them, a load instruction took
+    // four times the line lookups, which bounded the kernel.  Finding the rows
+    // is shared: of the 64 keys of two tiles (this one and the wave's next)
+    // each lane finds one, and the others ask it for the offset.
+    const int krow = lane >> 2, ch = lane & 3;
+    const uint64_t head_d = (uint64_t)((uint32_t)it.kv * (uint32_t)a.pages.d_sh);
+    const uint32_t head_s = (uint32_t)it.kv * (uint32_t)a.pages.s_sh;
+    const uint8_t *kd = a.kd + head_d, *vd = a.vd + head_d, *ks = a.ks + head_s, *vs = a.vs + head_s;
     const int32_t *table = a.block_table + (int64_t)req * a.bt_stride;
     const int32_t *sel = SELECTED ? a.idx + (int64_t)it.unit * a.idx_st : nullptr;
-    const uint32_t end_entry = SELECTED ? (uint32_t)min(a.n_sel * a.pool, t_end * 32) : 0u;
+    const uint32_t end_entry = SELECTED ? min((uint32_t)a.n_sel * (uint32_t)a.pool, (uint32_t)t_end * 32u) : 0u;
     const uint32_t end_unit = MODE == kPools ? (uint32_t)(cap_last + a.pool - 1) / (uint32_t)a.pool : 0u;
+    const uint32_t own_tile = (uint32_t)(qd >> 1) * W, own_key = (uint32_t)((qd & 1) * 16 + col);
 
-    // The three steps from a tile to its codes.  Each loads from a place that
-    // exists whatever the lane's key (a clamped entry, page 0 of the table,
-    // slot 0 of the cache), so none branches and the loads of a step overlap;
-    // `pos` = -1 and Raw::ok say what counts.
+    // The steps from a pair of tiles to its offsets.  Each loads from a place
+    // that exists whatever the lane's key (a clamped entry, page 0 of the table,
+    // slot 0 of the cache), so none branches and the loads of a step overlap; a
+    // position of -1 and the bits of `found` say what counts.
     // 1: the entry's selected index
-    auto load_index = [&](int tile, int u) -> int {
-        const uint32_t e = (uint32_t)(tile * 32 + u * 16 + col);
-        return sel[min(MODE == kPools ? quotient(e, a.div_pool) : e, (uint32_t)a.n_sel - 1u)];
+    auto load_index = [&](int tile) -> int {
+        const uint32_t e = ((uint32_t)tile + own_tile) * 32u + own_key;
+        return sel[min(MODE == kPools ? quotient(min(e, 0x7fffffffu), a.div_pool) : e, (uint32_t)a.n_sel - 1u)];
     };
-    // 2: the position (-1: none), and its page's id
-    auto position = [&](int tile, int u, int id) -> int {
-        const uint32_t e = (uint32_t)(tile * 32 + u * 16 + col);
+    // 2: the position
+    auto position = [&](int tile, int id) -> int {
+        const uint32_t mine = (uint32_t)tile + own_tile;
+        const uint32_t e = mine * 32u + own_key;
         if (MODE == kKeys) return e < end_entry && (uint32_t)id < (uint32_t)cap_last ? id : -1;
         if (MODE == kPools) {
-            const uint32_t p = (uint32_t)id * (uint32_t)a.pool + (e - quotient(e, a.div_pool) * (uint32_t)a.pool);
+            const uint32_t u = e - quotient(min(e, 0x7fffffffu), a.div_pool) * (uint32_t)a.pool;
+            const uint32_t p = (uint32_t)id * (uint32_t)a.pool + u;
             return e < end_entry && (uint32_t)id < end_unit && p < (uint32_t)cap_last ? (int)p : -1;
         }
-        const int p = (tile < sink_tiles ? tile * 32 : base + (tile - sink_tiles) * 32) + u * 16 + col;
-        return tile < t_end && p < cap_last ? p : -1;
+        const uint32_t p = (mine < (uint32_t)sink_tiles ? 0u : (uint32_t)(base - sink_tiles * 32)) + e;
+        return mine < (uint32_t)t_end && p < (uint32_t)cap_last ? (int)p : -1;
     };
+    // 3: its page's id
     auto load_page = [&](int p) -> int { return table[quotient((uint32_t)max(p, 0), a.pages.div_bs)]; };
-    // 3: the codes and scales.  A lane's KS words (8 values each) lie in blocks
-    // (qd * KS + s) / 4: at most NB of them
+    // 4: where its row begins, in data and (unless that is a sixteenth of it) scale bytes
+    uint64_t at = 0, sat = 0, found = 0;
+    auto locate = [&](int p, int page) {
+        const bool ok = p >= 0 && (uint32_t)page < (uint32_t)a.pages.n_blocks;
+        const uint32_t q = (uint32_t)max(p, 0);
+        const uint32_t off = q - __umul24(quotient(q, a.pages.div_bs), (uint32_t)a.pages.block_size);
+        const uint32_t o = ok ? off : 0u, pg = ok ? (uint32_t)page : 0u;
+        at = (uint64_t)pg * (uint32_t)a.pages.d_sb + __umul24(o, (uint32_t)a.pages.d_ss);
+        if (!a.pages.congruent) sat = (uint64_t)pg * (uint32_t)a.pages.s_sb + __umul24(o, (uint32_t)a.pages.s_ss);
+        found = __ballot(ok);
+    };
+    // from the lane that found row krow of score tile u of tile `b` of the pair
+    auto ask = [&](uint64_t v, int b, int u) -> uint64_t {
+        const int who = (b * 32 + u * 16 + krow) * 4;
+        const uint32_t lo = (uint32_t)__builtin_amdgcn_ds_bpermute(who, (int)(uint32_t)v);
+        const uint32_t hi = (uint32_t)__builtin_amdgcn_ds_bpermute(who, (int)(uint32_t)(v >> 32));
+        return ((uint64_t)hi << 32) | lo;
+    };
+    // 5: the codes and scales.  The KS words (8 values each) of quarter c lie in
+    // blocks (c * KS + s) / 4: at most NB of them
     constexpr int NB = KS % 4 == 0 ? KS / 4 : (KS == 2 ? 1 : 2);
     constexpr int ALIGN = KS % 4 == 0 ? 16 : (KS % 2 == 0 ? 8 : 4);
     struct Raw {
         uint32_t k[KS], v[KS];
         uint32_t sk[NB], sv[NB];
-        bool ok;
     };
-    const int blk0 = qd * KS / 4;
-    auto load_rows = [&](int p, int page) {
-        Raw r;
-        r.ok = p >= 0 && (uint32_t)page < (uint32_t)a.pages.n_blocks;
-        const uint32_t q = (uint32_t)max(p, 0);
-        const uint32_t off = r.ok ? q - __umul24(quotient(q, a.pages.div_bs), (uint32_t)a.pages.block_size) : 0u;
-        const uint32_t pg = r.ok ? (uint32_t)page : 0u;
-        const uint64_t at = (uint64_t)pg * (uint32_t)a.pages.d_sb + (__umul24(off, (uint32_t)a.pages.d_ss) + head_d);
-        __builtin_memcpy(r.k, __builtin_assume_aligned(a.kd + at, ALIGN), KS * 4);
-        __builtin_memcpy(r.v, __builtin_assume_aligned(a.vd + at, ALIGN), KS * 4);
-        const uint64_t sat = (uint64_t)pg * (uint32_t)a.pages.s_sb + (__umul24(off, (uint32_t)a.pages.s_ss) + head_s);
+    const int blk0 = ch * KS / 4;
+    const uint64_t chunk = (uint64_t)(uint32_t)(ch * KS * 4);
+    Raw raw[2];
+    uint32_t have = 0;  // the keys that count: bit u * 16 + row of score tile u
+    auto load_rows = [&](int b) {
+        have = (uint32_t)(found >> (b * 32));
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            // the last block of a row again where the lane has fewer than NB
-            const uint32_t more = NB * 4 == KS || NB == 1 ? (uint32_t)b : (uint32_t)(min(blk0 + b, D / 32 - 1) - blk0);
-            r.sk[b] = a.ks[sat + more];
-            r.sv[b] = a.vs[sat + more];
+        for (int u = 0; u < 2; ++u) {
+            const uint64_t d = ask(at, b, u) + chunk;
+            __builtin_memcpy(raw[u].k, __builtin_assume_aligned(kd + d, ALIGN), KS * 4);
+            __builtin_memcpy(raw[u].v, __builtin_assume_aligned(vd + d, ALIGN), KS * 4);
+            // d / 16 counts whole blocks: a row is d / 2 bytes of data and d / 32 of scales
+            const uint64_t sc = a.pages.congruent ? d >> 4 : ask(sat, b, u) + (uint64_t)(uint32_t)blk0;
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+                // the last block of a row again where the lane has fewer than NB
+                const uint32_t more =
+                    NB * 4 == KS || NB == 1 ? (uint32_t)n : (uint32_t)(min(blk0 + n, D / 32 - 1) - blk0);
+                raw[u].sk[n] = ks[sc + more];
+                raw[u].sv[n] = vs[sc + more];
+            }
         }
-        return r;
     };
-    // which of the lane's blocks its word s belongs to
-    auto block_of = [&](int s) { return KS % 4 == 0 ? s / 4 : (KS == 2 ? 0 : (qd * KS + s) / 4 - blk0); };
+    // which of the blocks of quarter c its word s belongs to
+    auto block_of = [&](int c, int s) { return KS % 4 == 0 ? s / 4 : (KS == 2 ? 0 : (c * KS + s) / 4 - c * KS / 4); };
 
     typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
     typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
     lds_u8 *stage = (lds_u8 *)smem + wave * (32 * S::ROW);
+    // K's codes change lanes through the same LDS rows before V needs them:
+    // units of 16 bytes, swapped inside a row so that the 8 lanes of an access
+    // meet different banks
+    auto unit_at = [&](int row, int unit) {
+        return S::UNITS == 4 ? row * 64 + ((unit ^ ((row >> 2) & 3)) * 16) : row * 128 + ((unit ^ ((row >> 1) & 7)) * 16);
+    };
 
-    int id[2] = {-1, -1}, pos[2], page[2];
-    Raw raw[2];
+    int id = -1, pos = -1, page = -1;
     if (t_begin < t_end) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            if (SELECTED) id[u] = load_index(t_begin, u);
-            pos[u] = position(t_begin, u, id[u]);
-            page[u] = load_page(pos[u]);
-            raw[u] = load_rows(pos[u], page[u]);
-            if (SELECTED) id[u] = load_index(t_begin + W, u);
-            pos[u] = position(t_begin + W, u, id[u]);
-            page[u] = load_page(pos[u]);
-            if (SELECTED) id[u] = load_index(t_begin + 2 * W, u);
-        }
+        if (SELECTED) id = load_index(t_begin);
+        pos = position(t_begin, id);
+        page = load_page(pos);
+        locate(pos, page);
+        load_rows(0);
+        if (SELECTED) id = load_index(t_begin + 2 * W);
+        pos = position(t_begin + 2 * W, id);
+        page = load_page(pos);
+        if (SELECTED) id = load_index(t_begin + 4 * W);
     }
 
-    for (int tile = t_begin; tile < t_end; tile += W) {
+    int odd = 0;
+    for (int tile = t_begin; tile < t_end; tile += W, odd ^= 1) {
+        const uint32_t valid = have;
+        const int p0 = SELECTED ? 0 : (tile < sink_tiles ? tile * 32 : base + (tile - sink_tiles) * 32);
+        bool whole = valid == 0xffffffffu;
+        if (!SELECTED) {
+            whole = whole && p0 + 32 <= cap_first &&
+                    (!a.window || p0 + 32 <= a.sinks || (int64_t)p0 >= last_seen - a.window);
+        }
+        // whether key `row` of score tile u counts for this lane's query row
+        auto counts = [&](int mt, int u, int row) -> bool {
+            bool in = (valid >> (u * 16 + row)) & 1u;
+            if (!SELECTED) {
+                const int p = p0 + u * 16 + row;
+                in = in && p < row_end[mt] && (p >= row_start[mt] || p < a.sinks);
+            }
+            return in;
+        };
+
+        // V's scales: 0 for keys that do not count and blocks of NaN (rare), and
+        // a mark for the rows that do attend to such a block
+        bool bad = false;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int n = 0; n < NB; ++n) bad |= raw[u].sv[n] == 255u;
+        if (valid != 0xffffffffu || __ballot(bad)) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const bool in = (valid >> (u * 16 + krow)) & 1u;
+                uint32_t mine = 0;  // this lane's key's blocks of NaN
+#pragma unroll
+                for (int n = 0; n < NB; ++n) {
+                    const bool b = raw[u].sv[n] == 255u;
+                    if (in && b) mine |= 1u << min(blk0 + n, D / 32 - 1);
+                    if (!in || b) raw[u].sv[n] = 0u;
+                }
+                if (__ballot(mine != 0u)) {
+                    for (int row = 0; row < 16; ++row) {
+                        uint32_t blocks = 0;
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) blocks |= (uint32_t)__builtin_amdgcn_readlane((int)mine, row * 4 + g);
+                        if (!blocks) continue;
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt)
+                            if (counts(mt, u, row)) nan_blocks[mt] |= blocks;
+                    }
+                }
+            }
+        }
+
+        // K's codes and scales to the lanes that multiply them: quarter qd of row
+        // col (a quarter of more than 4 words is two units)
+        constexpr int K1 = KS < 4 ? KS : 4, K2 = KS > 4 ? KS - 4 : 1, U = S::UNITS;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            lds_u8 *dst = stage + u * (16 * 16 * U);
+            uint32_t w1[K1], w2[K2];
+#pragma unroll
+            for (int i = 0; i < K1; ++i) w1[i] = raw[u].k[i];
+            put_words<K1>(dst + unit_at(krow, U == 4 ? ch : ch * 2), w1);
+            if constexpr (KS > 4) {
+#pragma unroll
+                for (int i = 0; i < K2; ++i) w2[i] = raw[u].k[4 + i];
+                put_words<K2>(dst + unit_at(krow, ch * 2 + 1), w2);
+            }
+        }
+        uint32_t kc[2][KS], sk[2][NB];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const lds_u8 *src = stage + u * (16 * 16 * U);
+            uint32_t w1[K1], w2[K2];
+            get_words<K1>(src + unit_at(col, U == 4 ? qd : qd * 2), w1);
+#pragma unroll
+            for (int i = 0; i < K1; ++i) kc[u][i] = w1[i];
+            if constexpr (KS > 4) {
+                get_words<K2>(src + unit_at(col, qd * 2 + 1), w2);
+#pragma unroll
+                for (int i = 0; i < K2; ++i) kc[u][4 + i] = w2[i];
+            }
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+                sk[u][n] = (uint32_t)__builtin_amdgcn_ds_bpermute((col * 4 + qd) * 4, (int)raw[u].sk[n]);
+        }
+
         // scores
         f32x4 s[MT][2];
 #pragma unroll
@@ -306,108 +462,59 @@ __global__ void __launch_bounds__(Shape<D>::WAVES * 64, (MT == 1 && D <= 128 ? 4
         for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int st = 0; st < KS; ++st) {
-                uint32_t sb = raw[u].sk[0];
+                uint32_t sb = sk[u][0];
 #pragma unroll
-                for (int b = 1; b < NB; ++b) sb = block_of(st) == b ? raw[u].sk[b] : sb;
-                const vec8 kv = T::from4(raw[u].k[st], __builtin_bit_cast(float, sb << 23));
+                for (int b = 1; b < NB; ++b) sb = block_of(qd, st) == b ? sk[u][b] : sb;
+                const vec8 kv = T::from4(kc[u][st], __builtin_bit_cast(float, sb << 23));
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) s[mt][u] = T::mfma(kv, q[mt][st], s[mt][u]);
             }
 
-        // V's rows into the wave's LDS, blocks of NaN as zeros
-        uint64_t valid[2];
-        bool has_nan = false;
+        // V's rows into the wave's LDS
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            valid[u] = __ballot(raw[u].ok);
-            uint32_t sv[NB];
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                const bool bad = raw[u].sv[b] == 255u;
-                has_nan |= raw[u].ok && bad;
-                sv[b] = raw[u].ok && !bad ? raw[u].sv[b] : 0u;
-            }
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int st = 0; st < KS; ++st) {
-                uint32_t sb = sv[0];
+                uint32_t sb = raw[u].sv[0];
 #pragma unroll
-                for (int b = 1; b < NB; ++b) sb = block_of(st) == b ? sv[b] : sb;
+                for (int b = 1; b < NB; ++b) sb = block_of(ch, st) == b ? raw[u].sv[b] : sb;
                 const vec8 vv = T::from4(raw[u].v[st], __builtin_bit_cast(float, sb << 23));
-                *(lds_u32x4 *)(stage + (u * 16 + col) * S::ROW + (qd * KS + st) * 16) = __builtin_bit_cast(u32x4, vv);
+                *(lds_u32x4 *)(stage + (u * 16 + krow) * S::ROW + (ch * KS + st) * 16) = __builtin_bit_cast(u32x4, vv);
             }
+
+        // the next tile's codes, into the registers this one's came from; every
+        // second tile the offsets of the next pair, the page ids of the one
+        // after, and the indices of the one after that
+        load_rows(odd ^ 1);
+        if (!odd) {
+            locate(pos, page);
+            pos = position(tile + 4 * W, id);
+            page = load_page(pos);
+            if (SELECTED) id = load_index(tile + 6 * W);
         }
 
-        // which scores count: bit 4 * qd + i of valid[u] is this lane's score i of tile u
-        const int p0 = SELECTED ? 0 : (tile < sink_tiles ? tile * 32 : base + (tile - sink_tiles) * 32);
-        bool whole = (valid[0] & valid[1] & 0xffffull) == 0xffffull;
-        if (!SELECTED) {
-            whole = whole && p0 + 32 <= cap_first &&
-                    (!a.window || p0 + 32 <= a.sinks || (int64_t)p0 >= last_seen - a.window);
-        }
-        auto counts = [&](int mt, int u, int i) -> bool {
-            bool in = (valid[u] >> (4 * qd + i)) & 1ull;
-            if (!SELECTED) {
-                const int p = p0 + u * 16 + 4 * qd + i;
-                in = in && p < row_end[mt] && (p >= row_start[mt] || p < a.sinks);
-            }
-            return in;
-        };
         if (!whole) {
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) s[mt][u][i] = counts(mt, u, i) ? s[mt][u][i] : kNegInf;
-        }
-        if (__ballot(has_nan)) {
-            // rare: mark, for each row, the blocks of V whose sum is NaN
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-                for (int kk = 0; kk < 16; ++kk) {  // row of score tile u
-                    uint32_t blocks = 0;
-#pragma unroll
-                    for (int b = 0; b < NB; ++b) {
-                        const uint64_t who = __ballot(raw[u].ok && raw[u].sv[b] == 255u && col == kk);
-#pragma unroll
-                        for (int g = 0; g < 4; ++g)
-                            if ((who >> (16 * g)) & 0xffffull) {
-                                const int blk = min(g * KS / 4 + b, D / 32 - 1);
-                                blocks |= 1u << blk;
-                            }
-                    }
-                    if (!blocks) continue;
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        bool in = (valid[u] >> kk) & 1ull;
-                        if (!SELECTED) {
-                            const int p = p0 + u * 16 + kk;
-                            in = in && p < row_end[mt] && (p >= row_start[mt] || p < a.sinks);
-                        }
-                        if (in) nan_blocks[mt] |= blocks;
-                    }
-                }
+                    for (int i = 0; i < 4; ++i) s[mt][u][i] = counts(mt, u, 4 * qd + i) ? s[mt][u][i] : kNegInf;
         }
 
-        // the next tile's codes, into the registers this one's came from; the
-        // page ids of the one after, and the indices of the one after that
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            raw[u] = load_rows(pos[u], page[u]);
-            pos[u] = position(tile + 2 * W, u, id[u]);
-            page[u] = load_page(pos[u]);
-            if (SELECTED) id[u] = load_index(tile + 3 * W, u);
-        }
-
-        // softmax: the maximum over the tile, the sum of this lane's part
+        // softmax.  The reference m of a row is a maximum so far, the same in its
+        // four lanes; it moves only when a score passes it by 2^8, so weights
+        // stay below 2^8 and the rescaling is rare
         vec8 p[MT];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-            float top = fmaxf(fmaxf(fmaxf(s[mt][0][0], s[mt][0][1]), fmaxf(s[mt][0][2], s[mt][0][3])),
-                              fmaxf(fmaxf(s[mt][1][0], s[mt][1][1]), fmaxf(s[mt][1][2], s[mt][1][3])));
-            top = quarter_max(top) * a.scale_log2;
-            if (__ballot(top > mx[mt])) {
-                const float m_new = fmaxf(mx[mt], top);
+            float top = larger(s[mt][0][0], s[mt][0][1]);
+            top = larger(larger(top, s[mt][0][2]), s[mt][0][3]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top = larger(top, s[mt][1][i]);
+            top *= a.scale_log2;
+            if (__ballot(top > mx[mt] + 8.0f)) {
+                const float m_new = larger(mx[mt], quarter_max(top));
                 const float f = m_new > mx[mt] ? __builtin_amdgcn_exp2f(mx[mt] - m_new) : 1.0f;
                 mx[mt] = m_new;
                 ls[mt] *= f;

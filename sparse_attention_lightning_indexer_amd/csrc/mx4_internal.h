@@ -37,6 +37,7 @@ struct Mx4Pages {
     int32_t block_size;
     FastDiv div_bs;
     int64_t n_slots;
+    bool congruent;  // every scale stride is a sixteenth of the data stride
 };
 
 struct Mx4Write {

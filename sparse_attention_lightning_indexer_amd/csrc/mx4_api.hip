@@ -152,7 +152,6 @@ indexer_status check_attend(const void *q, int64_t q_st, int64_t q_sh, int32_t t
     a->lse = lse;
     a->rows = n_requests * query_len;
     a->div_group = lidx::fast_div((uint32_t)a->group);
-    a->div_kv = lidx::fast_div((uint32_t)n_kv);
     a->div_pool = lidx::fast_div(1);
     return INDEXER_OK;
 }
@@ -170,6 +169,8 @@ indexer_status run_attend(lidx::Mx4Attend &a, int32_t type, int32_t head_dim, in
     a.units = p.units;
     a.m_tiles = p.m_tiles;
     a.n_splits = p.n_splits;
+    a.head_group = p.head_group;
+    a.div_kv = lidx::fast_div((uint32_t)(a.n_kv / (p.hp * p.head_group)));
     a.div_items = lidx::fast_div((uint32_t)(p.m_tiles * p.n_splits));
     a.part_o = (float *)workspace;
     a.part_ml = (float *)((char *)workspace + p.part_o_bytes);
@@ -187,7 +188,11 @@ int64_t window_keys(int32_t max_seq_len, int32_t window, int32_t sinks) {
 
 namespace lidx {
 
-// A wave holds one tile of 16 query rows, or two where a unit has more rows.
+// A wave holds one tile of 16 query rows, or two where a unit has more rows, or
+// one tile of two K/V heads where a head has at most 8 rows and the rows fill
+// the chip (1024 rows x 2048 selected keys, 8 heads: 457 us a head at a time,
+// 428 us in pairs; 128 rows 76 and 68 us; 32 rows x 512 keys 9.2 and 16.3 us).
+//
 // Where there are fewer workgroups than compute units, several share a row's
 // keys, about one workgroup per compute unit: one row of 131072 keys on 8 K/V
 // heads takes 123, 67, 41 and 43 us with 8, 16, 32 and 64 shares (32 is one a
@@ -195,8 +200,15 @@ namespace lidx {
 // of about 4 tiles of a wave; 32 rows of 512 keys on 8 heads, two tiles a
 // wave, take 9.3 us whole and 15.8 us in halves.  So keys are shared only
 // where that takes at least 4 tiles from every wave.
+//
+// Prompt rows under a window: the 8 waves of a workgroup take the same keys of
+// several K/V heads where the workgroups that leaves still fill whole rounds of
+// the compute units (one at a time fits one): 1000 rows over a window of 4096
+// 264 us with one head, 239, 221 and 219 us with 2, 4 and 8; 1024 causal rows
+// over 16384 keys 820, 787, 776 and 778 us.
 Mx4Plan plan_mx4_attend(int n_requests, int q_len, int64_t max_keys, bool selected, int n_heads, int n_kv,
                         int head_dim) {
+    constexpr int kCus = 256;
     Mx4Plan p{};
     const int group = n_heads / n_kv;
     const int64_t rows = (int64_t)n_requests * q_len;
@@ -204,17 +216,24 @@ Mx4Plan plan_mx4_attend(int n_requests, int q_len, int64_t max_keys, bool select
     p.units = selected ? (int)rows : n_requests;
     p.mt = n_m > 16 ? 2 : 1;
     p.m_tiles = (int)((n_m + 16 * p.mt - 1) / (16 * p.mt));
-    const int waves = head_dim <= 128 ? 8 : 4;
-    const int64_t items = (int64_t)p.units * p.m_tiles * n_kv;
+    p.hp = n_m <= 8 && n_kv % 2 == 0 && head_dim <= 128 && (int64_t)p.units * (n_kv / 2) >= 2 * kCus ? 2 : 1;
+    const int waves = head_dim <= 128 && p.hp == 1 ? 8 : 4;
+    const int64_t items = (int64_t)p.units * p.m_tiles * (n_kv / p.hp);
     const int64_t most = (max_keys + 32 * waves - 1) / (32 * waves);
-    int64_t splits = items > 0 ? 256 / items : 1;
+    int64_t splits = items > 0 ? kCus / items : 1;
     if (splits > most) splits = most;
     if (splits > kMx4MaxSplits) splits = kMx4MaxSplits;
     // most: tiles of a wave that has a row's keys to itself
     if (splits < 1 || most * (splits - 1) < 4 * splits) splits = 1;
     p.n_splits = (int)splits;
+    p.head_group = 1;
+    if (!selected && p.mt == 2 && waves == 8 && splits == 1)
+        for (int g = 8; g > 1 && p.head_group == 1; g /= 2) {
+            const int64_t wgs = items / g, rounds = (wgs + kCus - 1) / kCus;
+            if (n_kv % g == 0 && 10 * wgs >= 9 * rounds * kCus) p.head_group = g;
+        }
     const int64_t pieces = (int64_t)p.units * p.m_tiles * p.n_splits;
-    p.workgroups = (pieces + 7) / 8 * 8 * n_kv;
+    p.workgroups = (pieces + 7) / 8 * 8 * (n_kv / (p.hp * p.head_group));
     if (p.n_splits > 1) {
         const size_t parts = (size_t)rows * n_heads * p.n_splits;
         p.part_o_bytes = (parts * head_dim * 4 + 255) / 256 * 256;

@@ -140,16 +140,20 @@ __device__ __forceinline__ void get_words(const lds_u8 *src, uint32_t (&w)[N]) {
 
 constexpr float kNegInf = -__builtin_huge_valf();
 
-template <int D>
+template <int D, int HP>
 struct Shape {
     static constexpr int KS = D / 32;               // MFMA steps over the head dimension
     static constexpr int NT = D / 16;               // 16-dimension tiles of the product
     static constexpr int UNITS = D <= 128 ? 4 : 8;  // 16-byte units of a key's codes in LDS
     static constexpr int ROW = 2 * D + 32;          // bytes of a V row in LDS
-    static constexpr int WAVES = D <= 128 ? 8 : 4;
+    static constexpr int WAVES = D <= 128 && HP == 1 ? 8 : 4;
+    static constexpr int KPL = 16 / HP, NU = 2 * HP;  // keys of a load, loads of a tile
     static constexpr int OROW = D + 4;              // floats of a row of the join (padded)
     static constexpr int JOIN = WAVES * 16 * OROW * 4;
-    static constexpr int STAGE = WAVES * 32 * ROW;
+    // a wave's rows; the second head's (HP = 2) begin 32 bytes later, in other banks
+    static constexpr int SECOND = 16 * ROW + (HP == 2 ? 32 : 0);
+    static constexpr int WSTAGE = 16 * ROW + SECOND;
+    static constexpr int STAGE = WAVES * WSTAGE;
     static constexpr int LDS = (STAGE > JOIN ? STAGE : JOIN) + WAVES * 16 * 8;
 };
 
@@ -158,15 +162,15 @@ struct Item {
     int unit, kv, split, m0;  // row unit, K/V head, key share, first query row of its tile
 };
 
-__device__ __forceinline__ Item item_of(const Mx4Attend &a, int mt) {
+__device__ __forceinline__ Item item_of(const Mx4Attend &a, int mt, int hp) {
     // Workgroups b, b + 8, b + 16, ... run on one XCD.  Piece w = (unit, row
     // tile, key share) runs on XCD w mod 8 for all its K/V heads, one after the
     // other, so the 128-byte lines the heads of a token share are fetched into
     // one L2.
     Item it;
     const uint32_t b = blockIdx.x >> 3;
-    const uint32_t r = quotient(b, a.div_kv);
-    it.kv = (int)(b - r * a.div_kv.d);
+    const uint32_t r = quotient(b, a.div_kv);  // groups of K/V heads
+    it.kv = (int)(b - r * a.div_kv.d) * a.head_group * hp;
     const uint32_t w = r * 8u + (blockIdx.x & 7u);
     it.unit = (int)quotient(w, a.div_items);  // row tiles * key shares of a unit
     const uint32_t rest = w - (uint32_t)it.unit * a.div_items.d;
@@ -180,27 +184,41 @@ __device__ __forceinline__ Item item_of(const Mx4Attend &a, int mt) {
 // runs of `pool` keys.
 enum Mode { kWindow = 0, kKeys = 1, kPools = 2 };
 
-template <bool BF16, int D, int MT, int MODE>
-__global__ void __launch_bounds__(Shape<D>::WAVES * 64, (MT == 1 && D <= 128 ? 4 : (MT == 2 && D == 256 ? 1 : 2))) mx4_attend_kernel(Mx4Attend a) {
+// Waves per SIMD the registers have to leave room for.
+template <int D, int MT, int HP>
+constexpr int waves_per_simd() {
+    return HP == 2 ? 3 : (MT == 1 && D <= 128 ? 4 : (MT == 2 && D == 256 ? 1 : 2));
+}
+
+template <bool BF16, int D, int MT, int HP, int MODE>
+__global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D, MT, HP>())) mx4_attend_kernel(Mx4Attend a) {
+    static_assert(HP == 1 || MT == 1, "pairs of heads have one tile of rows");
     using T = Type<BF16>;
-    using S = Shape<D>;
+    using S = Shape<D, HP>;
     typedef typename T::vec8 vec8;
-    constexpr int KS = S::KS, NT = S::NT, W = S::WAVES;
+    constexpr int KS = S::KS, NT = S::NT, W = S::WAVES, NU = S::NU, KPL = S::KPL;
     constexpr bool SELECTED = MODE != kWindow;
     __shared__ __attribute__((aligned(16))) unsigned char smem[S::LDS];
 
-    const Item it = item_of(a, MT);
+    Item it = item_of(a, MT, HP);
     if (it.unit >= a.units) return;
     const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
+    // the waves: head_group groups of HP K/V heads, and for each of them
+    // `stride` waves that take its tiles in turn
+    const int stride = W / a.head_group, turn = wave / a.head_group;
+    const int first_kv = it.kv;
+    it.kv += (wave - turn * a.head_group) * HP;
     const int col = lane & 15, qd = lane >> 4;
+    // HP = 2: columns 0-7 are query rows of the first head, 8-15 of the second
+    const int hcol = HP == 2 ? col >> 3 : 0, mcol = HP == 2 ? col & 7 : col;
 
     // the unit's request, query rows and visible keys
     const int req = SELECTED ? it.unit / a.q_len : it.unit;
     const int seq = a.seq_lens[req];
     const int n_m = SELECTED ? a.group : a.q_len * a.group;  // query rows of the unit at this K/V head
     auto token_of = [&](int m) { return SELECTED ? it.unit : req * a.q_len + (int)quotient((uint32_t)m, a.div_group); };
-    auto head_of = [&](int m) {
-        return it.kv * a.group + (SELECTED ? m : m - (int)quotient((uint32_t)m, a.div_group) * a.group);
+    auto head_in = [&](int kv, int m) {
+        return kv * a.group + (SELECTED ? m : m - (int)quotient((uint32_t)m, a.div_group) * a.group);
     };
     // keys a token sees, before the cap by max_seq_len
     auto seen_of = [&](int token) { return (int64_t)seq - a.q_len + 1 + (token - req * a.q_len); };
@@ -223,7 +241,7 @@ __global__ void __launch_bounds__(Shape<D>::WAVES * 64, (MT == 1 && D <= 128 ? 4
     if (a.pages.n_blocks == 0) n_tiles = 0;
     const int per = (n_tiles + a.n_splits - 1) / a.n_splits;
     const int t_end = min(n_tiles, (it.split + 1) * per);
-    const int t_begin = it.split * per + wave;
+    const int t_begin = it.split * per + turn;
 
     // per query-row tile: this lane's column of Q (its row's values in the
     // order of the lane's part of the contraction), and the row's window
@@ -234,11 +252,10 @@ __global__ void __launch_bounds__(Shape<D>::WAVES * 64, (MT == 1 && D <= 128 ? 4
     uint32_t nan_blocks[MT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-        const int m = it.m0 + mt * 16 + col;
-        const int mc = min(m, n_m - 1);
+        const int mc = min(it.m0 + mt * 16 + mcol, n_m - 1);
         const int token = token_of(mc);
         const uint4 *src = reinterpret_cast<const uint4 *>((const uint16_t *)a.q + (int64_t)token * a.q_st +
-                                                           (int64_t)head_of(mc) * a.q_sh + qd * (KS * 8));
+                                                           (int64_t)head_in(it.kv + hcol, mc) * a.q_sh + qd * (KS * 8));
 #pragma unroll
         for (int s = 0; s < KS; ++s) q[mt][s] = __builtin_bit_cast(vec8, src[s]);
         const int64_t seen = seen_of(token);
@@ -253,12 +270,13 @@ __global__ void __launch_bounds__(Shape<D>::WAVES * 64, (MT == 1 && D <= 128 ? 4
 
     // A tile's 32 keys are the rows of score tiles 0 and 1 (keys `row` and 16 +
     // row of the tile).  Four neighbouring lanes load a key's row, a quarter
-    // each, so that their 16-byte loads fall into one line; where the lanes of
-    // one row were 16 apart, as the products want them, a load instruction took
-    // four times the line lookups, which bounded the kernel.  Finding the rows
-    // is shared: of the 64 keys of two tiles (this one and the wave's next)
-    // each lane finds one, and the others ask it for the offset.
-    const int krow = lane >> 2, ch = lane & 3;
+    // each (HP = 2: eight lanes the rows of both heads), so that their 16-byte
+    // loads fall into one line; where the lanes of one row were 16 apart, as the
+    // products want them, a load instruction took four times the line lookups.
+    // Load u takes keys u * KPL + krow.  Finding the rows is shared: of the 64
+    // keys of two tiles (this one and the wave's next) each lane finds one, and
+    // the others ask it for the offset.
+    const int krow = lane >> (HP + 1), ch = lane & 3, hsel = HP == 2 ? (lane >> 2) & 1 : 0;
     const uint64_t head_d = (uint64_t)((uint32_t)it.kv * (uint32_t)a.pages.d_sh);
     const uint32_t head_s = (uint32_t)it.kv * (uint32_t)a.pages.s_sh;
     const uint8_t *kd = a.kd + head_d, *vd = a.vd + head_d, *ks = a.ks + head_s, *vs = a.vs + head_s;
@@ -266,7 +284,7 @@ __global__ void __launch_bounds__(Shape<D>::WAVES * 64, (MT == 1 && D <= 128 ? 4
     const int32_t *sel = SELECTED ? a.idx + (int64_t)it.unit * a.idx_st : nullptr;
     const uint32_t end_entry = SELECTED ? min((uint32_t)a.n_sel * (uint32_t)a.pool, (uint32_t)t_end * 32u) : 0u;
     const uint32_t end_unit = MODE == kPools ? (uint32_t)(cap_last + a.pool - 1) / (uint32_t)a.pool : 0u;
-    const uint32_t own_tile = (uint32_t)(qd >> 1) * W, own_key = (uint32_t)((qd & 1) * 16 + col);
+    const uint32_t own_tile = (uint32_t)((qd >> 1) * stride), own_key = (uint32_t)((qd & 1) * 16 + col);
 
     // The steps from a pair of tiles to its offsets.  Each loads from a place
     // that exists whatever the lane's key (a clamped entry, page 0 of the table,
@@ -303,9 +321,9 @@ __global__ void __launch_bounds__(Shape<D>::WAVES * 64, (MT == 1 && D <= 128 ? 4
         if (!a.pages.congruent) sat = (uint64_t)pg * (uint32_t)a.pages.s_sb + __umul24(o, (uint32_t)a.pages.s_ss);
         found = __ballot(ok);
     };
-    // from the lane that found row krow of score tile u of tile `b` of the pair
+    // from the lane that found this lane's key of load u of tile `b` of the pair
     auto ask = [&](uint64_t v, int b, int u) -> uint64_t {
-        const int who = (b * 32 + u * 16 + krow) * 4;
+        const int who = (b * 32 + u * KPL + krow) * 4;
         const uint32_t lo = (uint32_t)__builtin_amdgcn_ds_bpermute(who, (int)(uint32_t)v);
         const uint32_t hi = (uint32_t)__builtin_amdgcn_ds_bpermute(who, (int)(uint32_t)(v >> 32));
         return ((uint64_t)hi << 32) | lo;
@@ -319,26 +337,22 @@ __global__ void __launch_bounds__(Shape<D>::WAVES * 64, (MT == 1 && D <= 128 ? 4
         uint32_t sk[NB], sv[NB];
     };
     const int blk0 = ch * KS / 4;
-    const uint64_t chunk = (uint64_t)(uint32_t)(ch * KS * 4);
-    Raw raw[2];
-    uint32_t have = 0;  // the keys that count: bit u * 16 + row of score tile u
-    auto load_rows = [&](int b) {
-        have = (uint32_t)(found >> (b * 32));
+    const uint64_t chunk = (uint64_t)((uint32_t)hsel * (uint32_t)a.pages.d_sh) + (uint32_t)(ch * KS * 4);
+    const uint64_t schunk = (uint64_t)((uint32_t)hsel * (uint32_t)a.pages.s_sh) + (uint32_t)blk0;
+    Raw raw[NU];
+    uint32_t have = 0;  // the keys that count: bit k is key k of the tile
+    // K's part of load u, V's, or both
+    auto load_rows = [&](int b, int u, bool k, bool v) {
+        const uint64_t row = ask(at, b, u), d = row + chunk;
+        if (k) __builtin_memcpy(raw[u].k, __builtin_assume_aligned(kd + d, ALIGN), KS * 4);
+        if (v) __builtin_memcpy(raw[u].v, __builtin_assume_aligned(vd + d, ALIGN), KS * 4);
+        const uint64_t sc = (a.pages.congruent ? row >> 4 : ask(sat, b, u)) + schunk;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const uint64_t d = ask(at, b, u) + chunk;
-            __builtin_memcpy(raw[u].k, __builtin_assume_aligned(kd + d, ALIGN), KS * 4);
-            __builtin_memcpy(raw[u].v, __builtin_assume_aligned(vd + d, ALIGN), KS * 4);
-            // d / 16 counts whole blocks: a row is d / 2 bytes of data and d / 32 of scales
-            const uint64_t sc = a.pages.congruent ? d >> 4 : ask(sat, b, u) + (uint64_t)(uint32_t)blk0;
-#pragma unroll
-            for (int n = 0; n < NB; ++n) {
-                // the last block of a row again where the lane has fewer than NB
-                const uint32_t more =
-                    NB * 4 == KS || NB == 1 ? (uint32_t)n : (uint32_t)(min(blk0 + n, D / 32 - 1) - blk0);
-                raw[u].sk[n] = ks[sc + more];
-                raw[u].sv[n] = vs[sc + more];
-            }
+        for (int n = 0; n < NB; ++n) {
+            // the last block of a row again where the lane has fewer than NB
+            const uint32_t more = NB * 4 == KS || NB == 1 ? (uint32_t)n : (uint32_t)(min(blk0 + n, D / 32 - 1) - blk0);
+            if (k) raw[u].sk[n] = ks[sc + more];
+            if (v) raw[u].sv[n] = vs[sc + more];
         }
     };
     // which of the blocks of quarter c its word s belongs to
@@ -346,12 +360,23 @@ __global__ void __launch_bounds__(Shape<D>::WAVES * 64, (MT == 1 && D <= 128 ? 4
 
     typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
     typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
-    lds_u8 *stage = (lds_u8 *)smem + wave * (32 * S::ROW);
+    lds_u8 *stage = (lds_u8 *)smem + wave * S::WSTAGE;
     // K's codes change lanes through the same LDS rows before V needs them:
     // units of 16 bytes, swapped inside a row so that the 8 lanes of an access
     // meet different banks
     auto unit_at = [&](int row, int unit) {
         return S::UNITS == 4 ? row * 64 + ((unit ^ ((row >> 2) & 3)) * 16) : row * 128 + ((unit ^ ((row >> 1) & 7)) * 16);
+    };
+
+    // four keys of 16 dimensions, transposed, and the four 16 rows on
+    auto two_reads = [&](lds_u8 *src) -> vec8 {
+        union {
+            s16x4 h[2];
+            vec8 v;
+        } vt;
+        vt.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)src);
+        vt.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(src + S::SECOND));
+        return vt.v;
     };
 
     int id = -1, pos = -1, page = -1;
@@ -360,15 +385,17 @@ __global__ void __launch_bounds__(Shape<D>::WAVES * 64, (MT == 1 && D <= 128 ? 4
         pos = position(t_begin, id);
         page = load_page(pos);
         locate(pos, page);
-        load_rows(0);
-        if (SELECTED) id = load_index(t_begin + 2 * W);
-        pos = position(t_begin + 2 * W, id);
+        have = (uint32_t)found;
+#pragma unroll
+        for (int u = 0; u < NU; ++u) load_rows(0, u, true, true);
+        if (SELECTED) id = load_index(t_begin + 2 * stride);
+        pos = position(t_begin + 2 * stride, id);
         page = load_page(pos);
-        if (SELECTED) id = load_index(t_begin + 4 * W);
+        if (SELECTED) id = load_index(t_begin + 4 * stride);
     }
 
     int odd = 0;
-    for (int tile = t_begin; tile < t_end; tile += W, odd ^= 1) {
+    for (int tile = t_begin; tile < t_end; tile += stride, odd ^= 1) {
         const uint32_t valid = have;
         const int p0 = SELECTED ? 0 : (tile < sink_tiles ? tile * 32 : base + (tile - sink_tiles) * 32);
         bool whole = valid == 0xffffffffu;
@@ -376,11 +403,11 @@ __global__ void __launch_bounds__(Shape<D>::WAVES * 64, (MT == 1 && D <= 128 ? 4
             whole = whole && p0 + 32 <= cap_first &&
                     (!a.window || p0 + 32 <= a.sinks || (int64_t)p0 >= last_seen - a.window);
         }
-        // whether key `row` of score tile u counts for this lane's query row
-        auto counts = [&](int mt, int u, int row) -> bool {
-            bool in = (valid >> (u * 16 + row)) & 1u;
+        // whether key k of the tile counts for this lane's query row
+        auto counts = [&](int mt, int k) -> bool {
+            bool in = (valid >> k) & 1u;
             if (!SELECTED) {
-                const int p = p0 + u * 16 + row;
+                const int p = p0 + k;
                 in = in && p < row_end[mt] && (p >= row_start[mt] || p < a.sinks);
             }
             return in;
@@ -390,14 +417,14 @@ __global__ void __launch_bounds__(Shape<D>::WAVES * 64, (MT == 1 && D <= 128 ? 4
         // a mark for the rows that do attend to such a block
         bool bad = false;
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < NU; ++u)
 #pragma unroll
             for (int n = 0; n < NB; ++n) bad |= raw[u].sv[n] == 255u;
         if (valid != 0xffffffffu || __ballot(bad)) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const bool in = (valid >> (u * 16 + krow)) & 1u;
-                uint32_t mine = 0;  // this lane's key's blocks of NaN
+            for (int u = 0; u < NU; ++u) {
+                const bool in = (valid >> (u * KPL + krow)) & 1u;
+                uint32_t mine = 0;  // blocks of NaN in this lane's part of its key
 #pragma unroll
                 for (int n = 0; n < NB; ++n) {
                     const bool b = raw[u].sv[n] == 255u;
@@ -405,14 +432,15 @@ __global__ void __launch_bounds__(Shape<D>::WAVES * 64, (MT == 1 && D <= 128 ? 4
                     if (!in || b) raw[u].sv[n] = 0u;
                 }
                 if (__ballot(mine != 0u)) {
-                    for (int row = 0; row < 16; ++row) {
-                        uint32_t blocks = 0;
+                    for (int row = 0; row < KPL; ++row) {
+                        uint32_t blocks[2] = {0u, 0u};
 #pragma unroll
-                        for (int g = 0; g < 4; ++g) blocks |= (uint32_t)__builtin_amdgcn_readlane((int)mine, row * 4 + g);
-                        if (!blocks) continue;
+                        for (int g = 0; g < 4 * HP; ++g)
+                            blocks[g >> 2] |= (uint32_t)__builtin_amdgcn_readlane((int)mine, row * 4 * HP + g);
+                        if (!(blocks[0] | blocks[1])) continue;
 #pragma unroll
                         for (int mt = 0; mt < MT; ++mt)
-                            if (counts(mt, u, row)) nan_blocks[mt] |= blocks;
+                            if (counts(mt, u * KPL + row)) nan_blocks[mt] |= hcol ? blocks[1] : blocks[0];
                     }
                 }
             }
@@ -420,78 +448,103 @@ __global__ void __launch_bounds__(Shape<D>::WAVES * 64, (MT == 1 && D <= 128 ? 4
 
         // K's codes and scales to the lanes that multiply them: quarter qd of row
         // col (a quarter of more than 4 words is two units)
-        constexpr int K1 = KS < 4 ? KS : 4, K2 = KS > 4 ? KS - 4 : 1, U = S::UNITS;
+        constexpr int K1 = KS < 4 ? KS : 4, K2 = KS > 4 ? KS - 4 : 1, U = S::UNITS, TILE = 16 * 16 * U, HEAD = 2 * TILE + 128;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            lds_u8 *dst = stage + u * (16 * 16 * U);
+        for (int u = 0; u < NU; ++u) {
+            const int key = u * KPL + krow;  // key >> 4 is the same in all lanes
+            lds_u8 *dst = stage + hsel * HEAD + (u * KPL >> 4) * TILE;
             uint32_t w1[K1], w2[K2];
 #pragma unroll
             for (int i = 0; i < K1; ++i) w1[i] = raw[u].k[i];
-            put_words<K1>(dst + unit_at(krow, U == 4 ? ch : ch * 2), w1);
+            put_words<K1>(dst + unit_at(key & 15, U == 4 ? ch : ch * 2), w1);
             if constexpr (KS > 4) {
 #pragma unroll
                 for (int i = 0; i < K2; ++i) w2[i] = raw[u].k[4 + i];
-                put_words<K2>(dst + unit_at(krow, ch * 2 + 1), w2);
+                put_words<K2>(dst + unit_at(key & 15, ch * 2 + 1), w2);
             }
         }
-        uint32_t kc[2][KS], sk[2][NB];
+        // scales, a byte per load in one word: lane (row, head, quarter) has them
+        uint32_t pack[NB];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const lds_u8 *src = stage + u * (16 * 16 * U);
-            uint32_t w1[K1], w2[K2];
-            get_words<K1>(src + unit_at(col, U == 4 ? qd : qd * 2), w1);
+        for (int n = 0; n < NB; ++n) {
+            pack[n] = raw[0].sk[n];
 #pragma unroll
-            for (int i = 0; i < K1; ++i) kc[u][i] = w1[i];
-            if constexpr (KS > 4) {
-                get_words<K2>(src + unit_at(col, qd * 2 + 1), w2);
-#pragma unroll
-                for (int i = 0; i < K2; ++i) kc[u][4 + i] = w2[i];
-            }
-#pragma unroll
-            for (int n = 0; n < NB; ++n)
-                sk[u][n] = (uint32_t)__builtin_amdgcn_ds_bpermute((col * 4 + qd) * 4, (int)raw[u].sk[n]);
+            for (int u = 1; u < NU; ++u) pack[n] |= raw[u].sk[n] << (8 * u);
         }
 
-        // scores
+        // scores: of each head with all columns, then each column its head's
         f32x4 s[MT][2];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int hh = 0; hh < HP; ++hh) {
+            uint32_t sk[NB];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) s[mt][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int st = 0; st < KS; ++st) {
-                uint32_t sb = sk[u][0];
-#pragma unroll
-                for (int b = 1; b < NB; ++b) sb = block_of(qd, st) == b ? sk[u][b] : sb;
-                const vec8 kv = T::from4(kc[u][st], __builtin_bit_cast(float, sb << 23));
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) s[mt][u] = T::mfma(kv, q[mt][st], s[mt][u]);
+            for (int n = 0; n < NB; ++n) {
+                const int who = ((col & (KPL - 1)) * 4 * HP + hh * 4 + qd) * 4;
+                sk[n] = (uint32_t)__builtin_amdgcn_ds_bpermute(who, (int)pack[n]) >> (HP == 2 ? 8 * hcol : 0);
             }
-
-        // V's rows into the wave's LDS
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+            for (int u = 0; u < 2; ++u) {
+                uint32_t kc[KS], w1[K1], w2[K2];
+                const lds_u8 *src = stage + hh * HEAD + u * TILE;
+                get_words<K1>(src + unit_at(col, U == 4 ? qd : qd * 2), w1);
+#pragma unroll
+                for (int i = 0; i < K1; ++i) kc[i] = w1[i];
+                if constexpr (KS > 4) {
+                    get_words<K2>(src + unit_at(col, qd * 2 + 1), w2);
+#pragma unroll
+                    for (int i = 0; i < K2; ++i) kc[4 + i] = w2[i];
+                }
+                f32x4 sum[MT];
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) sum[mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int st = 0; st < KS; ++st) {
+                    uint32_t sb = sk[0];
+#pragma unroll
+                    for (int b = 1; b < NB; ++b) sb = block_of(qd, st) == b ? sk[b] : sb;
+                    sb = (sb >> (8 * HP * u)) & 255u;
+                    const vec8 kv = T::from4(kc[st], __builtin_bit_cast(float, sb << 23));
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) sum[mt] = T::mfma(kv, q[mt][st], sum[mt]);
+                }
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s[mt][u][i] = hh == 0 || hcol ? sum[mt][i] : s[mt][u][i];
+            }
+        }
+
+        // V's rows into the wave's LDS: all of them, or (HP = 2) 16 keys of both
+        // heads, the other 16 when these are used up
+        auto store_v = [&](int u) {
 #pragma unroll
             for (int st = 0; st < KS; ++st) {
                 uint32_t sb = raw[u].sv[0];
 #pragma unroll
                 for (int b = 1; b < NB; ++b) sb = block_of(ch, st) == b ? raw[u].sv[b] : sb;
                 const vec8 vv = T::from4(raw[u].v[st], __builtin_bit_cast(float, sb << 23));
-                *(lds_u32x4 *)(stage + (u * 16 + krow) * S::ROW + (ch * KS + st) * 16) = __builtin_bit_cast(u32x4, vv);
+                lds_u8 *row = stage + (HP == 2 ? hsel * S::SECOND + ((u & 1) * KPL + krow) * S::ROW
+                                               : (u * KPL + krow) * S::ROW);
+                *(lds_u32x4 *)(row + (ch * KS + st) * 16) = __builtin_bit_cast(u32x4, vv);
             }
+        };
+        store_v(0);
+        store_v(1);
 
         // the next tile's codes, into the registers this one's came from; every
         // second tile the offsets of the next pair, the page ids of the one
         // after, and the indices of the one after that
-        load_rows(odd ^ 1);
-        if (!odd) {
+        have = (uint32_t)(found >> ((odd ^ 1) * 32));
+#pragma unroll
+        for (int u = 0; u < NU; ++u) load_rows(odd ^ 1, u, true, u < 2);
+        auto advance = [&]() {
+            if (odd) return;
             locate(pos, page);
-            pos = position(tile + 4 * W, id);
+            pos = position(tile + 4 * stride, id);
             page = load_page(pos);
-            if (SELECTED) id = load_index(tile + 6 * W);
-        }
+            if (SELECTED) id = load_index(tile + 6 * stride);
+        };
+        if (HP == 1) advance();
 
         if (!whole) {
 #pragma unroll
@@ -499,7 +552,8 @@ __global__ void __launch_bounds__(Shape<D>::WAVES * 64, (MT == 1 && D <= 128 ? 4
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) s[mt][u][i] = counts(mt, u, 4 * qd + i) ? s[mt][u][i] : kNegInf;
+                    for (int i = 0; i < 4; ++i)
+                        s[mt][u][i] = counts(mt, u * 16 + 4 * qd + i) ? s[mt][u][i] : kNegInf;
         }
 
         // softmax.  The reference m of a row is a maximum so far, the same in its
@@ -536,18 +590,34 @@ __global__ void __launch_bounds__(Shape<D>::WAVES * 64, (MT == 1 && D <= 128 ? 4
             ls[mt] += sum;
         }
 
-        // O^T += V^T P^T
+        // O^T += V^T P^T.  HP = 2: a product over 16 keys of both heads, with
+        // zeros for P where a column is the other head's
+        if constexpr (HP == 1) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            lds_u8 *src = stage + (4 * qd + (col >> 2)) * S::ROW + n * 32 + (col & 3) * 8;
-            union {
-                s16x4 h[2];
-                vec8 v;
-            } vt;
-            vt.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)src);
-            vt.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(src + 16 * S::ROW));
+            for (int n = 0; n < NT; ++n) {
+                const vec8 vt = two_reads(stage + (4 * qd + (col >> 2)) * S::ROW + n * 32 + (col & 3) * 8);
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) o[mt][n] = T::mfma(vt.v, p[mt], o[mt][n]);
+                for (int mt = 0; mt < MT; ++mt) o[mt][n] = T::mfma(vt, p[mt], o[mt][n]);
+            }
+        } else {
+            const u32x4 pw = __builtin_bit_cast(u32x4, p[0]);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if (t) {
+                    store_v(2);
+                    store_v(3);
+                    load_rows(odd ^ 1, 2, false, true);
+                    load_rows(odd ^ 1, 3, false, true);
+                    advance();
+                }
+                const vec8 pt = __builtin_bit_cast(vec8, u32x4{hcol ? 0u : pw[2 * t], hcol ? 0u : pw[2 * t + 1],
+                                                               hcol ? pw[2 * t] : 0u, hcol ? pw[2 * t + 1] : 0u});
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const vec8 vt = two_reads(stage + (4 * qd + (col >> 2)) * S::ROW + n * 32 + (col & 3) * 8);
+                    o[0][n] = T::mfma(vt, pt, o[0][n]);
+                }
+            }
         }
     }
 
@@ -571,24 +641,25 @@ __global__ void __launch_bounds__(Shape<D>::WAVES * 64, (MT == 1 && D <= 128 ? 4
             jml[(wave * 16 + col) * 2 + 1] = l;
         }
         __syncthreads();
-        for (int e = threadIdx.x; e < 16 * (D / 8); e += W * 64) {
-            const int row = e / (D / 8), c = e - row * (D / 8);
-            const int m = it.m0 + mt * 16 + row;
+        for (int e = threadIdx.x; e < a.head_group * 16 * (D / 8); e += W * 64) {
+            const int hrow = e / (D / 8), c = e - hrow * (D / 8);
+            const int hg = hrow >> 4, row = hrow & 15;
+            const int m = HP == 2 ? row & 7 : it.m0 + mt * 16 + row;
             if (m >= n_m) continue;
+            const float *ml = jml + (hg * 16 + row) * 2, *src = jo + (hg * 16 + row) * S::OROW + c * 8;
+            const int step = a.head_group * 16;  // to the next wave of this head
             float m_all = kNegInf;
-#pragma unroll
-            for (int w = 0; w < W; ++w) m_all = fmaxf(m_all, jml[(w * 16 + row) * 2]);
+            for (int w = 0; w < stride; ++w) m_all = fmaxf(m_all, ml[w * step * 2]);
             const float sub = m_all == kNegInf ? 0.0f : m_all;
             float l_all = 0.0f, acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+            for (int w = 0; w < stride; ++w) {
+                const float f = __builtin_amdgcn_exp2f(ml[w * step * 2] - sub);
+                l_all += f * ml[w * step * 2 + 1];
 #pragma unroll
-            for (int w = 0; w < W; ++w) {
-                const float f = __builtin_amdgcn_exp2f(jml[(w * 16 + row) * 2] - sub);
-                l_all += f * jml[(w * 16 + row) * 2 + 1];
-                const float *src = jo + (w * 16 + row) * S::OROW + c * 8;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) acc[i] += f * src[i];
+                for (int i = 0; i < 8; ++i) acc[i] += f * src[w * step * S::OROW + i];
             }
-            const int token = token_of(m), head = head_of(m);
+            const int token = token_of(m), head = head_in(first_kv + hg * HP + (HP == 2 ? row >> 3 : 0), m);
             const int64_t th = (int64_t)token * a.n_heads + head;
             if (a.n_splits > 1) {
                 float *dst2 = a.part_o + (th * a.n_splits + it.split) * D + c * 8;
@@ -670,15 +741,15 @@ __global__ void __launch_bounds__(256) mx4_join_kernel(Mx4Attend a) {
     *reinterpret_cast<vec8 *>((uint16_t *)a.out + token * a.out_st + (int64_t)head * a.out_sh + threadIdx.x * 8) = r;
 }
 
-template <bool BF16, int D, int MT>
+template <bool BF16, int D, int MT, int HP>
 hipError_t launch_tiles(const Mx4Attend &a, const Mx4Plan &p, hipStream_t stream) {
-    const dim3 grid((unsigned)p.workgroups), block(Shape<D>::WAVES * 64);
+    const dim3 grid((unsigned)p.workgroups), block(Shape<D, HP>::WAVES * 64);
     if (!a.idx)
-        hipLaunchKernelGGL((mx4_attend_kernel<BF16, D, MT, kWindow>), grid, block, 0, stream, a);
+        hipLaunchKernelGGL((mx4_attend_kernel<BF16, D, MT, HP, kWindow>), grid, block, 0, stream, a);
     else if (a.pool == 1)
-        hipLaunchKernelGGL((mx4_attend_kernel<BF16, D, MT, kKeys>), grid, block, 0, stream, a);
+        hipLaunchKernelGGL((mx4_attend_kernel<BF16, D, MT, HP, kKeys>), grid, block, 0, stream, a);
     else
-        hipLaunchKernelGGL((mx4_attend_kernel<BF16, D, MT, kPools>), grid, block, 0, stream, a);
+        hipLaunchKernelGGL((mx4_attend_kernel<BF16, D, MT, HP, kPools>), grid, block, 0, stream, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.n_splits == 1) return e;
     hipLaunchKernelGGL((mx4_join_kernel<BF16, D>), dim3((unsigned)(a.rows * a.n_heads)), dim3(256), 0, stream, a);
@@ -687,8 +758,11 @@ hipError_t launch_tiles(const Mx4Attend &a, const Mx4Plan &p, hipStream_t stream
 
 template <bool BF16, int D>
 hipError_t launch_dim(const Mx4Attend &a, const Mx4Plan &p, hipStream_t stream) {
-    if (p.mt == 1) return launch_tiles<BF16, D, 1>(a, p, stream);
-    return launch_tiles<BF16, D, 2>(a, p, stream);
+    if constexpr (D <= 128) {
+        if (p.hp == 2) return launch_tiles<BF16, D, 1, 2>(a, p, stream);
+    }
+    if (p.mt == 1) return launch_tiles<BF16, D, 1, 1>(a, p, stream);
+    return launch_tiles<BF16, D, 2, 1>(a, p, stream);
 }
 
 template <bool BF16>

@@ -93,6 +93,7 @@ struct Mx4Attend {
     int32_t units;      // row units: rows (selected) or requests (window)
     int32_t m_tiles;    // tiles of query rows per unit and K/V head
     int32_t n_splits;   // workgroups that share a tile's keys
+    int32_t head_group; // groups of hp K/V heads a workgroup's waves are shared out to
     float *part_o;      // [rows][n_heads][n_splits][head_dim]
     float *part_ml;     // [rows][n_heads][n_splits][2]
 };
@@ -102,7 +103,7 @@ constexpr int kMx4MaxSplits = 64;
 // Launch geometry: how many 16-row tiles a wave holds and how many workgroups
 // share a row's keys; a function of sizes alone.
 struct Mx4Plan {
-    int mt, m_tiles, n_splits, units;
+    int mt, hp, m_tiles, n_splits, head_group, units;
     int64_t workgroups;
     size_t part_o_bytes, workspace_bytes;
 };

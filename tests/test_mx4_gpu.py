@@ -347,6 +347,63 @@ def test_nan_stays_with_the_rows_that_see_it(kind):
     run_selected(case, selection(case, 30), where="V NaN selected or not")
 
 
+# Sizes at which a wave takes two K/V heads (at most 8 query rows a head, an even
+# number of K/V heads, rows * K/V heads >= 1024)
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("query,heads,kv,d,bs", [(1, 32, 16, 64, 16), (1, 128, 16, 128, 7), (2, 16, 16, 96, 32),
+                                                 (2, 64, 16, 128, 16)])
+def test_pairs_of_heads(query, heads, kv, d, bs, kind):
+    rng = np.random.default_rng(d + query)
+    lens = [0, 1, 2, 31, 32, 33, 64, 65] + rng.integers(1, 150, 56).tolist()
+    case = Case(40, lens, query, heads, kv, d, bs, kind)
+    where = f"pairs {query} {heads}/{kv} {d} {kind}"
+    run_selected(case, selection(case, 70), where=where)
+    run_selected(case, selection(case, 7, 9), 9, where=where + " pooled")
+    run_window(case, 0, 0, where=where + " causal")
+    run_window(case, 40, 3, where=where + " window")
+    # NaN: of one head only, in keys some rows see and others do not
+    for which, head, key, block in ((1, 3, 0, 0), (1, 4, 20, d // 32 - 1), (0, 6, 5, 0), (1, 9, 17, 1)):
+        for r in (6, 9, 20):
+            if key < lens[r]:
+                case.scale[which][case.table[r, key // bs], key % bs, head, block] = 255
+    out, _ = run_window(case, 40, 3, where=where + " window, NaN")
+    assert torch.isnan(out).any()
+    run_selected(case, selection(case, 70), where=where + " NaN")
+
+
+# Sizes at which the waves of a workgroup take 2, 4 and 8 K/V heads (more than 16
+# query rows a head and request, workgroups that fill the chip)
+@pytest.mark.parametrize("requests,kv,kind", [(64, 8, "f16"), (128, 8, "bf16"), (240, 8, "f16"), (120, 2, "bf16")])
+def test_groups_of_heads(requests, kv, kind):
+    rng = np.random.default_rng(requests)
+    lens = rng.integers(1, 90, requests).tolist()
+    case = Case(41, lens, 8, 4 * kv, kv, 64, 16, kind)
+    args = case.args()
+    scale = case.sm_scale
+    for window, sinks in ((0, 0), (30, 5)):
+        out, lse = li.mx4_attend_window(*args, case.max_seq_len, scale, window=window, sinks=sinks)
+        # a request at a time: the same keys in the same tiles of one wave's order or another
+        few = [0, 1, requests // 2, requests - 1]
+        small = Case(41, [lens[r] for r in few], 8, 4 * kv, kv, 64, 16, kind)
+        small.table, small.data, small.scale, small.n_blocks = (case.table[few], case.data, case.scale, case.n_blocks)
+        small.max_seq_len = case.max_seq_len
+        rows = np.concatenate([np.arange(8 * r, 8 * r + 8) for r in few])
+        small.q_t, small.q = case.q_t[torch.from_numpy(rows)], case.q[rows]
+        want = small.want(lambda t, v, e: plain.positions_window(v, e, window, sinks))
+        pick = torch.from_numpy(rows).to(DEV)
+        check((out[pick], lse[pick]), want, kind, 64, f"groups {requests} {kv} {window} {kind}")
+        for a in range(0, requests, 7):                     # every row against its own small call
+            b = min(requests, a + 7)
+            q, kd, ks, vd, vs, table, sl, Q = args
+            o, z = li.mx4_attend_window(q[8 * a:8 * b], kd, ks, vd, vs, table[a:b], sl[a:b], Q, case.max_seq_len, scale,
+                                        window=window, sinks=sinks)
+            # both within the bound of the exact values: at most twice it apart; |V| <= 6 * 2
+            assert float((o.float() - out[8 * a:8 * b].float()).abs().max()) <= 2 * (3 * UNIT[kind] + 2.0**-12) * 12
+            fine = torch.isfinite(z)
+            assert torch.equal(fine, torch.isfinite(lse[8 * a:8 * b]))
+            assert float((z - lse[8 * a:8 * b])[fine].abs().max()) <= 2.0**-12
+
+
 @pytest.mark.parametrize("kind", ["f16", "bf16"])
 def test_large_scores(kind):
     """Scores in the hundreds: one key takes nearly all the weight, maxima rise through the row."""

@@ -100,6 +100,27 @@ def test_write_and_read(kind, n, heads, d, bs, order):
         assert np.array_equal(got, want)                   # exact: every stored value is of the type
 
 
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+def test_write_and_read_many(kind):
+    """More values than the caches hold (the streaming forms), against the same rows written a few at a time."""
+    n, heads, d = 20011, 7, 128
+    x = (torch.randn((n, heads, d), device=DEV) * 3).to(DTYPE[kind])
+    slots = torch.randperm(n + 50, device=DEV)[:n]
+    slots[::101] = -1
+    big, small = fresh(n + 50, 1, heads, d), fresh(n + 50, 1, heads, d)
+    li.mx4_cache_write(x, slots, *big)
+    for a in range(0, n, 4000):
+        li.mx4_cache_write(x[a:a + 4000], slots[a:a + 4000], *small)
+    assert all(torch.equal(p, q) for p, q in zip(big, small))
+    got = li.mx4_cache_read(*big, slots, DTYPE[kind])
+    parts = [li.mx4_cache_read(*small, slots[a:a + 4000], DTYPE[kind]) for a in range(0, n, 4000)]
+    assert torch.equal(got, torch.cat(parts)) and (got[::101] == 0).all()
+    few = torch.arange(3, 40, device=DEV)
+    want = plain.values(*plain.quantise(x[few].double().cpu().numpy(), kind))
+    want[slots[few].cpu().numpy() < 0] = 0.0
+    assert np.array_equal(got[few].double().cpu().numpy(), want)
+
+
 def test_write_one_tensor_and_strided_rows():
     """K alone, taken from a fused projection's output, into one cache."""
     rng = np.random.default_rng(2)

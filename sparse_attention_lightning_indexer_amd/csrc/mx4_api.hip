@@ -188,6 +188,18 @@ int64_t window_keys(int32_t max_seq_len, int32_t window, int32_t sinks) {
 
 namespace lidx {
 
+// The launch size and workspace of a plan.
+static Mx4Plan sized(Mx4Plan p, int64_t rows, int n_heads, int n_kv, int head_dim) {
+    const int64_t pieces = (int64_t)p.units * p.m_tiles * p.n_splits;
+    p.workgroups = (pieces + 7) / 8 * 8 * (n_kv / (p.hp * p.head_group));
+    if (p.n_splits > 1) {
+        const size_t parts = (size_t)rows * n_heads * p.n_splits;
+        p.part_o_bytes = (parts * head_dim * 4 + 255) / 256 * 256;
+        p.workspace_bytes = p.part_o_bytes + (parts * 8 + 255) / 256 * 256;
+    }
+    return p;
+}
+
 // A wave holds one tile of 16 query rows, or two where a unit has more rows, or
 // one tile of two K/V heads where a head has at most 8 rows and the rows fill
 // the chip (1024 rows x 2048 selected keys, 8 heads: 457 us a head at a time,
@@ -201,7 +213,20 @@ namespace lidx {
 // wave, take 9.3 us whole and 15.8 us in halves.  So keys are shared only
 // where that takes at least 4 tiles from every wave.
 //
-// Prompt rows under a window: the 8 waves of a workgroup take the same keys of
+// Many rows of a request under a window go through the keys 256 at a time and
+// together (mx4_prompt_kernel) where that is the shorter of two estimates, fit
+// to head dimension 128 and 8 K/V heads of 8 query heads: 2.05 us for 64 keys
+// and 256 rows a compute unit (1.8 us half full), rounds of one workgroup a
+// compute unit and 10 us, the keys shared out where that fills the last round
+// better, at the price of a second launch and of the shares' traffic; against
+// 0.79 us a SIMD for 32 keys and 32 rows of a wave, and 7 us a round.  Measured,
+// together and apart, 8 query heads a K/V head: 1024 tokens over 16384 keys 510
+// and 783 us, 512 tokens 304 and 401, 1000 under a window of 4096 156 and 223,
+// 1100 under one of 512 77 and 108, 128 under one of 1024 37 and 18, 256 over
+// 2048 52 and 39, 16 tokens of 32 requests over 4096 115 and 128, 4 tokens of
+// them 106 and 41.
+//
+// Otherwise the 8 waves of a workgroup take the same keys of
 // several K/V heads where the workgroups that leaves still fill whole rounds of
 // the compute units (one at a time fits one): 1000 rows over a window of 4096
 // 264 us with one head, 239, 221 and 219 us with 2, 4 and 8; 1024 causal rows
@@ -217,6 +242,26 @@ Mx4Plan plan_mx4_attend(int n_requests, int q_len, int64_t max_keys, bool select
     p.mt = n_m > 16 ? 2 : 1;
     p.m_tiles = (int)((n_m + 16 * p.mt - 1) / (16 * p.mt));
     p.hp = n_m <= 8 && n_kv % 2 == 0 && head_dim <= 128 && (int64_t)p.units * (n_kv / 2) >= 2 * kCus ? 2 : 1;
+    p.head_group = 1;
+    if (!selected && head_dim <= 128 && n_m > 32) {
+        const int64_t tiles = (n_m + 255) / 256, items = (int64_t)p.units * tiles * n_kv;
+        const double steps = (double)max_keys / 64, fill = (double)n_m / (double)(tiles * 256);
+        const double a_step = 2.05 * (0.76 + 0.24 * fill) * head_dim / 128;
+        const int64_t apart = (int64_t)p.units * ((n_m + 31) / 32) * n_kv;  // workgroups of 32 rows
+        double best = 0.79 / (4 * kCus) * (double)apart * ((double)max_keys / 32) * head_dim / 128 +
+                      7.0 * (double)((apart + kCus - 1) / kCus);
+        for (int s = 1; s <= 16; ++s) {
+            const double rounds = (double)((items * s + kCus - 1) / kCus);
+            double t = 10.0 + rounds * ceil(steps / s) * a_step;
+            if (s > 1) t += 5.0 + (double)rows * n_heads * s * head_dim * 8 / 4.5e6;
+            if (t >= best) continue;
+            best = t;
+            p.prompt = true;
+            p.n_splits = s;
+            p.m_tiles = (int)tiles;
+        }
+        if (p.prompt) return sized(p, rows, n_heads, n_kv, head_dim);
+    }
     const int waves = head_dim <= 128 && p.hp == 1 ? 8 : 4;
     const int64_t items = (int64_t)p.units * p.m_tiles * (n_kv / p.hp);
     const int64_t most = (max_keys + 32 * waves - 1) / (32 * waves);
@@ -226,20 +271,12 @@ Mx4Plan plan_mx4_attend(int n_requests, int q_len, int64_t max_keys, bool select
     // most: tiles of a wave that has a row's keys to itself
     if (splits < 1 || most * (splits - 1) < 4 * splits) splits = 1;
     p.n_splits = (int)splits;
-    p.head_group = 1;
     if (!selected && p.mt == 2 && waves == 8 && splits == 1)
         for (int g = 8; g > 1 && p.head_group == 1; g /= 2) {
             const int64_t wgs = items / g, rounds = (wgs + kCus - 1) / kCus;
             if (n_kv % g == 0 && 10 * wgs >= 9 * rounds * kCus) p.head_group = g;
         }
-    const int64_t pieces = (int64_t)p.units * p.m_tiles * p.n_splits;
-    p.workgroups = (pieces + 7) / 8 * 8 * (n_kv / (p.hp * p.head_group));
-    if (p.n_splits > 1) {
-        const size_t parts = (size_t)rows * n_heads * p.n_splits;
-        p.part_o_bytes = (parts * head_dim * 4 + 255) / 256 * 256;
-        p.workspace_bytes = p.part_o_bytes + (parts * 8 + 255) / 256 * 256;
-    }
-    return p;
+    return sized(p, rows, n_heads, n_kv, head_dim);
 }
 
 }  // namespace lidx

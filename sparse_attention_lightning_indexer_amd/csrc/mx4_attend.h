@@ -683,6 +683,309 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
     }
 }
 
+// Many query rows of a request at one K/V head (a prompt's, or a chunk's) under
+// a window: 256 rows a workgroup, 32 a wave, and the workgroup goes through the
+// keys together, 64 at a time.  Each key is converted once for the 256 rows: a
+// thread converts 32 values of K or of V and stores them to LDS in the query's
+// type, where every wave reads the tile as the products' operand (V transposed,
+// as above).  Converting in every wave was 64 of the about 200 vector
+// instructions a wave spent on 32 rows and 32 keys, against 32 products.
+//
+// Two buffers, one barrier a step: after it a thread converts its part of the
+// next step into the other buffer, asks for the codes of the step after and the
+// page id of the one after that, and the wave multiplies.  A wave passes over
+// steps that none of its rows sees.  The maximum is looked for only where the
+// weights' sum says that the reference is too low (a weight past about 2^8), or
+// no key was seen yet; otherwise weights cost one multiply-add, one exponential
+// and one addition each.
+//
+// Per key of a buffer a word says what is unusual: bit 31 a page outside the
+// cache, bits 0-7 blocks of V that are NaN (stored as zeros; the rows that see
+// the key get their NaN at the end).
+template <int D>
+struct PromptShape {
+    static constexpr int MT = 2, W = 8, KEYS = 64, ROWS = W * 16 * MT;
+    static constexpr int ROW = 2 * D + 32;
+    static constexpr int BUFFER = 2 * KEYS * ROW;  // K, then V
+};
+
+template <bool BF16, int D>
+__global__ void __launch_bounds__(512, 2) mx4_prompt_kernel(Mx4Attend a) {
+    using T = Type<BF16>;
+    using P = PromptShape<D>;
+    typedef typename T::vec8 vec8;
+    constexpr int KS = D / 32, NT = D / 16, MT = P::MT, KEYS = P::KEYS, ROW = P::ROW;
+    __shared__ __attribute__((aligned(16))) unsigned char smem[2 * P::BUFFER];
+    __shared__ uint32_t unusual[2][KEYS];
+    __shared__ __attribute__((aligned(16))) uint32_t any[2][4];
+
+    Item it = item_of(a, P::ROWS / 16, 1);
+    if (it.unit >= a.units) return;
+    it.m0 = (a.m_tiles - 1) * P::ROWS - it.m0;  // the rows with the most keys first
+    const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
+    const int col = lane & 15, qd = lane >> 4;
+    const int req = it.unit, seq = a.seq_lens[req];
+    const int n_m = a.q_len * a.group;
+    auto token_in = [&](int m) { return (int)quotient((uint32_t)m, a.div_group); };  // of the request
+    auto seen_of = [&](int m) { return (int64_t)seq - a.q_len + 1 + token_in(min(m, n_m - 1)); };
+    auto capped = [&](int64_t v) { return (int)max((int64_t)0, min(v, (int64_t)a.max_seq_len)); };
+
+    // the workgroup's keys: steps of 64, the first tokens and then the window
+    const int64_t first_seen = seen_of(it.m0);
+    const int cap_last = capped(seen_of(it.m0 + P::ROWS - 1));
+    const int64_t lo = a.window ? first_seen - a.window : 0;
+    const int base = lo > 0 ? (int)min(lo, (int64_t)cap_last) & ~(KEYS - 1) : 0;
+    const int sink_steps = a.window ? (min(a.sinks, base) + KEYS - 1) / KEYS : 0;
+    int n_steps = sink_steps + (cap_last - base + KEYS - 1) / KEYS;
+    if (a.pages.n_blocks == 0) n_steps = 0;
+    const int per = (n_steps + a.n_splits - 1) / a.n_splits;
+    const int s_begin = it.split * per, s_end = min(n_steps, s_begin + per);
+    auto start_of = [&](int step) { return step < sink_steps ? step * KEYS : base + (step - sink_steps) * KEYS; };
+
+    // the wave's rows
+    const int m0 = it.m0 + wave * 16 * MT;
+    const int cap_first_w = capped(seen_of(m0));
+    const int cap_last_w = m0 < n_m ? capped(seen_of(m0 + 16 * MT - 1)) : 0;
+    const int64_t first_w = seen_of(m0) - a.window, last_w = seen_of(m0 + 16 * MT - 1) - a.window;
+    vec8 q[MT][KS];
+    int row_end[MT], row_start[MT];
+    float mx[MT], ls[MT];
+    f32x4 o[MT][NT];
+    uint32_t nan_blocks[MT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        const int m = min(m0 + mt * 16 + col, n_m - 1), t = token_in(m);
+        const uint4 *src = reinterpret_cast<const uint4 *>(
+            (const uint16_t *)a.q + (int64_t)(req * a.q_len + t) * a.q_st +
+            (int64_t)(it.kv * a.group + m - t * a.group) * a.q_sh + qd * 8);
+#pragma unroll
+        for (int st = 0; st < KS; ++st) q[mt][st] = __builtin_bit_cast(vec8, src[st * 4]);
+        const int64_t seen = seen_of(m);
+        row_end[mt] = capped(seen);
+        row_start[mt] = a.window ? (int)min(max((int64_t)0, seen - a.window), (int64_t)row_end[mt]) : 0;
+        mx[mt] = kNegInf;
+        ls[mt] = 0.0f;
+        nan_blocks[mt] = 0u;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) o[mt][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+
+    // the thread's part of a step: quarter ch of one key's K (waves 0-3) or V
+    const bool is_v = wave >= 4;
+    const int key = (threadIdx.x & 255) >> 2, ch = lane & 3;
+    constexpr int NB = KS % 4 == 0 ? KS / 4 : (KS == 2 ? 1 : 2);
+    constexpr int ALIGN = KS % 4 == 0 ? 16 : (KS % 2 == 0 ? 8 : 4);
+    const int blk0 = ch * KS / 4;
+    const uint8_t *src_d = (is_v ? a.vd : a.kd) + (uint64_t)((uint32_t)it.kv * (uint32_t)a.pages.d_sh);
+    const uint8_t *src_s = (is_v ? a.vs : a.ks) + (uint64_t)((uint32_t)it.kv * (uint32_t)a.pages.s_sh);
+    const int32_t *table = a.block_table + (int64_t)req * a.bt_stride;
+    uint32_t code[KS], sc[NB];
+    bool seen_key = false, bad_page = false;
+    // position of the thread's key in a step; -1 past the end
+    auto position = [&](int step) {
+        const int64_t p = (int64_t)start_of(step) + key;
+        return step < s_end && p < cap_last ? (int)p : -1;
+    };
+    auto load_page = [&](int p) -> int { return table[quotient((uint32_t)max(p, 0), a.pages.div_bs)]; };
+    auto load_codes = [&](int p, int page) {
+        const bool in = (uint32_t)page < (uint32_t)a.pages.n_blocks;
+        seen_key = p >= 0 && in;
+        bad_page = p >= 0 && !in;
+        const uint32_t r = (uint32_t)max(p, 0);
+        const uint32_t off = r - __umul24(quotient(r, a.pages.div_bs), (uint32_t)a.pages.block_size);
+        const uint32_t at = seen_key ? off : 0u, pg = seen_key ? (uint32_t)page : 0u;
+        const uint64_t d = (uint64_t)pg * (uint32_t)a.pages.d_sb + __umul24(at, (uint32_t)a.pages.d_ss) + ch * KS * 4;
+        const uint64_t sb = (uint64_t)pg * (uint32_t)a.pages.s_sb + __umul24(at, (uint32_t)a.pages.s_ss);
+        __builtin_memcpy(code, __builtin_assume_aligned(src_d + d, ALIGN), KS * 4);
+#pragma unroll
+        for (int n = 0; n < NB; ++n) sc[n] = src_s[sb + (uint32_t)min(blk0 + n, D / 32 - 1)];
+    };
+    typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+    typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
+    auto store_step = [&](int buf) {
+        uint32_t word = bad_page ? 0x80000000u : 0u;
+        if (is_v) {
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+                const bool nan = sc[n] == 255u;
+                if (seen_key && nan) word |= 1u << min(blk0 + n, D / 32 - 1);
+                if (!seen_key || nan) sc[n] = 0u;
+            }
+            word |= (uint32_t)dpp_move<0xb1>(0, (int)word);
+            word |= (uint32_t)dpp_move<0x4e>(0, (int)word);
+            if (ch == 0) unusual[buf][key] = word;
+            const bool some = __ballot(word != 0u) != 0;
+            if (lane == 0) any[buf][wave - 4] = some;
+        }
+        lds_u8 *dst = (lds_u8 *)smem + buf * P::BUFFER + (is_v ? KEYS * ROW : 0) + key * ROW;
+#pragma unroll
+        for (int st = 0; st < KS; ++st) {
+            uint32_t b = sc[0];
+#pragma unroll
+            for (int n = 1; n < NB; ++n) b = (ch * KS + st) / 4 - blk0 == n ? sc[n] : b;
+            const vec8 v = T::from4(code[st], __builtin_bit_cast(float, b << 23));
+            *(lds_u32x4 *)(dst + (ch * KS + st) * 16) = __builtin_bit_cast(u32x4, v);
+        }
+    };
+
+    int pos = -1, page = -1;
+    if (s_begin < s_end) {
+        pos = position(s_begin);
+        page = load_page(pos);
+        load_codes(pos, page);
+        pos = position(s_begin + 1);
+        page = load_page(pos);
+        store_step(0);
+        load_codes(pos, page);
+        pos = position(s_begin + 2);
+        page = load_page(pos);
+    }
+    for (int step = s_begin; step < s_end; ++step) {
+        const int buf = (step - s_begin) & 1;
+        lds_barrier();
+        if (step + 1 < s_end) {
+            store_step(buf ^ 1);
+            load_codes(pos, page);
+            pos = position(step + 3);
+            page = load_page(pos);
+        }
+        const int p0 = start_of(step);
+        // none of the wave's rows sees a key of this step
+        if (p0 >= cap_last_w || (a.window && p0 + KEYS <= first_w && p0 >= a.sinks)) continue;
+        const lds_u8 *kb = (const lds_u8 *)smem + buf * P::BUFFER;
+        const uint32_t odd = any[buf][0] | any[buf][1] | any[buf][2] | any[buf][3];
+        const bool strange = uni((int)odd) != 0;
+        const bool whole = !strange && p0 + KEYS <= cap_first_w &&
+                           (!a.window || p0 + KEYS <= a.sinks || (int64_t)p0 >= last_w);
+        auto counts = [&](int mt, int k) -> bool {
+            const int p = p0 + k;
+            return p < row_end[mt] && (p >= row_start[mt] || p < a.sinks) && !(unusual[buf][k] >> 31);
+        };
+        if (strange) {
+            for (int k = 0; k < KEYS; ++k) {
+                const uint32_t word = unusual[buf][k];
+                if (!(word & 0xffu)) continue;
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+                    if (counts(mt, k)) nan_blocks[mt] |= word & 0xffu;
+            }
+        }
+
+        // scores
+        f32x4 s[MT][4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) s[mt][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int st = 0; st < KS; ++st) {
+                const u32x4 w = *(const lds_u32x4 *)(kb + (u * 16 + col) * ROW + (st * 4 + qd) * 16);
+                const vec8 kv = __builtin_bit_cast(vec8, w);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) s[mt][u] = T::mfma(kv, q[mt][st], s[mt][u]);
+            }
+        }
+        if (!whole) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        s[mt][u][i] = counts(mt, u * 16 + 4 * qd + i) ? s[mt][u][i] : kNegInf;
+        }
+
+        // softmax
+        vec8 p[MT][2];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            auto weigh = [&]() {
+                const float sub = mx[mt] == kNegInf ? 0.0f : mx[mt];
+                float sum = 0.0f;
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[mt][u][i], a.scale_log2, -sub));
+                        sum += e;
+                        p[mt][u >> 1][(u & 1) * 4 + i] = (typename T::one)e;
+                    }
+                return sum;
+            };
+            float sum = weigh();
+            if (__ballot(sum > 256.0f || mx[mt] == kNegInf)) {
+                float top = s[mt][0][0];
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) top = larger(top, s[mt][u][i]);
+                const float m_new = larger(mx[mt], quarter_max(top) * a.scale_log2);
+                const float f = m_new > mx[mt] ? __builtin_amdgcn_exp2f(mx[mt] - m_new) : 1.0f;
+                mx[mt] = m_new;
+                ls[mt] *= f;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[mt][n][i] *= f;
+                sum = weigh();
+            }
+            ls[mt] += sum;
+        }
+
+        // O^T += V^T P^T
+        const lds_u8 *vb = kb + KEYS * ROW + (4 * qd + (col >> 2)) * ROW + (col & 3) * 8;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                union {
+                    s16x4 h[2];
+                    vec8 v;
+                } vt;
+                vt.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(vb + h * 32 * ROW + n * 32));
+                vt.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(vb + (h * 32 + 16) * ROW + n * 32));
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) o[mt][n] = T::mfma(vt.v, p[mt][h], o[mt][n]);
+            }
+    }
+
+    // a lane has 4 consecutive outputs of its row in each 16
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        const int m = m0 + mt * 16 + col;
+        const float l = quarter_sum(ls[mt]);
+        if (m >= n_m) continue;
+        const int t = token_in(m), token = req * a.q_len + t, head = it.kv * a.group + m - t * a.group;
+        const int64_t th = (int64_t)token * a.n_heads + head;
+        const float inv = a.n_splits > 1 ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            f32x4 v = o[mt][n];
+            if ((nan_blocks[mt] >> (n / 2)) & 1u) v = f32x4{NAN, NAN, NAN, NAN};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] *= inv;
+            if (a.n_splits > 1) {
+                *reinterpret_cast<f32x4 *>(a.part_o + (th * a.n_splits + it.split) * D + n * 16 + qd * 4) = v;
+            } else {
+                typename T::one r[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) r[i] = (typename T::one)v[i];
+                uint2 w;
+                __builtin_memcpy(&w, r, 8);
+                *reinterpret_cast<uint2 *>((uint16_t *)a.out + (int64_t)token * a.out_st + (int64_t)head * a.out_sh +
+                                           n * 16 + qd * 4) = w;
+            }
+        }
+        if (qd) continue;
+        if (a.n_splits > 1) {
+            a.part_ml[(th * a.n_splits + it.split) * 2] = mx[mt];
+            a.part_ml[(th * a.n_splits + it.split) * 2 + 1] = l;
+        } else if (a.lse) {
+            a.lse[th] = l == 0.0f ? kNegInf : (mx[mt] + log2f(l)) * 0.69314718055994530942f;
+        }
+    }
+}
+
 // Joins the shares of rows whose keys were split (at most kMx4MaxSplits): a workgroup per
 // query row and head.  Threads take 4 outputs of every 1024 / D-th share, so
 // the loads of a row's shares overlap, and add up through LDS.
@@ -759,6 +1062,14 @@ hipError_t launch_tiles(const Mx4Attend &a, const Mx4Plan &p, hipStream_t stream
 template <bool BF16, int D>
 hipError_t launch_dim(const Mx4Attend &a, const Mx4Plan &p, hipStream_t stream) {
     if constexpr (D <= 128) {
+        if (p.prompt) {
+            hipLaunchKernelGGL((mx4_prompt_kernel<BF16, D>), dim3((unsigned)p.workgroups), dim3(512), 0, stream, a);
+            hipError_t e = hipGetLastError();
+            if (e != hipSuccess || a.n_splits == 1) return e;
+            hipLaunchKernelGGL((mx4_join_kernel<BF16, D>), dim3((unsigned)(a.rows * a.n_heads)), dim3(256), 0, stream,
+                               a);
+            return hipGetLastError();
+        }
         if (p.hp == 2) return launch_tiles<BF16, D, 1, 2>(a, p, stream);
     }
     if (p.mt == 1) return launch_tiles<BF16, D, 1, 1>(a, p, stream);

@@ -425,6 +425,103 @@ def test_groups_of_heads(requests, kv, kind):
             assert float((z - lse[8 * a:8 * b])[fine].abs().max()) <= 2.0**-12
 
 
+def check_many(case, window, sinks, where, sample, step=1):
+    """A call of many rows: `sample` of them against the plain form, and all
+    against calls of `step` requests, whose rows another kernel may take."""
+    args = case.args()
+    q, kd, ks, vd, vs, table, sl, Q = args
+    out, lse = li.mx4_attend_window(*args, case.max_seq_len, case.sm_scale, window=window, sinks=sinks)
+    few = set(sample.tolist())
+    want = case.want(lambda t, v, e: plain.positions_window(v, e, window, sinks) if t in few else [])
+    pick = torch.from_numpy(sample).to(DEV)
+    o, z, b = want
+    b = {k: v[sample] for k, v in b.items()}
+    check((out[pick], lse[pick]), (o[sample], z[sample], b), case.kind, case.d, where)
+    for a in range(0, len(case.lens), step):
+        rows = slice(Q * a, Q * min(a + step, len(case.lens)))
+        o, z = li.mx4_attend_window(q[rows], kd, ks, vd, vs, table[a:a + step], sl[a:a + step], Q, case.max_seq_len,
+                                    case.sm_scale, window=window, sinks=sinks)
+        assert torch.equal(torch.isnan(o), torch.isnan(out[rows])), where
+        # each is within 3 roundings of the exact value and 2^-12 for the f32 sums, of at most the largest |V|, 6 * 2
+        far = float((o.float() - out[rows].float()).nan_to_num(nan=0.0).abs().max())
+        assert far <= 2 * (3 * UNIT[case.kind] + 2.0**-12) * 12, (where, a, far)
+        fine = torch.isfinite(z)
+        assert torch.equal(fine, torch.isfinite(lse[rows])) and torch.equal(torch.isnan(z), torch.isnan(lse[rows])), where
+        assert float((z - lse[rows])[fine].abs().max() if fine.any() else 0.0) <= 2.0**-12, where
+    return out, lse
+
+
+# Sizes at which a workgroup goes through the keys together: 16 requests of 256
+# query rows at each of 8 K/V heads
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("query,group,d,bs", [(32, 8, 64, 16), (37, 7, 96, 7), (64, 4, 128, 64), (130, 2, 64, 33)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1, 0), (70, 3), (64, 200), (200, 64), (4000, 9)])
+def test_prompt_rows(query, group, d, bs, window, sinks, kind):
+    rng = np.random.default_rng(query)
+    lens = [0, 1, query - 1, query, 64, 65, 128, 129] + rng.integers(1, 330, 8).tolist()
+    case = Case(42, lens, query, 8 * group, 8, d, bs, kind)
+    sample = np.sort(rng.permutation(16 * query)[:40])
+    check_many(case, window, sinks, f"prompt {query} {group} {d} {window}+{sinks} {kind}", sample, step=4)
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+def test_prompt_rows_share_keys_out(kind):
+    """Rows whose keys several workgroups share (a long context, few rows), against the plain form."""
+    case = Case(45, [9000], 650, 16, 8, 64, 64, kind)
+    check_many(case, 0, 0, f"prompt shares {kind}", np.array([0, 77, 649]))
+    check_many(case, 8000, 30, f"prompt shares, window {kind}", np.array([0, 300, 649]))
+    # the same rows, 13 to a call, whose keys a wave shares out by itself
+    q, kd, ks, vd, vs, table, sl, Q = case.args()
+    whole, z = li.mx4_attend_window(q, kd, ks, vd, vs, table, sl, Q, 9000, case.sm_scale)
+    for a in (0, 325, 637):
+        some = torch.tensor([9000 - 650 + a + 13], dtype=torch.int32, device=DEV)
+        o, y = li.mx4_attend_window(q[a:a + 13], kd, ks, vd, vs, table, some, 13, 9000, case.sm_scale)
+        assert float((o.float() - whole[a:a + 13].float()).abs().max()) <= 2 * (3 * UNIT[kind] + 2.0**-12) * 12
+        assert float((y - z[a:a + 13]).abs().max()) <= 2.0**-12
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+def test_prompt_rows_with_bad_pages_and_nan(kind):
+    rng = np.random.default_rng(43)
+    lens = [400, 170] + rng.integers(64, 330, 14).tolist()
+    case = Case(43, lens, 64, 32, 8, 128, 16, kind)
+    sample = np.concatenate([np.arange(0, 128, 9), rng.permutation(896)[:20] + 128])
+    case.table[0, 3], case.table[0, 20], case.table[1, 2] = -1, case.n_blocks, 2**30
+    check_many(case, 0, 0, "prompt, bad pages", sample, 4)
+    check_many(case, 90, 60, "prompt, bad pages, window", sample, 4)
+    for r in range(16):                                       # behind the last key
+        for p in range(int(case.lens[r]), case.table.shape[1] * 16):
+            page = case.table[r, p // 16]
+            if 0 <= page < case.n_blocks:
+                for s in case.scale:
+                    s[page, p % 16] = 255
+    out, _ = check_many(case, 0, 0, "prompt, NaN behind the last key", sample, 4)
+    assert not torch.isnan(out).any()
+    for which, p, head, block in ((1, 390, 0, 3), (1, 100, 1, 0), (0, 370, 1, 2)):
+        case.scale[which][case.table[0, p // 16], p % 16, head, block] = 255
+    out, lse = check_many(case, 100, 7, "prompt, NaN, window", sample, 4)
+    # V at 390: queries 54 on (query j's last key is 336 + j), first K/V head, dimensions 96-127
+    assert torch.isnan(out[54:64, :4, 96:]).all() and not torch.isnan(out[:54, :4]).any()
+    assert not torch.isnan(out[54:64, :4, :96]).any() and torch.isnan(lse[34:64, 4:8]).all()
+    assert not torch.isnan(out[64:]).any() and not torch.isnan(out[:64, 8:]).any()
+    check_many(case, 0, 0, "prompt, NaN", sample, 4)
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+def test_prompt_rows_of_large_scores(kind):
+    rng = np.random.default_rng(44)
+    case = Case(44, rng.integers(64, 400, 16).tolist(), 64, 32, 8, 128, 16, kind, spread=40.0)
+    sample = np.sort(rng.permutation(1024)[:40])
+    for window, sinks in ((0, 0), (150, 5)):
+        out, lse = li.mx4_attend_window(*case.args(), case.max_seq_len, case.sm_scale, window=window, sinks=sinks)
+        few = set(sample.tolist())
+        o, z, b = case.want(lambda t, v, e: plain.positions_window(v, e, window, sinks) if t in few else [])
+        pick = torch.from_numpy(sample).to(DEV)
+        check((out[pick], lse[pick]), (o[sample], z[sample], {k: v[sample] for k, v in b.items()}), kind, 128,
+              f"prompt, large {window} {kind}")
+        case.max_seq_len = 250
+
+
 @pytest.mark.parametrize("kind", ["f16", "bf16"])
 def test_large_scores(kind):
     """Scores in the hundreds: one key takes nearly all the weight, maxima rise through the row."""

@@ -56,11 +56,22 @@ typedef enum {
 } indexer_mx4_type;
 
 /*
+ * These entry points take their arguments in a structure (every member set; no
+ * padding between members), which the call reads and does not keep.
+ */
+
+/* Byte strides of the cache's block, slot and head, for data and for scale. */
+typedef struct {
+    int64_t data_block, data_slot, data_head;
+    int64_t scale_block, scale_slot, scale_head;
+} indexer_mx4_strides;
+
+/*
  * indexer_mx4_cache_write -- quantise rows into the cache as they come.
  *
  *   k, v         [n_tokens][n_heads][head_dim] of `type`, strides in elements
  *                (multiples of 8), 16-byte aligned; v NULL: k alone (then the
- *                v arguments are not used)
+ *                v members are not used)
  *   slots        i64 [n_tokens], 8-byte aligned: token t goes to slot
  *                slots[t]; one that is negative or past the cache is skipped
  *                (padding of a batch).  Slots that are not skipped are
@@ -68,18 +79,21 @@ typedef enum {
  *   k_data ...   the cache; K and V have the same strides.  Other slots keep
  *                their bytes.
  *
- * n_heads >= 1; head_dim a multiple of 32 in [32, 1024].
+ * n_heads in [1, 1024]; head_dim a multiple of 32 in [32, 1024].
  */
-indexer_status indexer_mx4_cache_write(
-    const void *k, int64_t k_stride_t, int64_t k_stride_h,
-    const void *v, int64_t v_stride_t, int64_t v_stride_h,
-    int32_t type, int32_t n_tokens, int32_t n_heads, int32_t head_dim,
-    const int64_t *slots,
-    void *k_data, void *k_scale, void *v_data, void *v_scale,
-    int32_t n_blocks, int32_t block_size,
-    int64_t data_stride_b, int64_t data_stride_s, int64_t data_stride_h,
-    int64_t scale_stride_b, int64_t scale_stride_s, int64_t scale_stride_h,
-    void *stream);
+typedef struct {
+    const void *k;
+    int64_t k_stride_t, k_stride_h;
+    const void *v;
+    int64_t v_stride_t, v_stride_h;
+    const int64_t *slots;
+    void *k_data, *k_scale, *v_data, *v_scale;
+    indexer_mx4_strides strides;
+    void *stream;
+    int32_t type, n_tokens, n_heads, head_dim, n_blocks, block_size;
+} indexer_mx4_write_args;
+
+indexer_status indexer_mx4_cache_write(const indexer_mx4_write_args *args);
 
 /*
  * indexer_mx4_cache_read -- rows of one of the two caches as numbers.
@@ -92,14 +106,17 @@ indexer_status indexer_mx4_cache_write(
  *
  * Shapes as in indexer_mx4_cache_write.
  */
-indexer_status indexer_mx4_cache_read(
-    const void *data, const void *scale,
-    int32_t n_blocks, int32_t block_size,
-    int64_t data_stride_b, int64_t data_stride_s, int64_t data_stride_h,
-    int64_t scale_stride_b, int64_t scale_stride_s, int64_t scale_stride_h,
-    const int64_t *slots, int32_t n_rows, int32_t n_heads, int32_t head_dim,
-    void *out, int64_t out_stride_t, int64_t out_stride_h, int32_t type,
-    void *stream);
+typedef struct {
+    const void *data, *scale;
+    indexer_mx4_strides strides;
+    const int64_t *slots;
+    void *out;
+    int64_t out_stride_t, out_stride_h;
+    void *stream;
+    int32_t type, n_rows, n_heads, head_dim, n_blocks, block_size;
+} indexer_mx4_read_args;
+
+indexer_status indexer_mx4_cache_read(const indexer_mx4_read_args *args);
 
 /*
  * indexer_mx4_attend_selected -- attention of each query row to the keys its
@@ -120,6 +137,12 @@ indexer_status indexer_mx4_cache_read(
  *
  * A row with no position has out 0 and lse -inf.
  *
+ * indexer_mx4_attend_window -- the same attention to a sliding window and the
+ * first tokens: with v = seq_lens[r] - query_len + 1 + j, row r*query_len + j
+ * attends to the positions p < min(v, max_seq_len) that have
+ *   p >= v - window  or  p < sinks        (window >= 1), or
+ *   any p                                  (window = 0: plain causal).
+ *
  *   q            [n_requests*query_len][n_heads][head_dim] of `type` (strides
  *                in elements, multiples of 8; 16-byte aligned).  The cached
  *                values enter the products in this type: exact for a cache
@@ -128,54 +151,47 @@ indexer_status indexer_mx4_cache_read(
  *                product with V.
  *   block_table  i32 [n_requests][bt_stride], pages of each request; entries
  *                of the first ceil(max_seq_len / block_size) columns are read
- *                where a position needs them
- *   idx          i32 [n_requests*query_len][idx_stride], the first n_sel used
+ *                where a position needs them (and the first of each row)
  *   out          like q (strides multiples of 8, 16-byte aligned), not
  *                overlapping any input
  *   lse          f32 [n_requests*query_len][n_heads], contiguous, or NULL
  *   workspace    indexer_mx4_attend_workspace_bytes(...) bytes, 256-byte
  *                aligned; NULL when that is 0
+ *   idx          selected: i32 [n_requests*query_len][idx_stride], the first
+ *                n_sel of a row used
  *
- * head_dim 64, 96, 128, 192 or 256; n_heads a multiple of n_kv_heads;
- * sm_scale positive and finite; pool_size in [1, 8192]; n_sel * pool_size
- * below 2^31.  n_requests = 0 enqueues nothing; n_sel = 0 writes the empty
- * rows' values.
+ * The members from idx to pool_size belong to the selected form, window and
+ * sinks to the other; each form ignores the other's.
+ *
+ * head_dim 64, 96, 128, 192 or 256; n_heads (at most 1024) a multiple of
+ * n_kv_heads; sm_scale positive and finite; pool_size in [1, 8192];
+ * max_seq_len and n_sel * pool_size at most 2^31 - 1024; window, sinks >= 0.
+ * n_requests = 0 enqueues nothing; n_sel = 0 writes the empty rows' values.
  */
-indexer_status indexer_mx4_attend_selected(
-    const void *q, int64_t q_stride_t, int64_t q_stride_h, int32_t type,
-    const void *k_data, const void *k_scale, const void *v_data, const void *v_scale,
-    int32_t n_blocks, int32_t block_size,
-    int64_t data_stride_b, int64_t data_stride_s, int64_t data_stride_h,
-    int64_t scale_stride_b, int64_t scale_stride_s, int64_t scale_stride_h,
-    const int32_t *block_table, int64_t bt_stride, const int32_t *seq_lens,
-    int32_t n_requests, int32_t query_len, int32_t max_seq_len,
-    int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, float sm_scale,
-    const int32_t *idx, int64_t idx_stride, int32_t n_sel, int32_t pool_size,
-    void *out, int64_t out_stride_t, int64_t out_stride_h, float *lse,
-    void *workspace, size_t workspace_bytes,
-    void *stream);
+typedef struct {
+    const void *q;
+    int64_t q_stride_t, q_stride_h;
+    const void *k_data, *k_scale, *v_data, *v_scale;
+    indexer_mx4_strides strides;
+    const int32_t *block_table;
+    int64_t bt_stride;
+    const int32_t *seq_lens;
+    void *out;
+    int64_t out_stride_t, out_stride_h;
+    float *lse;
+    void *workspace;
+    size_t workspace_bytes;
+    void *stream;
+    const int32_t *idx;
+    int64_t idx_stride;
+    int32_t n_sel, pool_size;
+    int32_t window, sinks;
+    int32_t type, n_blocks, block_size, n_requests, query_len, max_seq_len, n_heads, n_kv_heads, head_dim;
+    float sm_scale;
+} indexer_mx4_attend_args;
 
-/*
- * indexer_mx4_attend_window -- the same attention to a sliding window and the
- * first tokens: with v = seq_lens[r] - query_len + 1 + j, row r*query_len + j
- * attends to the positions p < min(v, max_seq_len) that have
- *   p >= v - window  or  p < sinks        (window >= 1), or
- *   any p                                  (window = 0: plain causal).
- * window, sinks >= 0; the other arguments as above.
- */
-indexer_status indexer_mx4_attend_window(
-    const void *q, int64_t q_stride_t, int64_t q_stride_h, int32_t type,
-    const void *k_data, const void *k_scale, const void *v_data, const void *v_scale,
-    int32_t n_blocks, int32_t block_size,
-    int64_t data_stride_b, int64_t data_stride_s, int64_t data_stride_h,
-    int64_t scale_stride_b, int64_t scale_stride_s, int64_t scale_stride_h,
-    const int32_t *block_table, int64_t bt_stride, const int32_t *seq_lens,
-    int32_t n_requests, int32_t query_len, int32_t max_seq_len,
-    int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, float sm_scale,
-    int32_t window, int32_t sinks,
-    void *out, int64_t out_stride_t, int64_t out_stride_h, float *lse,
-    void *workspace, size_t workspace_bytes,
-    void *stream);
+indexer_status indexer_mx4_attend_selected(const indexer_mx4_attend_args *args);
+indexer_status indexer_mx4_attend_window(const indexer_mx4_attend_args *args);
 
 /*
  * Bytes of workspace an attention call needs (0 if none): the partial results

@@ -13,6 +13,10 @@ using lidx::api_error;
 
 bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
+static_assert(sizeof(indexer_mx4_write_args) == 18 * 8 + 6 * 4 && sizeof(indexer_mx4_read_args) == 13 * 8 + 6 * 4 &&
+                  sizeof(indexer_mx4_attend_args) == 25 * 8 + 14 * 4,
+              "members without padding: the binding packs them");
+
 constexpr int32_t kMaxKeys = INT32_MAX - 1023;  // room for positions of a last, partly filled tile
 
 #define MX4_FAIL(st, ...) return (indexer_status)api_error(st, __VA_ARGS__)
@@ -42,8 +46,9 @@ indexer_status check_rows(const char *name, const void *p, int64_t st, int64_t s
 
 // Strides of the pages: no two rows may share bytes along one dimension.
 indexer_status check_pages(int32_t n_blocks, int32_t block_size, int32_t n_heads, int32_t head_dim,
-                           int64_t d_sb, int64_t d_ss, int64_t d_sh, int64_t s_sb, int64_t s_ss, int64_t s_sh,
-                           lidx::Mx4Pages *out) {
+                           const indexer_mx4_strides &st, lidx::Mx4Pages *out) {
+    int64_t d_sb = st.data_block, d_ss = st.data_slot, d_sh = st.data_head;
+    int64_t s_sb = st.scale_block, s_ss = st.scale_slot, s_sh = st.scale_head;
     if (n_blocks < 0) MX4_FAIL(INDEXER_EINVAL, "n_blocks=%d must be >= 0", n_blocks);
     if (block_size < 1) MX4_FAIL(INDEXER_EINVAL, "block_size=%d must be >= 1", block_size);
     const int64_t row = head_dim / 2, srow = head_dim / 32;
@@ -89,82 +94,79 @@ bool attend_dim(int32_t d) { return d == 64 || d == 96 || d == 128 || d == 192 |
 
 // Everything the two attentions share; fills all of `a` but the selection or
 // window, and the launch fields.
-indexer_status check_attend(const void *q, int64_t q_st, int64_t q_sh, int32_t type, const void *kd, const void *ks,
-                            const void *vd, const void *vs, int32_t n_blocks, int32_t block_size, int64_t d_sb,
-                            int64_t d_ss, int64_t d_sh, int64_t s_sb, int64_t s_ss, int64_t s_sh,
-                            const int32_t *block_table, int64_t bt_stride, const int32_t *seq_lens,
-                            int32_t n_requests, int32_t query_len, int32_t max_seq_len, int32_t n_heads,
-                            int32_t n_kv, int32_t head_dim, float sm_scale, void *out, int64_t out_st,
-                            int64_t out_sh, float *lse, lidx::Mx4Attend *a) {
-    MX4_TRY(check_type(type));
-    if (n_requests < 0 || max_seq_len < 0)
-        MX4_FAIL(INDEXER_EINVAL, "n_requests=%d max_seq_len=%d must be >= 0", n_requests, max_seq_len);
-    if (query_len < 1) MX4_FAIL(INDEXER_EINVAL, "query_len=%d must be >= 1", query_len);
-    if (max_seq_len > kMaxKeys) MX4_FAIL(INDEXER_ENOTSUP, "max_seq_len=%d exceeds %d", max_seq_len, kMaxKeys);
-    if (n_heads < 1 || n_heads > lidx::kMaxHeads || n_kv < 1 || n_heads % n_kv || !attend_dim(head_dim))
+indexer_status check_attend(const indexer_mx4_attend_args &g, lidx::Mx4Attend *a) {
+    MX4_TRY(check_type(g.type));
+    if (g.n_requests < 0 || g.max_seq_len < 0)
+        MX4_FAIL(INDEXER_EINVAL, "n_requests=%d max_seq_len=%d must be >= 0", g.n_requests, g.max_seq_len);
+    if (g.query_len < 1) MX4_FAIL(INDEXER_EINVAL, "query_len=%d must be >= 1", g.query_len);
+    if (g.max_seq_len > kMaxKeys) MX4_FAIL(INDEXER_ENOTSUP, "max_seq_len=%d exceeds %d", g.max_seq_len, kMaxKeys);
+    if (g.n_heads < 1 || g.n_heads > lidx::kMaxHeads || g.n_kv_heads < 1 || g.n_heads % g.n_kv_heads ||
+        !attend_dim(g.head_dim))
         MX4_FAIL(INDEXER_ENOTSUP, "n_heads=%d n_kv_heads=%d head_dim=%d not supported (n_heads in 1..%d, a multiple of "
-                 "n_kv_heads; head_dim 64, 96, 128, 192 or 256)", n_heads, n_kv, head_dim, lidx::kMaxHeads);
-    if ((int64_t)n_requests * query_len * n_heads > INT32_MAX)
+                 "n_kv_heads; head_dim 64, 96, 128, 192 or 256)", g.n_heads, g.n_kv_heads, g.head_dim, lidx::kMaxHeads);
+    if ((int64_t)g.n_requests * g.query_len > INT32_MAX / g.n_heads)
         MX4_FAIL(INDEXER_EINVAL, "n_requests*query_len*n_heads exceeds the int32 range");
-    if (!(sm_scale > 0.0f) || !isfinite(sm_scale) || !isfinite(sm_scale * 1.44269504f))
-        MX4_FAIL(INDEXER_EINVAL, "sm_scale=%g must be positive and finite", (double)sm_scale);
+    if (!(g.sm_scale > 0.0f) || !isfinite(g.sm_scale) || !isfinite(g.sm_scale * 1.44269504f))
+        MX4_FAIL(INDEXER_EINVAL, "sm_scale=%g must be positive and finite", (double)g.sm_scale);
     lidx::Mx4Pages pages;
-    MX4_TRY(check_pages(n_blocks, block_size, n_kv, head_dim, d_sb, d_ss, d_sh, s_sb, s_ss, s_sh, &pages));
-    MX4_TRY(check_rows("q", q, q_st, q_sh, n_heads, head_dim));
-    MX4_TRY(check_rows("out", out, out_st, out_sh, n_heads, head_dim));
-    if (n_blocks > 0) {
-        MX4_TRY(check_cache("k", kd, ks));
-        MX4_TRY(check_cache("v", vd, vs));
+    MX4_TRY(check_pages(g.n_blocks, g.block_size, g.n_kv_heads, g.head_dim, g.strides, &pages));
+    MX4_TRY(check_rows("q", g.q, g.q_stride_t, g.q_stride_h, g.n_heads, g.head_dim));
+    MX4_TRY(check_rows("out", g.out, g.out_stride_t, g.out_stride_h, g.n_heads, g.head_dim));
+    if (g.n_blocks > 0) {
+        MX4_TRY(check_cache("k", g.k_data, g.k_scale));
+        MX4_TRY(check_cache("v", g.v_data, g.v_scale));
     }
-    if (!seq_lens) MX4_FAIL(INDEXER_EINVAL, "seq_lens is NULL");
-    if (!aligned(seq_lens, 4) || !aligned(block_table, 4))
+    if (!g.seq_lens) MX4_FAIL(INDEXER_EINVAL, "seq_lens is NULL");
+    if (!aligned(g.seq_lens, 4) || !aligned(g.block_table, 4))
         MX4_FAIL(INDEXER_EINVAL, "block_table and seq_lens must be 4-byte aligned");
-    if (lse && !aligned(lse, 4)) MX4_FAIL(INDEXER_EINVAL, "lse must be 4-byte aligned");
-    if (max_seq_len > 0) {
-        if (!block_table) MX4_FAIL(INDEXER_EINVAL, "block_table is NULL");
-        const int64_t need = ((int64_t)max_seq_len + block_size - 1) / block_size;
-        if (bt_stride < need)
-            MX4_FAIL(INDEXER_EINVAL, "bt_stride=%lld < ceil(max_seq_len/block_size)=%lld", (long long)bt_stride,
+    if (g.lse && !aligned(g.lse, 4)) MX4_FAIL(INDEXER_EINVAL, "lse must be 4-byte aligned");
+    if (g.max_seq_len > 0) {
+        if (!g.block_table) MX4_FAIL(INDEXER_EINVAL, "block_table is NULL");
+        const int64_t need = ((int64_t)g.max_seq_len + g.block_size - 1) / g.block_size;
+        if (g.bt_stride < need)
+            MX4_FAIL(INDEXER_EINVAL, "bt_stride=%lld < ceil(max_seq_len/block_size)=%lld", (long long)g.bt_stride,
                      (long long)need);
     }
     *a = lidx::Mx4Attend{};
-    a->q = q;
-    a->q_st = q_st;
-    a->q_sh = q_sh;
-    a->kd = (const uint8_t *)kd;
-    a->ks = (const uint8_t *)ks;
-    a->vd = (const uint8_t *)vd;
-    a->vs = (const uint8_t *)vs;
+    a->q = g.q;
+    a->q_st = g.q_stride_t;
+    a->q_sh = g.q_stride_h;
+    a->kd = (const uint8_t *)g.k_data;
+    a->ks = (const uint8_t *)g.k_scale;
+    a->vd = (const uint8_t *)g.v_data;
+    a->vs = (const uint8_t *)g.v_scale;
     a->pages = pages;
-    a->block_table = block_table;
-    a->bt_stride = bt_stride;
-    a->seq_lens = seq_lens;
-    a->n_requests = n_requests;
-    a->q_len = query_len;
-    a->max_seq_len = max_seq_len;
-    a->n_heads = n_heads;
-    a->n_kv = n_kv;
-    a->group = n_heads / n_kv;
-    a->scale_log2 = (float)((double)sm_scale * 1.4426950408889634);
-    a->out = out;
-    a->out_st = out_st;
-    a->out_sh = out_sh;
-    a->lse = lse;
-    a->rows = n_requests * query_len;
+    a->block_table = g.block_table;
+    a->bt_stride = g.bt_stride;
+    a->seq_lens = g.seq_lens;
+    a->n_requests = g.n_requests;
+    a->q_len = g.query_len;
+    a->max_seq_len = g.max_seq_len;
+    a->n_heads = g.n_heads;
+    a->n_kv = g.n_kv_heads;
+    a->group = g.n_heads / g.n_kv_heads;
+    a->scale_log2 = (float)((double)g.sm_scale * 1.4426950408889634);
+    a->out = g.out;
+    a->out_st = g.out_stride_t;
+    a->out_sh = g.out_stride_h;
+    a->lse = g.lse;
+    a->rows = g.n_requests * g.query_len;
     a->div_group = lidx::fast_div((uint32_t)a->group);
     a->div_pool = lidx::fast_div(1);
     return INDEXER_OK;
 }
 
-indexer_status run_attend(lidx::Mx4Attend &a, int32_t type, int32_t head_dim, int64_t max_keys, void *workspace,
-                          size_t workspace_bytes, hipStream_t stream) {
+indexer_status run_attend(lidx::Mx4Attend &a, const indexer_mx4_attend_args &g, int64_t max_keys) {
+    const int head_dim = g.head_dim;
+    void *workspace = g.workspace;
+    hipStream_t stream = (hipStream_t)g.stream;
     const bool selected = a.idx != nullptr;
     const lidx::Mx4Plan p = lidx::plan_mx4_attend(a.n_requests, a.q_len, max_keys, selected, a.n_heads, a.n_kv,
                                                   head_dim);
     if (p.workgroups > INT32_MAX) MX4_FAIL(INDEXER_EINVAL, "problem too large for one launch");
-    if (p.workspace_bytes && (!workspace || workspace_bytes < p.workspace_bytes || !aligned(workspace, 256)))
+    if (p.workspace_bytes && (!workspace || g.workspace_bytes < p.workspace_bytes || !aligned(workspace, 256)))
         MX4_FAIL(INDEXER_EWORKSPACE, "attention needs %zu bytes of 256-byte aligned workspace, got %zu",
-                 p.workspace_bytes, workspace ? workspace_bytes : (size_t)0);
+                 p.workspace_bytes, workspace ? g.workspace_bytes : (size_t)0);
     if (a.rows == 0) return done(hipSuccess, "");
     a.units = p.units;
     a.m_tiles = p.m_tiles;
@@ -174,7 +176,7 @@ indexer_status run_attend(lidx::Mx4Attend &a, int32_t type, int32_t head_dim, in
     a.div_items = lidx::fast_div((uint32_t)(p.m_tiles * p.n_splits));
     a.part_o = (float *)workspace;
     a.part_ml = (float *)((char *)workspace + p.part_o_bytes);
-    return done(type == INDEXER_MX4_BF16 ? lidx::launch_mx4_attend_bf16(a, p, head_dim, stream)
+    return done(g.type == INDEXER_MX4_BF16 ? lidx::launch_mx4_attend_bf16(a, p, head_dim, stream)
                                          : lidx::launch_mx4_attend_f16(a, p, head_dim, stream),
                 "attention kernel launch");
 }
@@ -283,129 +285,112 @@ Mx4Plan plan_mx4_attend(int n_requests, int q_len, int64_t max_keys, bool select
 
 extern "C" {
 
-indexer_status indexer_mx4_cache_write(const void *k, int64_t k_st, int64_t k_sh, const void *v, int64_t v_st,
-                                       int64_t v_sh, int32_t type, int32_t n_tokens, int32_t n_heads,
-                                       int32_t head_dim, const int64_t *slots, void *k_data, void *k_scale,
-                                       void *v_data, void *v_scale, int32_t n_blocks, int32_t block_size,
-                                       int64_t d_sb, int64_t d_ss, int64_t d_sh, int64_t s_sb, int64_t s_ss,
-                                       int64_t s_sh, void *stream) {
-    MX4_TRY(check_type(type));
-    if (n_tokens < 0) MX4_FAIL(INDEXER_EINVAL, "n_tokens=%d must be >= 0", n_tokens);
-    MX4_TRY(check_row_shape(n_heads, head_dim));
+indexer_status indexer_mx4_cache_write(const indexer_mx4_write_args *args) {
+    if (!args) MX4_FAIL(INDEXER_EINVAL, "args is NULL");
+    const indexer_mx4_write_args &g = *args;
+    MX4_TRY(check_type(g.type));
+    if (g.n_tokens < 0) MX4_FAIL(INDEXER_EINVAL, "n_tokens=%d must be >= 0", g.n_tokens);
+    MX4_TRY(check_row_shape(g.n_heads, g.head_dim));
     lidx::Mx4Write a{};
-    MX4_TRY(check_pages(n_blocks, block_size, n_heads, head_dim, d_sb, d_ss, d_sh, s_sb, s_ss, s_sh, &a.pages));
-    MX4_TRY(check_rows("k", k, k_st, k_sh, n_heads, head_dim));
-    if (n_blocks > 0) MX4_TRY(check_cache("k", k_data, k_scale));
-    if (v) {
-        MX4_TRY(check_rows("v", v, v_st, v_sh, n_heads, head_dim));
-        if (n_blocks > 0) MX4_TRY(check_cache("v", v_data, v_scale));
+    MX4_TRY(check_pages(g.n_blocks, g.block_size, g.n_heads, g.head_dim, g.strides, &a.pages));
+    MX4_TRY(check_rows("k", g.k, g.k_stride_t, g.k_stride_h, g.n_heads, g.head_dim));
+    if (g.n_blocks > 0) MX4_TRY(check_cache("k", g.k_data, g.k_scale));
+    if (g.v) {
+        MX4_TRY(check_rows("v", g.v, g.v_stride_t, g.v_stride_h, g.n_heads, g.head_dim));
+        if (g.n_blocks > 0) MX4_TRY(check_cache("v", g.v_data, g.v_scale));
     }
-    if (!slots) MX4_FAIL(INDEXER_EINVAL, "slots is NULL");
-    if (!aligned(slots, 8)) MX4_FAIL(INDEXER_EINVAL, "slots must be 8-byte aligned");
-    if (n_tokens == 0 || n_blocks == 0) return done(hipSuccess, "");
-    a.x[0] = k;
-    a.x[1] = v;
-    a.st[0] = k_st;
-    a.st[1] = v_st;
-    a.sh[0] = k_sh;
-    a.sh[1] = v_sh;
-    a.data[0] = (uint8_t *)k_data;
-    a.data[1] = (uint8_t *)v_data;
-    a.scale[0] = (uint8_t *)k_scale;
-    a.scale[1] = (uint8_t *)v_scale;
-    a.slots = slots;
-    a.n_tokens = n_tokens;
-    a.n_heads = n_heads;
-    a.head_dim = head_dim;
-    a.n_tensors = v ? 2 : 1;
-    a.div_e = lidx::fast_div((uint32_t)(n_heads * (head_dim / 8)));
-    a.div_c = lidx::fast_div((uint32_t)(head_dim / 8));
-    a.bf16 = type == INDEXER_MX4_BF16;
-    return done(lidx::launch_mx4_write(a, (hipStream_t)stream), "cache write launch");
+    if (!g.slots) MX4_FAIL(INDEXER_EINVAL, "slots is NULL");
+    if (!aligned(g.slots, 8)) MX4_FAIL(INDEXER_EINVAL, "slots must be 8-byte aligned");
+    if (g.n_tokens == 0 || g.n_blocks == 0) return done(hipSuccess, "");
+    a.x[0] = g.k;
+    a.x[1] = g.v;
+    a.st[0] = g.k_stride_t;
+    a.st[1] = g.v_stride_t;
+    a.sh[0] = g.k_stride_h;
+    a.sh[1] = g.v_stride_h;
+    a.data[0] = (uint8_t *)g.k_data;
+    a.data[1] = (uint8_t *)g.v_data;
+    a.scale[0] = (uint8_t *)g.k_scale;
+    a.scale[1] = (uint8_t *)g.v_scale;
+    a.slots = g.slots;
+    a.n_tokens = g.n_tokens;
+    a.n_heads = g.n_heads;
+    a.head_dim = g.head_dim;
+    a.n_tensors = g.v ? 2 : 1;
+    a.div_e = lidx::fast_div((uint32_t)(g.n_heads * (g.head_dim / 8)));
+    a.div_c = lidx::fast_div((uint32_t)(g.head_dim / 8));
+    a.bf16 = g.type == INDEXER_MX4_BF16;
+    return done(lidx::launch_mx4_write(a, (hipStream_t)g.stream), "cache write launch");
 }
 
-indexer_status indexer_mx4_cache_read(const void *data, const void *scale, int32_t n_blocks, int32_t block_size,
-                                      int64_t d_sb, int64_t d_ss, int64_t d_sh, int64_t s_sb, int64_t s_ss,
-                                      int64_t s_sh, const int64_t *slots, int32_t n_rows, int32_t n_heads,
-                                      int32_t head_dim, void *out, int64_t out_st, int64_t out_sh, int32_t type,
-                                      void *stream) {
-    MX4_TRY(check_type(type));
-    if (n_rows < 0) MX4_FAIL(INDEXER_EINVAL, "n_rows=%d must be >= 0", n_rows);
-    MX4_TRY(check_row_shape(n_heads, head_dim));
+indexer_status indexer_mx4_cache_read(const indexer_mx4_read_args *args) {
+    if (!args) MX4_FAIL(INDEXER_EINVAL, "args is NULL");
+    const indexer_mx4_read_args &g = *args;
+    MX4_TRY(check_type(g.type));
+    if (g.n_rows < 0) MX4_FAIL(INDEXER_EINVAL, "n_rows=%d must be >= 0", g.n_rows);
+    MX4_TRY(check_row_shape(g.n_heads, g.head_dim));
+    if (g.n_blocks < 1) MX4_FAIL(INDEXER_EINVAL, "n_blocks=%d must be >= 1 to read", g.n_blocks);
     lidx::Mx4Read a{};
-    MX4_TRY(check_pages(n_blocks, block_size, n_heads, head_dim, d_sb, d_ss, d_sh, s_sb, s_ss, s_sh, &a.pages));
-    if (n_blocks > 0) MX4_TRY(check_cache("the cache's", data, scale));
-    MX4_TRY(check_rows("out", out, out_st, out_sh, n_heads, head_dim));
-    if (!slots) MX4_FAIL(INDEXER_EINVAL, "slots is NULL");
-    if (!aligned(slots, 8)) MX4_FAIL(INDEXER_EINVAL, "slots must be 8-byte aligned");
-    if (n_rows == 0) return done(hipSuccess, "");
-    a.data = (const uint8_t *)data;
-    a.scale = (const uint8_t *)scale;
-    a.slots = slots;
-    a.out = out;
-    a.st = out_st;
-    a.sh = out_sh;
-    a.n_rows = n_rows;
-    a.n_heads = n_heads;
-    a.head_dim = head_dim;
-    a.div_e = lidx::fast_div((uint32_t)(n_heads * (head_dim / 8)));
-    a.div_c = lidx::fast_div((uint32_t)(head_dim / 8));
-    a.bf16 = type == INDEXER_MX4_BF16;
-    return done(lidx::launch_mx4_read(a, (hipStream_t)stream), "cache read launch");
+    MX4_TRY(check_pages(g.n_blocks, g.block_size, g.n_heads, g.head_dim, g.strides, &a.pages));
+    MX4_TRY(check_cache("the cache's", g.data, g.scale));
+    MX4_TRY(check_rows("out", g.out, g.out_stride_t, g.out_stride_h, g.n_heads, g.head_dim));
+    if (!g.slots) MX4_FAIL(INDEXER_EINVAL, "slots is NULL");
+    if (!aligned(g.slots, 8)) MX4_FAIL(INDEXER_EINVAL, "slots must be 8-byte aligned");
+    if (g.n_rows == 0) return done(hipSuccess, "");
+    a.data = (const uint8_t *)g.data;
+    a.scale = (const uint8_t *)g.scale;
+    a.slots = g.slots;
+    a.out = g.out;
+    a.st = g.out_stride_t;
+    a.sh = g.out_stride_h;
+    a.n_rows = g.n_rows;
+    a.n_heads = g.n_heads;
+    a.head_dim = g.head_dim;
+    a.div_e = lidx::fast_div((uint32_t)(g.n_heads * (g.head_dim / 8)));
+    a.div_c = lidx::fast_div((uint32_t)(g.head_dim / 8));
+    a.bf16 = g.type == INDEXER_MX4_BF16;
+    return done(lidx::launch_mx4_read(a, (hipStream_t)g.stream), "cache read launch");
 }
 
-indexer_status indexer_mx4_attend_selected(
-    const void *q, int64_t q_st, int64_t q_sh, int32_t type, const void *k_data, const void *k_scale,
-    const void *v_data, const void *v_scale, int32_t n_blocks, int32_t block_size, int64_t d_sb, int64_t d_ss,
-    int64_t d_sh, int64_t s_sb, int64_t s_ss, int64_t s_sh, const int32_t *block_table, int64_t bt_stride,
-    const int32_t *seq_lens, int32_t n_requests, int32_t query_len, int32_t max_seq_len, int32_t n_heads,
-    int32_t n_kv_heads, int32_t head_dim, float sm_scale, const int32_t *idx, int64_t idx_stride, int32_t n_sel,
-    int32_t pool_size, void *out, int64_t out_st, int64_t out_sh, float *lse, void *workspace,
-    size_t workspace_bytes, void *stream) {
+indexer_status indexer_mx4_attend_selected(const indexer_mx4_attend_args *args) {
+    if (!args) MX4_FAIL(INDEXER_EINVAL, "args is NULL");
+    const indexer_mx4_attend_args &g = *args;
     lidx::Mx4Attend a;
-    MX4_TRY(check_attend(q, q_st, q_sh, type, k_data, k_scale, v_data, v_scale, n_blocks, block_size, d_sb, d_ss, d_sh,
-                         s_sb, s_ss, s_sh, block_table, bt_stride, seq_lens, n_requests, query_len, max_seq_len,
-                         n_heads, n_kv_heads, head_dim, sm_scale, out, out_st, out_sh, lse, &a));
-    if (n_sel < 0) MX4_FAIL(INDEXER_EINVAL, "n_sel=%d must be >= 0", n_sel);
-    if (pool_size < 1) MX4_FAIL(INDEXER_EINVAL, "pool_size=%d must be >= 1", pool_size);
-    if (pool_size > lidx::kMaxPool) MX4_FAIL(INDEXER_ENOTSUP, "pool_size=%d exceeds %d", pool_size, lidx::kMaxPool);
-    if ((int64_t)n_sel * pool_size > kMaxKeys)
-        MX4_FAIL(INDEXER_ENOTSUP, "n_sel*pool_size=%lld exceeds %d", (long long)n_sel * pool_size, kMaxKeys);
-    if (!idx) MX4_FAIL(INDEXER_EINVAL, "idx is NULL");
-    if (!aligned(idx, 4)) MX4_FAIL(INDEXER_EINVAL, "idx must be 4-byte aligned");
-    if (idx_stride < n_sel)
-        MX4_FAIL(INDEXER_EINVAL, "idx_stride=%lld < n_sel=%d", (long long)idx_stride, n_sel);
-    a.idx = idx;
-    a.idx_st = idx_stride;
-    a.n_sel = n_sel;
-    a.pool = pool_size;
-    a.div_pool = lidx::fast_div((uint32_t)pool_size);
-    return run_attend(a, type, head_dim, (int64_t)n_sel * pool_size, workspace, workspace_bytes, (hipStream_t)stream);
+    MX4_TRY(check_attend(g, &a));
+    if (g.n_sel < 0) MX4_FAIL(INDEXER_EINVAL, "n_sel=%d must be >= 0", g.n_sel);
+    if (g.pool_size < 1) MX4_FAIL(INDEXER_EINVAL, "pool_size=%d must be >= 1", g.pool_size);
+    if (g.pool_size > lidx::kMaxPool) MX4_FAIL(INDEXER_ENOTSUP, "pool_size=%d exceeds %d", g.pool_size, lidx::kMaxPool);
+    if ((int64_t)g.n_sel * g.pool_size > kMaxKeys)
+        MX4_FAIL(INDEXER_ENOTSUP, "n_sel*pool_size=%lld exceeds %d", (long long)g.n_sel * g.pool_size, kMaxKeys);
+    if (!g.idx) MX4_FAIL(INDEXER_EINVAL, "idx is NULL");
+    if (!aligned(g.idx, 4)) MX4_FAIL(INDEXER_EINVAL, "idx must be 4-byte aligned");
+    if (g.idx_stride < g.n_sel)
+        MX4_FAIL(INDEXER_EINVAL, "idx_stride=%lld < n_sel=%d", (long long)g.idx_stride, g.n_sel);
+    a.idx = g.idx;
+    a.idx_st = g.idx_stride;
+    a.n_sel = g.n_sel;
+    a.pool = g.pool_size;
+    a.div_pool = lidx::fast_div((uint32_t)g.pool_size);
+    return run_attend(a, g, (int64_t)g.n_sel * g.pool_size);
 }
 
-indexer_status indexer_mx4_attend_window(
-    const void *q, int64_t q_st, int64_t q_sh, int32_t type, const void *k_data, const void *k_scale,
-    const void *v_data, const void *v_scale, int32_t n_blocks, int32_t block_size, int64_t d_sb, int64_t d_ss,
-    int64_t d_sh, int64_t s_sb, int64_t s_ss, int64_t s_sh, const int32_t *block_table, int64_t bt_stride,
-    const int32_t *seq_lens, int32_t n_requests, int32_t query_len, int32_t max_seq_len, int32_t n_heads,
-    int32_t n_kv_heads, int32_t head_dim, float sm_scale, int32_t window, int32_t sinks, void *out, int64_t out_st,
-    int64_t out_sh, float *lse, void *workspace, size_t workspace_bytes, void *stream) {
+indexer_status indexer_mx4_attend_window(const indexer_mx4_attend_args *args) {
+    if (!args) MX4_FAIL(INDEXER_EINVAL, "args is NULL");
+    const indexer_mx4_attend_args &g = *args;
     lidx::Mx4Attend a;
-    MX4_TRY(check_attend(q, q_st, q_sh, type, k_data, k_scale, v_data, v_scale, n_blocks, block_size, d_sb, d_ss, d_sh,
-                         s_sb, s_ss, s_sh, block_table, bt_stride, seq_lens, n_requests, query_len, max_seq_len,
-                         n_heads, n_kv_heads, head_dim, sm_scale, out, out_st, out_sh, lse, &a));
-    if (window < 0 || sinks < 0) MX4_FAIL(INDEXER_EINVAL, "window=%d sinks=%d must be >= 0", window, sinks);
-    a.window = window;
-    a.sinks = window ? sinks : 0;
-    return run_attend(a, type, head_dim, window_keys(max_seq_len, window, sinks), workspace, workspace_bytes,
-                      (hipStream_t)stream);
+    MX4_TRY(check_attend(g, &a));
+    if (g.window < 0 || g.sinks < 0)
+        MX4_FAIL(INDEXER_EINVAL, "window=%d sinks=%d must be >= 0", g.window, g.sinks);
+    a.window = g.window;
+    a.sinks = g.window ? g.sinks : 0;
+    return run_attend(a, g, window_keys(g.max_seq_len, g.window, g.sinks));
 }
 
 size_t indexer_mx4_attend_workspace_bytes(int32_t n_requests, int32_t query_len, int32_t max_keys, int32_t selected,
                                           int32_t n_heads, int32_t n_kv_heads, int32_t head_dim) {
     if (n_requests < 0 || query_len < 1 || max_keys < 0 || n_heads < 1 || n_heads > lidx::kMaxHeads ||
         n_kv_heads < 1 || n_heads % n_kv_heads || !attend_dim(head_dim) ||
-        (int64_t)n_requests * query_len * n_heads > INT32_MAX)
+        (int64_t)n_requests * query_len > INT32_MAX / n_heads)
         return (size_t)-1;
     return lidx::plan_mx4_attend(n_requests, query_len, max_keys, selected != 0, n_heads, n_kv_heads, head_dim)
         .workspace_bytes;

@@ -16,6 +16,7 @@ slot and head may be strided in any order (a permuted view of
 from __future__ import annotations
 
 import ctypes
+import struct
 import sys
 from typing import Optional, Tuple
 
@@ -28,6 +29,12 @@ MX4_EXPORTS = (
 MX4_F16, MX4_BF16 = 0, 1
 MAX_KEYS = 2**31 - 1024
 
+# The argument structures of include/indexer_mx4.h, member by member: packing
+# one is several times quicker than passing 40 arguments through ctypes
+WRITE = struct.Struct("=18q6i")
+READ = struct.Struct("=13q6i")
+ATTEND = struct.Struct("=25q13if")
+
 _lib = None        # the library with these entry points' signatures declared
 _torch = None
 _types = {}        # torch dtype -> the library's type code
@@ -38,19 +45,11 @@ def _library():
     lib = _pkg.load_library()
     if _lib is lib:
         return lib
-    p, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
-    pages = [i32, i32] + [i64] * 6
-    cached = [p, i64, i64, i32, p, p, p, p] + pages + [p, i64, p] + [i32] * 6 + [ctypes.c_float]
-    out = [p, i64, i64, p, p, sz, p]
-    lib.indexer_mx4_cache_write.argtypes = [p, i64, i64, p, i64, i64, i32, i32, i32, i32, p, p, p, p, p] + pages + [p]
-    lib.indexer_mx4_cache_read.argtypes = [p, p] + pages + [p, i32, i32, i32, p, i64, i64, i32, p]
-    lib.indexer_mx4_attend_selected.argtypes = cached + [p, i64, i32, i32] + out
-    lib.indexer_mx4_attend_window.argtypes = cached + [i32, i32] + out
-    for f in (lib.indexer_mx4_cache_write, lib.indexer_mx4_cache_read, lib.indexer_mx4_attend_selected,
-              lib.indexer_mx4_attend_window):
-        f.restype = ctypes.c_int
-    lib.indexer_mx4_attend_workspace_bytes.argtypes = [i32] * 7
-    lib.indexer_mx4_attend_workspace_bytes.restype = sz
+    for name in MX4_EXPORTS[:4]:
+        f = getattr(lib, name)
+        f.argtypes, f.restype = [ctypes.c_char_p], ctypes.c_int   # a packed argument structure
+    lib.indexer_mx4_attend_workspace_bytes.argtypes = [ctypes.c_int32] * 7
+    lib.indexer_mx4_attend_workspace_bytes.restype = ctypes.c_size_t
     if _torch is None:
         _torch = _pkg._torch()
         _types.update({_torch.float16: MX4_F16, _torch.bfloat16: MX4_BF16})
@@ -128,14 +127,24 @@ def _slots(slots, n, dev):
         raise ValueError("slots must be contiguous")
 
 
-def _call(dev, entry, *args):
-    """Calls the library on torch's current stream of the tensors' device,
-    with that device current."""
+def _pack(layout, *members):
+    try:
+        return layout.pack(*members)
+    except (struct.error, OverflowError) as e:
+        raise ValueError(f"an argument is out of its range: {e}") from None
+
+
+def _stream(dev):
+    return _torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _call(dev, entry, args):
+    """Calls the library with the tensors' device current."""
     if dev == _torch._C._cuda_getDevice():
-        status = entry(*args, _torch._C._cuda_getCurrentRawStream(dev))
+        status = entry(args)
     else:
         with _torch.cuda.device(dev):
-            status = entry(*args, _torch._C._cuda_getCurrentRawStream(dev))
+            status = entry(args)
     if status:
         _pkg._check(status)
 
@@ -152,7 +161,7 @@ def mx4_cache_write(k, slots, k_data, k_scale, v=None, v_data=None, v_scale=None
     n, heads, d = shape = tuple(k.shape)
     pages = _cache(k_data, k_scale, "k", dev, heads, d)
     _slots(slots, n, dev)
-    v_args, v_strides = (None, None), (0, 0)
+    v_args, v_strides = (0, 0), (0, 0)
     if v is not None and v_data is not None and v_scale is not None:
         v_strides = _rows(v, "v", k.dtype, dev, shape)
         if _cache(v_data, v_scale, "v", dev, heads, d) != pages:
@@ -162,8 +171,10 @@ def mx4_cache_write(k, slots, k_data, k_scale, v=None, v_data=None, v_scale=None
         raise ValueError("v, v_data and v_scale come together")
     if n == 0 or pages[0] == 0:  # nothing to write, or nowhere (and empty tensors have no address)
         return
-    _call(dev, lib.indexer_mx4_cache_write, k.data_ptr(), *k_strides, None if v is None else v.data_ptr(), *v_strides,
-          kind, n, heads, d, slots.data_ptr(), k_data.data_ptr(), k_scale.data_ptr(), *v_args, *pages)
+    blocks, size, *strides = pages
+    _call(dev, lib.indexer_mx4_cache_write, _pack(
+        WRITE, k.data_ptr(), *k_strides, 0 if v is None else v.data_ptr(), *v_strides, slots.data_ptr(),
+        k_data.data_ptr(), k_scale.data_ptr(), *v_args, *strides, _stream(dev), kind, n, heads, d, blocks, size))
 
 
 def mx4_cache_read(data, scale, slots, dtype=None, out=None):
@@ -190,8 +201,10 @@ def mx4_cache_read(data, scale, slots, dtype=None, out=None):
         return out
     if pages[0] == 0:  # an empty cache has no slot, and no address
         return out.zero_()
-    _call(dev, lib.indexer_mx4_cache_read, data.data_ptr(), scale.data_ptr(), *pages, slots.data_ptr(), n, heads, d,
-          out.data_ptr(), *strides, kind)
+    blocks, size, *page_strides = pages
+    _call(dev, lib.indexer_mx4_cache_read, _pack(
+        READ, data.data_ptr(), scale.data_ptr(), *page_strides, slots.data_ptr(), out.data_ptr(), *strides,
+        _stream(dev), kind, n, heads, d, blocks, size))
     return out
 
 
@@ -251,11 +264,13 @@ def _attend(entry, q, k_data, k_scale, v_data, v_scale, block_table, seq_lens, q
         need = _lib.indexer_mx4_attend_workspace_bytes(requests, query_len, max_keys, selected, heads, kv, d)
         if 0 < need < 2**63:  # sizes the library refuses have none: the call below names them
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    _call(dev, entry, q.data_ptr(), *q_strides, kind, k_data.data_ptr(), k_scale.data_ptr(), v_data.data_ptr(),
-          v_scale.data_ptr(), *pages, block_table.data_ptr(), bt_stride if bt_rows > 1 else bt_cols,
-          seq_lens.data_ptr(), requests, query_len, max_seq_len, heads, kv, d, sm_scale, *form, out.data_ptr(),
-          *out_strides, None if lse is None else lse.data_ptr(), None if workspace is None else workspace.data_ptr(),
-          0 if workspace is None else workspace.numel())
+    blocks, size, *strides = pages
+    _call(dev, entry, _pack(
+        ATTEND, q.data_ptr(), *q_strides, k_data.data_ptr(), k_scale.data_ptr(), v_data.data_ptr(),
+        v_scale.data_ptr(), *strides, block_table.data_ptr(), bt_stride if bt_rows > 1 else bt_cols,
+        seq_lens.data_ptr(), out.data_ptr(), *out_strides, 0 if lse is None else lse.data_ptr(),
+        0 if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(), _stream(dev),
+        *form, kind, blocks, size, requests, query_len, max_seq_len, heads, kv, d, sm_scale))
     return out, lse
 
 
@@ -292,7 +307,7 @@ def mx4_attend_selected(q, k_data, k_scale, v_data, v_scale, block_table, seq_le
     return _attend(lib.indexer_mx4_attend_selected, q, k_data, k_scale, v_data, v_scale, block_table, seq_lens,
                    query_len, min(block_table.shape[1] * k_data.shape[1], MAX_KEYS), sm_scale, 1,
                    min(n_sel * pool_size, 2**31 - 1),
-                   (idx.data_ptr(), idx_stride if rows > 1 else n_sel, n_sel, pool_size), out, lse, with_lse,
+                   (idx.data_ptr(), idx_stride if rows > 1 else n_sel, n_sel, pool_size, 0, 0), out, lse, with_lse,
                    workspace)
 
 
@@ -306,5 +321,6 @@ def mx4_attend_window(q, k_data, k_scale, v_data, v_scale, block_table, seq_lens
     lib = _library()
     keys = max_seq_len if window == 0 else min(max_seq_len, window + sinks)
     return _attend(lib.indexer_mx4_attend_window, q, k_data, k_scale, v_data, v_scale, block_table, seq_lens, query_len,
-                   max_seq_len, sm_scale, 0, max(0, min(keys, 2**31 - 1)), (window, sinks), out, lse, with_lse,
+                   max_seq_len, sm_scale, 0, max(0, min(keys, 2**31 - 1)),
+                   (0, 0, 0, 0, window, sinks), out, lse, with_lse,
                    workspace)

@@ -32,17 +32,20 @@ def test_exports_every_declared_symbol(lib):
 PAGES = dict(nb=4, bs=16, dsb=16 * 8 * 64, dss=8 * 64, dsh=64, ssb=16 * 8 * 4, sss=8 * 4, ssh=4)
 
 
-def pages_of(a):
-    return [a[n] for n in ("nb", "bs", "dsb", "dss", "dsh", "ssb", "sss", "ssh")]
+def packed(layout, a, names):
+    """The argument structure of the members `names` of `a`, in the header's order."""
+    return layout.pack(*(0 if a[n] is None else a[n] for n in names.split()))
+
+
+STRIDES = "dsb dss dsh ssb sss ssh "
 
 
 def write(lib, **kw):
     a = dict(k=A, kst=1024, ksh=128, v=B, vst=1024, vsh=128, type=0, n=2, H=8, d=128, slots=A, kd=A, ks=A, vd=B, vs=B,
              stream=None, **PAGES)
     a.update(kw)
-    return lib.indexer_mx4_cache_write(a["k"], a["kst"], a["ksh"], a["v"], a["vst"], a["vsh"], a["type"], a["n"],
-                                       a["H"], a["d"], a["slots"], a["kd"], a["ks"], a["vd"], a["vs"], *pages_of(a),
-                                       a["stream"])
+    return lib.indexer_mx4_cache_write(packed(
+        mx4.WRITE, a, "k kst ksh v vst vsh slots kd ks vd vs " + STRIDES + "stream type n H d nb bs"))
 
 
 PAGE_REFUSALS = [
@@ -98,13 +101,14 @@ def test_nothing_to_write_is_a_no_op(lib):
 def read(lib, **kw):
     a = dict(data=A, scale=A, slots=A, n=2, H=8, d=128, out=B, ost=1024, osh=128, type=1, stream=None, **PAGES)
     a.update(kw)
-    return lib.indexer_mx4_cache_read(a["data"], a["scale"], *pages_of(a), a["slots"], a["n"], a["H"], a["d"],
-                                      a["out"], a["ost"], a["osh"], a["type"], a["stream"])
+    return lib.indexer_mx4_cache_read(packed(
+        mx4.READ, a, "data scale " + STRIDES + "slots out ost osh stream type n H d nb bs"))
 
 
 @pytest.mark.parametrize("kw,status,msg", PAGE_REFUSALS + [
     (dict(type=-1), li.EINVAL, b"type=-1"),
     (dict(n=-2), li.EINVAL, b"n_rows"),
+    (dict(nb=0), li.EINVAL, b"n_blocks"),
     (dict(d=48), li.ENOTSUP, b"head_dim=48"),
     (dict(out=None), li.EINVAL, b"out is NULL"),
     (dict(out=B + 2), li.EINVAL, b"out must be 16-byte"),
@@ -127,12 +131,10 @@ def attend(lib, form, **kw):
              KV=8, d=128, scale=0.1, idx=A, idxs=32, n=32, pool=1, window=0, sinks=0, out=B, ost=64 * 128, osh=128,
              lse=A, ws=A, wsn=1 << 40, stream=None, **PAGES)
     a.update(kw)
-    head = [a[n] for n in ("q", "qst", "qsh", "type", "kd", "ks", "vd", "vs")] + pages_of(a) + [
-        a[n] for n in ("bt", "bts", "sl", "R", "Q", "L", "H", "KV", "d", "scale")]
-    tail = [a[n] for n in ("out", "ost", "osh", "lse", "ws", "wsn", "stream")]
-    if form == "selected":
-        return lib.indexer_mx4_attend_selected(*head, a["idx"], a["idxs"], a["n"], a["pool"], *tail)
-    return lib.indexer_mx4_attend_window(*head, a["window"], a["sinks"], *tail)
+    entry = lib.indexer_mx4_attend_selected if form == "selected" else lib.indexer_mx4_attend_window
+    return entry(packed(
+        mx4.ATTEND, a, "q qst qsh kd ks vd vs " + STRIDES + "bt bts sl out ost osh lse ws wsn stream idx idxs "
+        "n pool window sinks type nb bs R Q L H KV d scale"))
 
 
 @pytest.mark.parametrize("form", ["selected", "window"])
@@ -201,6 +203,19 @@ def test_attend_needs_its_workspace(lib):
     need = li.mx4_attend_workspace_bytes(2, 1, 2048, True, 64, 8, 128)
     assert need > 0
     assert attend(lib, "selected", n=2048, idxs=2048, wsn=need - 1) == li.EWORKSPACE
+
+
+def test_no_arguments(lib):
+    for name in li.MX4_EXPORTS[:4]:
+        assert getattr(lib, name)(None) == li.EINVAL
+        assert b"args is NULL" in lib.indexer_last_error()
+
+
+def test_binding_refuses_what_a_member_cannot_hold():
+    for layout, members in ((mx4.READ, [0] * 18 + [2**31]), (mx4.ATTEND, [0] * 38 + [1e39]),
+                            (mx4.WRITE, [2**63] + [0] * 23)):
+        with pytest.raises(ValueError, match="out of its range"):
+            mx4._pack(layout, *members)
 
 
 def test_no_requests_is_a_no_op(lib):

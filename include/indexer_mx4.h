@@ -156,7 +156,8 @@ indexer_status indexer_mx4_cache_read(const indexer_mx4_read_args *args);
  *                overlapping any input
  *   lse          f32 [n_requests*query_len][n_heads], contiguous, or NULL
  *   workspace    indexer_mx4_attend_workspace_bytes(...) bytes, 256-byte
- *                aligned; NULL when that is 0
+ *                aligned; NULL when that is 0.  Calls that may overlap (other
+ *                streams, graphs replayed side by side) need one each
  *   idx          selected: i32 [n_requests*query_len][idx_stride], the first
  *                n_sel of a row used
  *
@@ -165,7 +166,8 @@ indexer_status indexer_mx4_cache_read(const indexer_mx4_read_args *args);
  *
  * head_dim 64, 96, 128, 192 or 256; n_heads (at most 1024) a multiple of
  * n_kv_heads; sm_scale positive and finite; pool_size in [1, 8192];
- * max_seq_len and n_sel * pool_size at most 2^31 - 1024; window, sinks >= 0.
+ * max_seq_len, n_sel * pool_size and n_requests * query_len * n_heads at most
+ * 2^31 - 1024; window, sinks >= 0.
  * n_requests = 0 enqueues nothing; n_sel = 0 writes the empty rows' values.
  */
 typedef struct {

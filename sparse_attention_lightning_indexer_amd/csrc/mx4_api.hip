@@ -104,8 +104,8 @@ indexer_status check_attend(const indexer_mx4_attend_args &g, lidx::Mx4Attend *a
         !attend_dim(g.head_dim))
         MX4_FAIL(INDEXER_ENOTSUP, "n_heads=%d n_kv_heads=%d head_dim=%d not supported (n_heads in 1..%d, a multiple of "
                  "n_kv_heads; head_dim 64, 96, 128, 192 or 256)", g.n_heads, g.n_kv_heads, g.head_dim, lidx::kMaxHeads);
-    if ((int64_t)g.n_requests * g.query_len > INT32_MAX / g.n_heads)
-        MX4_FAIL(INDEXER_EINVAL, "n_requests*query_len*n_heads exceeds the int32 range");
+    if ((int64_t)g.n_requests * g.query_len > kMaxKeys / g.n_heads)
+        MX4_FAIL(INDEXER_EINVAL, "n_requests*query_len*n_heads exceeds the int32 range (%d)", kMaxKeys);
     if (!(g.sm_scale > 0.0f) || !isfinite(g.sm_scale) || !isfinite(g.sm_scale * 1.44269504f))
         MX4_FAIL(INDEXER_EINVAL, "sm_scale=%g must be positive and finite", (double)g.sm_scale);
     lidx::Mx4Pages pages;
@@ -163,7 +163,9 @@ indexer_status run_attend(lidx::Mx4Attend &a, const indexer_mx4_attend_args &g, 
     const bool selected = a.idx != nullptr;
     const lidx::Mx4Plan p = lidx::plan_mx4_attend(a.n_requests, a.q_len, max_keys, selected, a.n_heads, a.n_kv,
                                                   head_dim);
-    if (p.workgroups > INT32_MAX) MX4_FAIL(INDEXER_EINVAL, "problem too large for one launch");
+    // a launch holds fewer than 2^32 threads
+    if (p.workgroups * 512 > UINT32_MAX || (p.n_splits > 1 && (int64_t)a.rows * a.n_heads * 256 > UINT32_MAX))
+        MX4_FAIL(INDEXER_EINVAL, "problem too large for one launch: %lld workgroups", (long long)p.workgroups);
     if (p.workspace_bytes && (!workspace || g.workspace_bytes < p.workspace_bytes || !aligned(workspace, 256)))
         MX4_FAIL(INDEXER_EWORKSPACE, "attention needs %zu bytes of 256-byte aligned workspace, got %zu",
                  p.workspace_bytes, workspace ? g.workspace_bytes : (size_t)0);
@@ -214,6 +216,11 @@ static Mx4Plan sized(Mx4Plan p, int64_t rows, int n_heads, int n_kv, int head_di
 // of about 4 tiles of a wave; 32 rows of 512 keys on 8 heads, two tiles a
 // wave, take 9.3 us whole and 15.8 us in halves.  So keys are shared only
 // where that takes at least 4 tiles from every wave.
+//
+// With one workgroup a compute unit there are registers for the codes of two
+// tiles on the way instead of one: one row of 131072 keys 38.1 and 34.9 us, but
+// 32 rows of 512 keys, two tiles a wave, 9.3 and 10.7 us (its first loads wait
+// for those that no tile needs); so from 8 tiles a wave on.
 //
 // Many rows of a request under a window go through the keys 256 at a time and
 // together (mx4_prompt_kernel) where that is the shorter of two estimates, fit
@@ -273,6 +280,7 @@ Mx4Plan plan_mx4_attend(int n_requests, int q_len, int64_t max_keys, bool select
     // most: tiles of a wave that has a row's keys to itself
     if (splits < 1 || most * (splits - 1) < 4 * splits) splits = 1;
     p.n_splits = (int)splits;
+    p.ahead = p.mt == 1 && p.hp == 1 && head_dim <= 128 && items * splits <= kCus && most >= 8 * splits ? 2 : 1;
     if (!selected && p.mt == 2 && waves == 8 && splits == 1)
         for (int g = 8; g > 1 && p.head_group == 1; g /= 2) {
             const int64_t wgs = items / g, rounds = (wgs + kCus - 1) / kCus;
@@ -390,7 +398,7 @@ size_t indexer_mx4_attend_workspace_bytes(int32_t n_requests, int32_t query_len,
                                           int32_t n_heads, int32_t n_kv_heads, int32_t head_dim) {
     if (n_requests < 0 || query_len < 1 || max_keys < 0 || n_heads < 1 || n_heads > lidx::kMaxHeads ||
         n_kv_heads < 1 || n_heads % n_kv_heads || !attend_dim(head_dim) ||
-        (int64_t)n_requests * query_len > INT32_MAX / n_heads)
+        (int64_t)n_requests * query_len > kMaxKeys / n_heads)
         return (size_t)-1;
     return lidx::plan_mx4_attend(n_requests, query_len, max_keys, selected != 0, n_heads, n_kv_heads, head_dim)
         .workspace_bytes;

@@ -21,12 +21,16 @@
 //  - A lane then holds 8 scores of one query row, (l & 15), which is the
 //    layout the product's P operand wants: P never leaves its lane, and
 //    neither do m, l and the rescaling of O^T = V^T P^T.
+//    The weights are rounded to the query's type there (the product takes one
+//    type; half a step of it each, averaged over the keys, is what the output's
+//    own rounding costs); their sum and everything else stays f32.
 //  - V's rows are converted like K's, stored to the wave's own LDS rows and
 //    read back transposed (ds_read_b64_tr_b16), 16 dimensions by 4 keys each.
 //    Rows are padded by 32 bytes: the 8 consecutive rows that half a wave reads
 //    32 bytes of, or writes 16 bytes of, then lie in different banks.
-//  - Loads run ahead: a tile's codes from when the one before is converted,
-//    its page ids one tile further, the selected indices one more.
+//  - Loads run ahead: a tile's codes from when the one before (PF = 2: two
+//    before) is converted, the page ids a pair of tiles further, the selected
+//    indices one more.
 //
 // Masked positions: their scores become -inf by selection, so K's NaN there
 // never spreads; V's blocks of NaN are replaced by zeros in the product, and
@@ -185,14 +189,21 @@ __device__ __forceinline__ Item item_of(const Mx4Attend &a, int mt, int hp) {
 enum Mode { kWindow = 0, kKeys = 1, kPools = 2 };
 
 // Waves per SIMD the registers have to leave room for.
-template <int D, int MT, int HP>
+template <int D, int MT, int HP, int PF>
 constexpr int waves_per_simd() {
+    if (PF == 2) return 2;
     return HP == 2 ? 3 : (MT == 1 && D <= 128 ? 4 : (MT == 2 && D == 256 ? 1 : 2));
 }
 
-template <bool BF16, int D, int MT, int HP, int MODE>
-__global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D, MT, HP>())) mx4_attend_kernel(Mx4Attend a) {
+template <int N>
+struct Set {
+    static constexpr int value = N;
+};
+
+template <bool BF16, int D, int MT, int HP, int PF, int MODE>
+__global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D, MT, HP, PF>())) mx4_attend_kernel(Mx4Attend a) {
     static_assert(HP == 1 || MT == 1, "pairs of heads have one tile of rows");
+    static_assert(HP == 1 || PF == 1, "a pair's second 16 keys are asked for late");
     using T = Type<BF16>;
     using S = Shape<D, HP>;
     typedef typename T::vec8 vec8;
@@ -339,10 +350,10 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
     const int blk0 = ch * KS / 4;
     const uint64_t chunk = (uint64_t)((uint32_t)hsel * (uint32_t)a.pages.d_sh) + (uint32_t)(ch * KS * 4);
     const uint64_t schunk = (uint64_t)((uint32_t)hsel * (uint32_t)a.pages.s_sh) + (uint32_t)blk0;
-    Raw raw[NU];
-    uint32_t have = 0;  // the keys that count: bit k is key k of the tile
-    // K's part of load u, V's, or both
-    auto load_rows = [&](int b, int u, bool k, bool v) {
+    Raw raw[PF][NU];    // PF = 2: of the wave's even and odd tiles
+    uint32_t have[PF];  // the keys that count: bit k is key k of the tile
+    // K's part of load u, V's, or both, of tile b of the pair
+    auto load_rows = [&](Raw (&raw)[NU], int b, int u, bool k, bool v) {
         const uint64_t row = ask(at, b, u), d = row + chunk;
         if (k) __builtin_memcpy(raw[u].k, __builtin_assume_aligned(kd + d, ALIGN), KS * 4);
         if (v) __builtin_memcpy(raw[u].v, __builtin_assume_aligned(vd + d, ALIGN), KS * 4);
@@ -385,18 +396,30 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
         pos = position(t_begin, id);
         page = load_page(pos);
         locate(pos, page);
-        have = (uint32_t)found;
 #pragma unroll
-        for (int u = 0; u < NU; ++u) load_rows(0, u, true, true);
-        if (SELECTED) id = load_index(t_begin + 2 * stride);
-        pos = position(t_begin + 2 * stride, id);
-        page = load_page(pos);
-        if (SELECTED) id = load_index(t_begin + 4 * stride);
+        for (int b = 0; b < PF; ++b) {
+            have[b] = (uint32_t)(found >> (b * 32));
+#pragma unroll
+            for (int u = 0; u < NU; ++u) load_rows(raw[b], b, u, true, true);
+        }
+        auto following = [&](int tile) {
+            if (SELECTED) id = load_index(tile);
+            pos = position(tile, id);
+            page = load_page(pos);
+        };
+        following(t_begin + 2 * stride);
+        if (PF == 2) {
+            locate(pos, page);
+            following(t_begin + 4 * stride);
+        }
+        if (SELECTED) id = load_index(t_begin + (PF == 2 ? 6 : 4) * stride);
     }
 
-    int odd = 0;
-    for (int tile = t_begin; tile < t_end; tile += stride, odd ^= 1) {
-        const uint32_t valid = have;
+    // one tile: `b` is its place in its pair, SET where its codes are
+    auto multiply = [&](auto set, int b, int tile) __attribute__((always_inline)) {
+        constexpr int SET = decltype(set)::value;
+        Raw(&raw_)[NU] = raw[SET];
+        const uint32_t valid = have[SET];
         const int p0 = SELECTED ? 0 : (tile < sink_tiles ? tile * 32 : base + (tile - sink_tiles) * 32);
         bool whole = valid == 0xffffffffu;
         if (!SELECTED) {
@@ -419,7 +442,7 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
 #pragma unroll
         for (int u = 0; u < NU; ++u)
 #pragma unroll
-            for (int n = 0; n < NB; ++n) bad |= raw[u].sv[n] == 255u;
+            for (int n = 0; n < NB; ++n) bad |= raw_[u].sv[n] == 255u;
         if (valid != 0xffffffffu || __ballot(bad)) {
 #pragma unroll
             for (int u = 0; u < NU; ++u) {
@@ -427,9 +450,9 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
                 uint32_t mine = 0;  // blocks of NaN in this lane's part of its key
 #pragma unroll
                 for (int n = 0; n < NB; ++n) {
-                    const bool b = raw[u].sv[n] == 255u;
+                    const bool b = raw_[u].sv[n] == 255u;
                     if (in && b) mine |= 1u << min(blk0 + n, D / 32 - 1);
-                    if (!in || b) raw[u].sv[n] = 0u;
+                    if (!in || b) raw_[u].sv[n] = 0u;
                 }
                 if (__ballot(mine != 0u)) {
                     for (int row = 0; row < KPL; ++row) {
@@ -455,11 +478,11 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
             lds_u8 *dst = stage + hsel * HEAD + (u * KPL >> 4) * TILE;
             uint32_t w1[K1], w2[K2];
 #pragma unroll
-            for (int i = 0; i < K1; ++i) w1[i] = raw[u].k[i];
+            for (int i = 0; i < K1; ++i) w1[i] = raw_[u].k[i];
             put_words<K1>(dst + unit_at(key & 15, U == 4 ? ch : ch * 2), w1);
             if constexpr (KS > 4) {
 #pragma unroll
-                for (int i = 0; i < K2; ++i) w2[i] = raw[u].k[4 + i];
+                for (int i = 0; i < K2; ++i) w2[i] = raw_[u].k[4 + i];
                 put_words<K2>(dst + unit_at(key & 15, ch * 2 + 1), w2);
             }
         }
@@ -467,9 +490,9 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
         uint32_t pack[NB];
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
-            pack[n] = raw[0].sk[n];
+            pack[n] = raw_[0].sk[n];
 #pragma unroll
-            for (int u = 1; u < NU; ++u) pack[n] |= raw[u].sk[n] << (8 * u);
+            for (int u = 1; u < NU; ++u) pack[n] |= raw_[u].sk[n] << (8 * u);
         }
 
         // scores: of each head with all columns, then each column its head's
@@ -519,10 +542,10 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
         auto store_v = [&](int u) {
 #pragma unroll
             for (int st = 0; st < KS; ++st) {
-                uint32_t sb = raw[u].sv[0];
+                uint32_t sb = raw_[u].sv[0];
 #pragma unroll
-                for (int b = 1; b < NB; ++b) sb = block_of(ch, st) == b ? raw[u].sv[b] : sb;
-                const vec8 vv = T::from4(raw[u].v[st], __builtin_bit_cast(float, sb << 23));
+                for (int b = 1; b < NB; ++b) sb = block_of(ch, st) == b ? raw_[u].sv[b] : sb;
+                const vec8 vv = T::from4(raw_[u].v[st], __builtin_bit_cast(float, sb << 23));
                 lds_u8 *row = stage + (HP == 2 ? hsel * S::SECOND + ((u & 1) * KPL + krow) * S::ROW
                                                : (u * KPL + krow) * S::ROW);
                 *(lds_u32x4 *)(row + (ch * KS + st) * 16) = __builtin_bit_cast(u32x4, vv);
@@ -531,18 +554,20 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
         store_v(0);
         store_v(1);
 
-        // the next tile's codes, into the registers this one's came from; every
-        // second tile the offsets of the next pair, the page ids of the one
-        // after, and the indices of the one after that
-        have = (uint32_t)(found >> ((odd ^ 1) * 32));
+        // the codes of the tile PF on, into the registers this one's came from;
+        // after the pair's last of these the offsets of the pair after, and the
+        // page ids of the one after that, and the indices of the next
+        const int nb = PF == 2 ? b : b ^ 1;
+        have[SET] = (uint32_t)(found >> (nb * 32));
 #pragma unroll
-        for (int u = 0; u < NU; ++u) load_rows(odd ^ 1, u, true, u < 2);
+        for (int u = 0; u < NU; ++u) load_rows(raw_, nb, u, true, u < 2);
         auto advance = [&]() {
-            if (odd) return;
+            if (nb == 0) return;
+            const int first = tile - b * stride;  // of this pair
             locate(pos, page);
-            pos = position(tile + 4 * stride, id);
+            pos = position(first + (PF == 2 ? 6 : 4) * stride, id);
             page = load_page(pos);
-            if (SELECTED) id = load_index(tile + 6 * stride);
+            if (SELECTED) id = load_index(first + (PF == 2 ? 8 : 6) * stride);
         };
         if (HP == 1) advance();
 
@@ -606,8 +631,8 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
                 if (t) {
                     store_v(2);
                     store_v(3);
-                    load_rows(odd ^ 1, 2, false, true);
-                    load_rows(odd ^ 1, 3, false, true);
+                    load_rows(raw_, nb, 2, false, true);
+                    load_rows(raw_, nb, 3, false, true);
                     advance();
                 }
                 const vec8 pt = __builtin_bit_cast(vec8, u32x4{hcol ? 0u : pw[2 * t], hcol ? 0u : pw[2 * t + 1],
@@ -619,6 +644,15 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
                 }
             }
         }
+    };
+    if constexpr (PF == 2) {
+        for (int tile = t_begin; tile < t_end; tile += 2 * stride) {
+            multiply(Set<0>{}, 0, tile);
+            if (tile + stride < t_end) multiply(Set<1>{}, 1, tile + stride);
+        }
+    } else {
+        int odd = 0;
+        for (int tile = t_begin; tile < t_end; tile += stride, odd ^= 1) multiply(Set<0>{}, odd, tile);
     }
 
     // join the waves: each writes its product, m and l; every thread then adds
@@ -1044,15 +1078,15 @@ __global__ void __launch_bounds__(256) mx4_join_kernel(Mx4Attend a) {
     *reinterpret_cast<vec8 *>((uint16_t *)a.out + token * a.out_st + (int64_t)head * a.out_sh + threadIdx.x * 8) = r;
 }
 
-template <bool BF16, int D, int MT, int HP>
+template <bool BF16, int D, int MT, int HP, int PF>
 hipError_t launch_tiles(const Mx4Attend &a, const Mx4Plan &p, hipStream_t stream) {
     const dim3 grid((unsigned)p.workgroups), block(Shape<D, HP>::WAVES * 64);
     if (!a.idx)
-        hipLaunchKernelGGL((mx4_attend_kernel<BF16, D, MT, HP, kWindow>), grid, block, 0, stream, a);
+        hipLaunchKernelGGL((mx4_attend_kernel<BF16, D, MT, HP, PF, kWindow>), grid, block, 0, stream, a);
     else if (a.pool == 1)
-        hipLaunchKernelGGL((mx4_attend_kernel<BF16, D, MT, HP, kKeys>), grid, block, 0, stream, a);
+        hipLaunchKernelGGL((mx4_attend_kernel<BF16, D, MT, HP, PF, kKeys>), grid, block, 0, stream, a);
     else
-        hipLaunchKernelGGL((mx4_attend_kernel<BF16, D, MT, HP, kPools>), grid, block, 0, stream, a);
+        hipLaunchKernelGGL((mx4_attend_kernel<BF16, D, MT, HP, PF, kPools>), grid, block, 0, stream, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.n_splits == 1) return e;
     hipLaunchKernelGGL((mx4_join_kernel<BF16, D>), dim3((unsigned)(a.rows * a.n_heads)), dim3(256), 0, stream, a);
@@ -1070,10 +1104,13 @@ hipError_t launch_dim(const Mx4Attend &a, const Mx4Plan &p, hipStream_t stream) 
                                a);
             return hipGetLastError();
         }
-        if (p.hp == 2) return launch_tiles<BF16, D, 1, 2>(a, p, stream);
+        if (p.hp == 2) return launch_tiles<BF16, D, 1, 2, 1>(a, p, stream);
     }
-    if (p.mt == 1) return launch_tiles<BF16, D, 1, 1>(a, p, stream);
-    return launch_tiles<BF16, D, 2, 1>(a, p, stream);
+    if constexpr (D <= 128) {
+        if (p.ahead == 2) return launch_tiles<BF16, D, 1, 1, 2>(a, p, stream);
+    }
+    if (p.mt == 1) return launch_tiles<BF16, D, 1, 1, 1>(a, p, stream);
+    return launch_tiles<BF16, D, 2, 1, 1>(a, p, stream);
 }
 
 template <bool BF16>

@@ -193,6 +193,13 @@ def test_attend_window_refuses(lib, kw):
     assert b"window" in lib.indexer_last_error()
 
 
+def test_attend_refuses_what_one_launch_cannot_hold(lib):
+    many = dict(R=2_000_000, H=64, KV=16, ost=64 * 128, idxs=32, n=32)     # 2 million rows of 16 K/V heads
+    many.update(dsb=16 * 16 * 64, dss=16 * 64, ssb=16 * 16 * 4, sss=16 * 4, KV=16, H=160, qst=160 * 128, ost=160 * 128)
+    assert attend(lib, "selected", **many) == li.EINVAL
+    assert b"too large for one launch" in lib.indexer_last_error()
+
+
 def test_attend_needs_its_workspace(lib):
     need = li.mx4_attend_workspace_bytes(1, 1, 131072, False, 64, 8, 128)
     assert need > 0 and need % 256 == 0

@@ -392,6 +392,28 @@ def test_pairs_of_heads(query, heads, kv, d, bs, kind):
     run_selected(case, selection(case, 70), where=where + " NaN")
 
 
+# Sizes at which a wave has the codes of two tiles on the way (129 to 256 pairs of
+# a row tile and a K/V head, room for at least 2048 keys), its tiles none to many
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("heads,kv,d,bs", [(16, 16, 64, 16), (80, 16, 128, 7), (48, 16, 96, 32)])
+def test_two_tiles_ahead(heads, kv, d, bs, kind):
+    lens = [0, 1, 31, 33, 256, 257, 300, 513, 544, 600, 767, 800, 1025, 40, 900, 1300]
+    case = Case(46, lens, 1, heads, kv, d, bs, kind)
+    case.max_seq_len = 2100
+    more = -(-2100 // bs) - case.table.shape[1]
+    case.table = np.concatenate([case.table, np.full((16, more), -1, dtype=np.int32)], 1)
+    where = f"two ahead {heads}/{kv} {d} {kind}"
+    run_window(case, 0, 0, where=where)
+    run_window(case, 2000, 90, where=where + " window")
+    run_selected(case, selection(case, 2048), where=where + " selected")
+    run_selected(case, selection(case, 256, 9), 9, where=where + " pooled")
+    for which, head, key, block in ((1, 3, 0, 0), (1, 4, 20, d // 32 - 1), (0, 6, 5, 0)):
+        for r in (7, 9, 15):
+            case.scale[which][case.table[r, key // bs], key % bs, head, block] = 255
+    out, _ = run_window(case, 0, 0, where=where + " NaN")
+    assert torch.isnan(out).any()
+
+
 # Sizes at which the waves of a workgroup take 2, 4 and 8 K/V heads (more than 16
 # query rows a head and request, workgroups that fill the chip)
 @pytest.mark.parametrize("requests,kv,kind", [(64, 8, "f16"), (128, 8, "bf16"), (240, 8, "f16"), (120, 2, "bf16")])

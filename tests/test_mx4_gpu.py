@@ -583,6 +583,161 @@ def test_shared_keys_and_split_rows_agree():
     run_selected(case, selection(case, 2048), where="split selection")
 
 
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("heads,kv,d", [(3, 1, 64), (20, 2, 96), (5, 1, 192), (40, 2, 256), (17, 1, 256), (4, 4, 128)])
+def test_shared_keys_at_every_head_dimension(heads, kv, d, kind):
+    """Rows whose keys several workgroups share, each form."""
+    case = Case(47, [3300, 2000], 1, heads, kv, d, 32, kind)
+    where = f"shares {heads}/{kv} {d} {kind}"
+    assert li.mx4_attend_workspace_bytes(2, 1, 3300, False, heads, kv, d) > 0
+    run_window(case, 0, 0, where=where)
+    run_window(case, 1700, 65, where=where + " window")
+    run_selected(case, selection(case, 2000), where=where + " selected")
+    run_selected(case, selection(case, 60, 32), 32, where=where + " pooled")
+    case.scale[1][case.table[0, 10], 5, kv - 1, d // 32 - 1] = 255
+    case.scale[0][case.table[1, 7], 3, 0, 0] = 255
+    run_window(case, 0, 0, where=where + " NaN")
+
+
+def laid_out(case, how):
+    """The case's cache in other layouts of the same values."""
+    q, kd, ks, vd, vs, table, lens, Q = case.args()
+    B, bs, H, w = kd.shape
+    sw = ks.shape[3]
+    if how == "scales by head":
+        ks, vs = (t.transpose(1, 2).contiguous().transpose(1, 2) for t in (ks, vs))
+    elif how == "scales of a slot together":
+        both = torch.stack([ks, vs], 2)
+        ks, vs = both[:, :, 0], both[:, :, 1]
+    elif how == "one record a slot":
+        rec = torch.zeros((B, bs, 2 * H * (w + sw) + 16 - 2 * H * (w + sw) % 16), dtype=torch.uint8, device=DEV)
+        step = (bs * rec.shape[2], rec.shape[2])
+        parts = [rec.as_strided((B, bs, H, x), step + (x, 1), at)
+                 for x, at in ((w, 0), (w, H * w), (sw, 2 * H * w), (sw, 2 * H * w + H * sw))]
+        for part, t in zip(parts, (kd, vd, ks, vs)):
+            part.copy_(t)
+        kd, vd, ks, vs = parts
+    elif how == "scales at odd addresses":
+        pad = [torch.zeros((B, bs, H, sw + 1), dtype=torch.uint8, device=DEV) for _ in range(2)]
+        for p, t in zip(pad, (ks, vs)):
+            p[..., 1:] = t
+        ks, vs = pad[0][..., 1:], pad[1][..., 1:]
+    return q, kd, ks, vd, vs, table, lens, Q
+
+
+@pytest.mark.parametrize("how", ["scales by head", "scales of a slot together", "one record a slot",
+                                 "scales at odd addresses"])
+@pytest.mark.parametrize("lens,query,heads,kv,d", [
+    ([130, 77], 2, 8, 4, 96),                    # a head at a time
+    ([60] * 64, 1, 64, 16, 128),                 # two heads at a time
+    ([3000, 900], 1, 16, 2, 128),                # shared keys
+    ([200] * 16, 32, 32, 8, 64),                 # many rows
+    ([300] * 16, 1, 32, 16, 64),                 # two tiles ahead
+])
+def test_layouts_of_the_cache(lens, query, heads, kv, d, how):
+    case = Case(48, lens, query, heads, kv, d, 16, "bf16")
+    if heads == 32 and kv == 16:
+        case.max_seq_len = 2048
+        case.table = np.concatenate([case.table, np.full((16, 128 - case.table.shape[1]), -1, dtype=np.int32)], 1)
+    idx = torch.from_numpy(selection(case, 50)).to(DEV)
+    results = []
+    for layout in ("as made", how):
+        args = laid_out(case, layout)
+        results.append(li.mx4_attend_window(*args, case.max_seq_len, case.sm_scale) +
+                       li.mx4_attend_window(*args, case.max_seq_len, case.sm_scale, window=40, sinks=3) +
+                       li.mx4_attend_selected(*args, idx, case.sm_scale))
+    for a, b in zip(*results):
+        assert torch.equal(a, b), how
+
+
+def test_a_cache_of_more_than_four_gigabytes():
+    """Pages whose bytes lie past 2^32: written, read back and attended to as in a small cache."""
+    bs, kv, d = 64, 8, 256
+    n_blocks = (2**32 + 2**27) // (bs * kv * d // 2)
+    def make(blocks):  # noqa: E306
+        return [torch.empty((blocks, bs, kv, w), dtype=torch.uint8, device=DEV) for w in (d // 2, d // 32) * 2]
+    big, small = make(n_blocks), make(4)
+    assert big[0].numel() > 2**32
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(5)
+    k, v = (torch.randn((200, kv, d), generator=gen, device=DEV).half() for _ in range(2))
+    pages = torch.tensor([n_blocks - 1, 2, n_blocks - 3, n_blocks - 2], device=DEV)
+    at = torch.arange(200, device=DEV)
+    for cache, table in ((big, pages), (small, torch.arange(4, device=DEV))):
+        li.mx4_cache_write(k, table[at // bs] * bs + at % bs, cache[0], cache[1], v, cache[2], cache[3])
+    slots = pages[at // bs] * bs + at % bs
+    assert torch.equal(li.mx4_cache_read(big[2], big[3], slots), li.mx4_cache_read(small[2], small[3], at))
+    q = torch.randn((40, 16, d), generator=gen, device=DEV).half()
+    lens = torch.tensor([200], dtype=torch.int32, device=DEV)
+    idx = torch.randint(0, 160, (40, 70), generator=gen, device=DEV, dtype=torch.int32)
+    results = []
+    for cache, table in ((big, pages), (small, torch.arange(4, device=DEV))):
+        args = (q, *cache, table.int()[None], lens, 40)
+        results.append(li.mx4_attend_window(*args, 200, 0.06) + li.mx4_attend_selected(*args, idx, 0.06))
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+    # the many-rows form, at a head dimension that has it
+    rows = [torch.empty_like(big[0]).view(-1, bs, kv, 64), torch.empty_like(big[1]).view(-1, bs, kv, 4)]
+    few = [t[-8:].clone().random_(100, 130) for t in rows]
+    for t, f in zip(rows, few):
+        t[-8:] = f
+    q = torch.randn((2048, 16, 128), generator=gen, device=DEV).half()
+    lens = torch.full((16,), 300, dtype=torch.int32, device=DEV)
+    own = torch.randint(0, 8, (16, 5), generator=gen, device=DEV)
+    got = [li.mx4_attend_window(q, t[0], t[1], t[0], t[1], (own + t[0].shape[0] - 8).int(), lens, 128, 300, 0.09)
+           for t in (rows, few)]
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+def test_slots_past_32_bits():
+    """A cache of more than 2^31 slots (of one head of 32 values)."""
+    n = 2**31 + 4096
+    if torch.cuda.mem_get_info()[0] < 60 * 2**30:
+        pytest.skip("needs 60 GiB of free GPU memory")
+    data = torch.empty((n // 64, 64, 1, 16), dtype=torch.uint8, device=DEV)
+    scale = torch.empty((n // 64, 64, 1, 1), dtype=torch.uint8, device=DEV)
+    x, v = typed(np.random.default_rng(6).standard_normal((6, 1, 32)), "f16")
+    slots = torch.tensor([n - 1, 2**31, 2**31 - 1, 5, n, -1], device=DEV)
+    data.view(-1, 16)[-4097:] = 0xA5
+    li.mx4_cache_write(x.to(DEV), slots, data, scale)
+    got = li.mx4_cache_read(data, scale, slots)
+    want = plain.values(*plain.quantise(v, "f16"))
+    want[4:] = 0.0
+    assert np.array_equal(got.double().cpu().numpy(), want)
+    assert (data.view(-1, 16)[-4095:-1] == 0xA5).all()
+    del data, scale
+    torch.cuda.empty_cache()
+
+
+def test_largest_windows():
+    case = Case(49, [90, 40], 2, 8, 2, 64, 16, "f16")
+    whole = run_window(case, 0, 0)
+    top = 2**31 - 1
+    for window, sinks in ((top, 0), (top, top), (1, top)):
+        got = run_window(case, window, sinks, where=f"{window} {sinks}")
+        assert torch.equal(got[0], whole[0]) and torch.equal(got[1], whole[1])
+    with pytest.raises(ValueError):
+        run_window(case, top + 1, 0)
+
+
+def test_calls_at_once_on_two_streams():
+    """Calls with shares of their rows in workspaces, side by side."""
+    cases = [Case(50 + i, [4000 + 500 * i], 1, 16, 2, 128, 64, "f16") for i in range(2)]
+    args = [c.args() for c in cases]
+    want = [li.mx4_attend_window(*a, c.max_seq_len, c.sm_scale) for a, c in zip(args, cases)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(10):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(li.mx4_attend_window(*args[i], cases[i].max_seq_len, cases[i].sm_scale))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for out, lse in got[i]:
+            assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])
+
+
 def test_pool_and_selection_of_the_whole_row_equal_the_causal_form():
     case = Case(20, [256], 1, 8, 2, 128, 16, "f16")
     whole, _ = run_window(case, 0, 0)

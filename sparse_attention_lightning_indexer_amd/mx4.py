@@ -42,9 +42,9 @@ _types = {}        # torch dtype -> the library's type code
 
 def _library():
     global _lib, _torch
+    if _lib is not None:
+        return _lib
     lib = _pkg.load_library()
-    if _lib is lib:
-        return lib
     for name in MX4_EXPORTS[:4]:
         f = getattr(lib, name)
         f.argtypes, f.restype = [ctypes.c_char_p], ctypes.c_int   # a packed argument structure
@@ -119,6 +119,15 @@ def _cache(data, scale, name, dev, heads, d):
     return blocks, size, db, ds, dh, sb, ss, sh
 
 
+def _like(data, scale, k_data, k_scale, dev):
+    """Whether V's cache is as K's, which was checked."""
+    tensor, uint8 = _torch.Tensor, _torch.uint8
+    return (isinstance(data, tensor) and isinstance(scale, tensor) and data.dtype is uint8 and scale.dtype is uint8
+            and data.get_device() == dev and scale.get_device() == dev and data.shape == k_data.shape
+            and scale.shape == k_scale.shape and data.stride() == k_data.stride()
+            and scale.stride() == k_scale.stride())
+
+
 def _slots(slots, n, dev):
     _need(slots, "slots", _torch.int64, dev, 1)
     if slots.shape[0] != n:
@@ -164,7 +173,7 @@ def mx4_cache_write(k, slots, k_data, k_scale, v=None, v_data=None, v_scale=None
     v_args, v_strides = (0, 0), (0, 0)
     if v is not None and v_data is not None and v_scale is not None:
         v_strides = _rows(v, "v", k.dtype, dev, shape)
-        if _cache(v_data, v_scale, "v", dev, heads, d) != pages:
+        if not _like(v_data, v_scale, k_data, k_scale, dev) and _cache(v_data, v_scale, "v", dev, heads, d) != pages:
             raise ValueError("the K and V caches must have the same shape and strides")
         v_args = (v_data.data_ptr(), v_scale.data_ptr())
     elif v is not None or v_data is not None or v_scale is not None:
@@ -195,7 +204,7 @@ def mx4_cache_read(data, scale, slots, dtype=None, out=None):
     n = slots.shape[0]
     _slots(slots, n, dev)
     if out is None:
-        out = _torch.empty((n, heads, d), dtype=dtype, device=data.device)
+        out = data.new_empty((n, heads, d), dtype=dtype)
     strides = _rows(out, "out", dtype, dev, (n, heads, d))
     if n == 0 or heads == 0 or d == 0:
         return out
@@ -227,7 +236,7 @@ def _attend(entry, q, k_data, k_scale, v_data, v_scale, block_table, seq_lens, q
         raise ValueError("k_data must be [n_blocks, block_size, n_kv_heads, head_dim/2]")
     kv = k_data.shape[2]
     pages = _cache(k_data, k_scale, "k", dev, kv, d)
-    if _cache(v_data, v_scale, "v", dev, kv, d) != pages:
+    if not _like(v_data, v_scale, k_data, k_scale, dev) and _cache(v_data, v_scale, "v", dev, kv, d) != pages:
         raise ValueError("the K and V caches must have the same shape and strides")
     _need(block_table, "block_table", torch.int32, dev, 2)
     _need(seq_lens, "seq_lens", torch.int32, dev, 1)
@@ -244,7 +253,7 @@ def _attend(entry, q, k_data, k_scale, v_data, v_scale, block_table, seq_lens, q
     if rows != requests * query_len:
         raise ValueError(f"q has {rows} rows, expected n_requests*query_len = {requests * query_len}")
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=q.device)
+        out = q.new_empty(shape)
         out_strides = (heads * d, d)
     else:
         out_strides = _rows(out, "out", dtype, dev, shape)
@@ -253,7 +262,7 @@ def _attend(entry, q, k_data, k_scale, v_data, v_scale, block_table, seq_lens, q
         if lse.shape != (rows, heads) or not lse.is_contiguous():
             raise ValueError(f"lse must be contiguous [{rows}, {heads}]")
     elif with_lse:
-        lse = torch.empty((rows, heads), dtype=torch.float32, device=q.device)
+        lse = q.new_empty((rows, heads), dtype=torch.float32)
     if workspace is not None:
         _need(workspace, "workspace", torch.uint8, dev, 1)
         if not workspace.is_contiguous():
@@ -263,7 +272,7 @@ def _attend(entry, q, k_data, k_scale, v_data, v_scale, block_table, seq_lens, q
     if workspace is None:
         need = _lib.indexer_mx4_attend_workspace_bytes(requests, query_len, max_keys, selected, heads, kv, d)
         if 0 < need < 2**63:  # sizes the library refuses have none: the call below names them
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            workspace = q.new_empty(need, dtype=torch.uint8)
     blocks, size, *strides = pages
     _call(dev, entry, _pack(
         ATTEND, q.data_ptr(), *q_strides, k_data.data_ptr(), k_scale.data_ptr(), v_data.data_ptr(),

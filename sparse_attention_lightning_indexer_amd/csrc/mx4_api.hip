@@ -161,8 +161,13 @@ indexer_status run_attend(lidx::Mx4Attend &a, const indexer_mx4_attend_args &g, 
     void *workspace = g.workspace;
     hipStream_t stream = (hipStream_t)g.stream;
     const bool selected = a.idx != nullptr;
-    const lidx::Mx4Plan p = lidx::plan_mx4_attend(a.n_requests, a.q_len, max_keys, selected, a.n_heads, a.n_kv,
-                                                  head_dim);
+    lidx::Mx4Plan p =
+        lidx::plan_mx4_attend(a.n_requests, a.q_len, max_keys, selected, a.n_heads, a.n_kv, head_dim);
+    // shared scales are loaded in whole 16-byte parts, those of 8 heads one after
+    // the other; the order of the sums is the same either way
+    const lidx::Mx4Pages &pages = a.pages;
+    p.share = p.hp == 2 && p.head_group == 4 && (head_dim == 64 || head_dim == 128) && pages.s_sh == head_dim / 32 &&
+              pages.s_ss % 16 == 0 && pages.s_sb % 16 == 0 && aligned(a.ks, 16) && aligned(a.vs, 16);
     // a launch holds fewer than 2^32 threads
     if (p.workgroups * 512 > UINT32_MAX || (p.n_splits > 1 && (int64_t)a.rows * a.n_heads * 256 > UINT32_MAX))
         MX4_FAIL(INDEXER_EINVAL, "problem too large for one launch: %lld workgroups", (long long)p.workgroups);
@@ -235,6 +240,21 @@ static Mx4Plan sized(Mx4Plan p, int64_t rows, int n_heads, int n_kv, int head_di
 // 2048 52 and 39, 16 tokens of 32 requests over 4096 115 and 128, 4 tokens of
 // them 106 and 41.
 //
+// Where a row's pairs of heads make a multiple of four and the rows fill the
+// chip, the four waves of a workgroup take the same keys of four pairs, instead
+// of different keys of one: nothing has to be joined, and (where the cache's
+// layout allows, see run_attend) the waves share the keys' scales.  Measured,
+// same and different keys, head dimension 128: 1024 rows x 2048 keys, 8 heads
+// 390 and 450 us, 512 rows 206 and 218, 448 rows 200 and 198, 256 rows 143 and
+// 123; 640, 512 and 384 rows x 512 keys 80 and 86, 63 and 71, 57 and 56; 256
+// rows x 64 keys 11.7 and 17.3, 192 rows 11.2 and 11.6.  Head dimension 64, 2048
+// keys: 512 rows of 8 heads 135 and 127, 384 rows of 16 heads 179 and 195, 320
+// rows of them 166 and 163; 256 rows of 8 heads x 64 keys 8.6 and 11.5.  Head
+// dimension 96, which does not share: 1024 rows x 2048 keys 363 and 457.  So from
+// two workgroups a compute unit on (three below head dimension 128), or one
+// where a wave has at most four tiles.  Workgroups that would share the scales
+// but cannot take 443 us where those that do take 390.
+//
 // Otherwise the 8 waves of a workgroup take the same keys of
 // several K/V heads where the workgroups that leaves still fill whole rounds of
 // the compute units (one at a time fits one): 1000 rows over a window of 4096
@@ -270,6 +290,13 @@ Mx4Plan plan_mx4_attend(int n_requests, int q_len, int64_t max_keys, bool select
             p.m_tiles = (int)tiles;
         }
         if (p.prompt) return sized(p, rows, n_heads, n_kv, head_dim);
+    }
+    const int64_t wgs = (int64_t)p.units * (n_kv / 8);
+    if (selected && p.hp == 2 && n_kv % 8 == 0 && wgs >= (max_keys <= 128 ? kCus : (head_dim == 128 ? 2 : 3) * kCus)) {
+        p.head_group = 4;
+        p.n_splits = 1;
+        p.ahead = 1;
+        return sized(p, rows, n_heads, n_kv, head_dim);
     }
     const int waves = head_dim <= 128 && p.hp == 1 ? 8 : 4;
     const int64_t items = (int64_t)p.units * p.m_tiles * (n_kv / p.hp);

@@ -28,6 +28,13 @@
 //    read back transposed (ds_read_b64_tr_b16), 16 dimensions by 4 keys each.
 //    Rows are padded by 32 bytes: the 8 consecutive rows that half a wave reads
 //    32 bytes of, or writes 16 bytes of, then lie in different banks.
+//  - Keys picked one by one come from beyond the L2s, in lines of 128 bytes: a
+//    row of 4 bytes of scales costs what two rows of codes do.  Where the four
+//    waves of a workgroup take the same keys of 8 K/V heads (SHARE), the scales
+//    of all heads come in one load for 64 keys at a time, through LDS, one
+//    barrier for them: 10 lines a key instead of up to 16.  1024 rows x 2048 of
+//    131072 keys, 8 heads of 128: 450 us apart, 390-410 us shared, when 2.6 GB
+//    pass the L2s at 6.5 TB/s, as fast as this card reads memory.
 //  - Loads run ahead: a tile's codes from when the one before (PF = 2: two
 //    before) is converted, the page ids a pair of tiles further, the selected
 //    indices one more.
@@ -200,16 +207,21 @@ struct Set {
     static constexpr int value = N;
 };
 
-template <bool BF16, int D, int MT, int HP, int PF, int MODE>
+template <bool BF16, int D, int MT, int HP, int PF, int MODE, bool SHARE>
 __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D, MT, HP, PF>())) mx4_attend_kernel(Mx4Attend a) {
     static_assert(HP == 1 || MT == 1, "pairs of heads have one tile of rows");
     static_assert(HP == 1 || PF == 1, "a pair's second 16 keys are asked for late");
+    static_assert(!SHARE || (HP == 2 && MODE != kWindow && (D == 64 || D == 128)), "shared scales: pairs of heads of selected rows");
     using T = Type<BF16>;
     using S = Shape<D, HP>;
     typedef typename T::vec8 vec8;
     constexpr int KS = S::KS, NT = S::NT, W = S::WAVES, NU = S::NU, KPL = S::KPL;
     constexpr bool SELECTED = MODE != kWindow;
     __shared__ __attribute__((aligned(16))) unsigned char smem[S::LDS];
+    // SHARE: the scales of a pair of tiles and of the one after, of all the
+    // workgroup's heads: 16-byte parts of K's, then of V's, each for the 64 keys
+    constexpr int PARTS = D / 64;
+    __shared__ u32x4 scales[SHARE ? 2 : 1][SHARE ? 2 * PARTS : 1][64];
 
     Item it = item_of(a, MT, HP);
     if (it.unit >= a.units) return;
@@ -332,13 +344,13 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
         if (!a.pages.congruent) sat = (uint64_t)pg * (uint32_t)a.pages.s_sb + __umul24(o, (uint32_t)a.pages.s_ss);
         found = __ballot(ok);
     };
-    // from the lane that found this lane's key of load u of tile `b` of the pair
-    auto ask = [&](uint64_t v, int b, int u) -> uint64_t {
-        const int who = (b * 32 + u * KPL + krow) * 4;
-        const uint32_t lo = (uint32_t)__builtin_amdgcn_ds_bpermute(who, (int)(uint32_t)v);
-        const uint32_t hi = (uint32_t)__builtin_amdgcn_ds_bpermute(who, (int)(uint32_t)(v >> 32));
+    auto ask_lane = [&](uint64_t v, int from) -> uint64_t {
+        const uint32_t lo = (uint32_t)__builtin_amdgcn_ds_bpermute(from * 4, (int)(uint32_t)v);
+        const uint32_t hi = (uint32_t)__builtin_amdgcn_ds_bpermute(from * 4, (int)(uint32_t)(v >> 32));
         return ((uint64_t)hi << 32) | lo;
     };
+    // from the lane that found this lane's key of load u of tile `b` of the pair
+    auto ask = [&](uint64_t v, int b, int u) -> uint64_t { return ask_lane(v, b * 32 + u * KPL + krow); };
     // 5: the codes and scales.  The KS words (8 values each) of quarter c lie in
     // blocks (c * KS + s) / 4: at most NB of them
     constexpr int NB = KS % 4 == 0 ? KS / 4 : (KS == 2 ? 1 : 2);
@@ -357,6 +369,7 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
         const uint64_t row = ask(at, b, u), d = row + chunk;
         if (k) __builtin_memcpy(raw[u].k, __builtin_assume_aligned(kd + d, ALIGN), KS * 4);
         if (v) __builtin_memcpy(raw[u].v, __builtin_assume_aligned(vd + d, ALIGN), KS * 4);
+        if (SHARE) return;
         const uint64_t sc = (a.pages.congruent ? row >> 4 : ask(sat, b, u)) + schunk;
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
@@ -366,6 +379,24 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
             if (v) raw[u].sv[n] = vs[sc + more];
         }
     };
+    // SHARE: thread (key, part) of the workgroup asks for its part of the
+    // scales of the pair that was located last, and puts it into LDS
+    u32x4 part = {0u, 0u, 0u, 0u};
+    const int part_key = (int)threadIdx.x / (2 * PARTS), part_of = (int)threadIdx.x % (2 * PARTS);
+    auto load_part = [&]() {
+        const uint64_t row = ask_lane(a.pages.congruent ? at >> 4 : sat, part_key & 63);
+        const uint8_t *src = (part_of < PARTS ? a.ks : a.vs) + (uint32_t)first_kv * (uint32_t)a.pages.s_sh;
+        part = *reinterpret_cast<const u32x4 *>(src + row + (part_of & (PARTS - 1)) * 16);
+    };
+    auto store_part = [&](int buffer) {
+        if (2 * PARTS * 64 == W * 64 || part_key < 64) scales[buffer][part_of][part_key & 63] = part;
+    };
+    // the byte of block `blk` of the workgroup's head `hd` (tensor 0: K, 1: V)
+    auto shared_scale = [&](int buffer, int tensor, int key, int hd, int blk) -> uint32_t {
+        const int byte = hd * (D / 32) + blk;
+        return ((const __attribute__((address_space(3))) uint8_t *)&scales[buffer][tensor * PARTS + (byte >> 4)][key])[byte & 15];
+    };
+    int buffer = 0;
     // which of the blocks of quarter c its word s belongs to
     auto block_of = [&](int c, int s) { return KS % 4 == 0 ? s / 4 : (KS == 2 ? 0 : (c * KS + s) / 4 - c * KS / 4); };
 
@@ -396,6 +427,7 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
         pos = position(t_begin, id);
         page = load_page(pos);
         locate(pos, page);
+        if (SHARE) load_part();
 #pragma unroll
         for (int b = 0; b < PF; ++b) {
             have[b] = (uint32_t)(found >> (b * 32));
@@ -413,6 +445,10 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
             following(t_begin + 4 * stride);
         }
         if (SELECTED) id = load_index(t_begin + (PF == 2 ? 6 : 4) * stride);
+        if (SHARE) {
+            store_part(0);
+            __syncthreads();
+        }
     }
 
     // one tile: `b` is its place in its pair, SET where its codes are
@@ -436,6 +472,11 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
             return in;
         };
 
+        if (SHARE) {
+#pragma unroll
+            for (int u = 0; u < NU; ++u)
+                raw_[u].sv[0] = shared_scale(buffer, 1, b * 32 + u * KPL + krow, it.kv - first_kv + hsel, blk0);
+        }
         // V's scales: 0 for keys that do not count and blocks of NaN (rare), and
         // a mark for the rows that do attend to such a block
         bool bad = false;
@@ -489,7 +530,7 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
         // scales, a byte per load in one word: lane (row, head, quarter) has them
         uint32_t pack[NB];
 #pragma unroll
-        for (int n = 0; n < NB; ++n) {
+        for (int n = 0; n < (SHARE ? 0 : NB); ++n) {
             pack[n] = raw_[0].sk[n];
 #pragma unroll
             for (int u = 1; u < NU; ++u) pack[n] |= raw_[u].sk[n] << (8 * u);
@@ -501,13 +542,14 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
         for (int hh = 0; hh < HP; ++hh) {
             uint32_t sk[NB];
 #pragma unroll
-            for (int n = 0; n < NB; ++n) {
+            for (int n = 0; n < (SHARE ? 0 : NB); ++n) {
                 const int who = ((col & (KPL - 1)) * 4 * HP + hh * 4 + qd) * 4;
                 sk[n] = (uint32_t)__builtin_amdgcn_ds_bpermute(who, (int)pack[n]) >> (HP == 2 ? 8 * hcol : 0);
             }
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                uint32_t kc[KS], w1[K1], w2[K2];
+                uint32_t kc[KS], w1[K1], w2[K2], shared_k = 0;
+                if (SHARE) shared_k = shared_scale(buffer, 0, b * 32 + u * 16 + col, it.kv - first_kv + hh, qd * KS / 4);
                 const lds_u8 *src = stage + hh * HEAD + u * TILE;
                 get_words<K1>(src + unit_at(col, U == 4 ? qd : qd * 2), w1);
 #pragma unroll
@@ -522,10 +564,15 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
                 for (int mt = 0; mt < MT; ++mt) sum[mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int st = 0; st < KS; ++st) {
-                    uint32_t sb = sk[0];
+                    uint32_t sb;
+                    if constexpr (SHARE) {
+                        sb = shared_k;
+                    } else {
+                        sb = sk[0];
 #pragma unroll
-                    for (int b = 1; b < NB; ++b) sb = block_of(qd, st) == b ? sk[b] : sb;
-                    sb = (sb >> (8 * HP * u)) & 255u;
+                        for (int b = 1; b < NB; ++b) sb = block_of(qd, st) == b ? sk[b] : sb;
+                        sb = (sb >> (8 * HP * u)) & 255u;
+                    }
                     const vec8 kv = T::from4(kc[st], __builtin_bit_cast(float, sb << 23));
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) sum[mt] = T::mfma(kv, q[mt][st], sum[mt]);
@@ -565,6 +612,7 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
             if (nb == 0) return;
             const int first = tile - b * stride;  // of this pair
             locate(pos, page);
+            if (SHARE) load_part();
             pos = position(first + (PF == 2 ? 6 : 4) * stride, id);
             page = load_page(pos);
             if (SELECTED) id = load_index(first + (PF == 2 ? 8 : 6) * stride);
@@ -652,7 +700,13 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
         }
     } else {
         int odd = 0;
-        for (int tile = t_begin; tile < t_end; tile += stride, odd ^= 1) multiply(Set<0>{}, odd, tile);
+        for (int tile = t_begin; tile < t_end; tile += stride, odd ^= 1) {
+            multiply(Set<0>{}, odd, tile);
+            if (SHARE && odd) {  // the same tiles in every wave; nobody reads the other buffer any more
+                store_part(buffer ^= 1);
+                __syncthreads();
+            }
+        }
     }
 
     // join the waves: each writes its product, m and l; every thread then adds
@@ -1078,15 +1132,15 @@ __global__ void __launch_bounds__(256) mx4_join_kernel(Mx4Attend a) {
     *reinterpret_cast<vec8 *>((uint16_t *)a.out + token * a.out_st + (int64_t)head * a.out_sh + threadIdx.x * 8) = r;
 }
 
-template <bool BF16, int D, int MT, int HP, int PF>
+template <bool BF16, int D, int MT, int HP, int PF, bool SHARE = false>
 hipError_t launch_tiles(const Mx4Attend &a, const Mx4Plan &p, hipStream_t stream) {
     const dim3 grid((unsigned)p.workgroups), block(Shape<D, HP>::WAVES * 64);
     if (!a.idx)
-        hipLaunchKernelGGL((mx4_attend_kernel<BF16, D, MT, HP, PF, kWindow>), grid, block, 0, stream, a);
+        hipLaunchKernelGGL((mx4_attend_kernel<BF16, D, MT, HP, PF, kWindow, false>), grid, block, 0, stream, a);
     else if (a.pool == 1)
-        hipLaunchKernelGGL((mx4_attend_kernel<BF16, D, MT, HP, PF, kKeys>), grid, block, 0, stream, a);
+        hipLaunchKernelGGL((mx4_attend_kernel<BF16, D, MT, HP, PF, kKeys, SHARE>), grid, block, 0, stream, a);
     else
-        hipLaunchKernelGGL((mx4_attend_kernel<BF16, D, MT, HP, PF, kPools>), grid, block, 0, stream, a);
+        hipLaunchKernelGGL((mx4_attend_kernel<BF16, D, MT, HP, PF, kPools, SHARE>), grid, block, 0, stream, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.n_splits == 1) return e;
     hipLaunchKernelGGL((mx4_join_kernel<BF16, D>), dim3((unsigned)(a.rows * a.n_heads)), dim3(256), 0, stream, a);
@@ -1103,6 +1157,9 @@ hipError_t launch_dim(const Mx4Attend &a, const Mx4Plan &p, hipStream_t stream) 
             hipLaunchKernelGGL((mx4_join_kernel<BF16, D>), dim3((unsigned)(a.rows * a.n_heads)), dim3(256), 0, stream,
                                a);
             return hipGetLastError();
+        }
+        if constexpr (D != 96) {
+            if (p.share) return launch_tiles<BF16, D, 1, 2, 1, true>(a, p, stream);
         }
         if (p.hp == 2) return launch_tiles<BF16, D, 1, 2, 1>(a, p, stream);
     }

@@ -650,6 +650,40 @@ def test_layouts_of_the_cache(lens, query, heads, kv, d, how):
         assert torch.equal(a, b), how
 
 
+# Sizes at which a workgroup takes a selected row's keys at 8 K/V heads and shares
+# their scales (K/V heads a multiple of 8, rows * K/V heads / 8 >= 256 for at most
+# 128 keys, 512 or (head dimension 64) 768 for more), tiles of keys none to seven
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("query,heads,kv,d,bs", [(4, 64, 64, 128, 16), (4, 128, 64, 128, 7), (6, 64, 64, 64, 16),
+                                                 (12, 128, 32, 64, 33)])
+def test_shared_scales(query, heads, kv, d, bs, kind):
+    lens = [0, 1, 2, 31, 35, 63, 64, 69, 96, 97, 127, 131, 160, 162, 190, 200]
+    case = Case(49, lens, query, heads, kv, d, bs, kind)
+    where = f"shared scales {query} {heads}/{kv} {d} {kind}"
+    run_selected(case, selection(case, 70), where=where + " few")
+    run_selected(case, selection(case, 1), where=where + " one")
+    run_selected(case, selection(case, 200), where=where + " many")
+    run_selected(case, selection(case, 23, 9), 9, where=where + " pooled")
+    run_selected(case, np.full((case.q.shape[0], 40), -1, dtype=np.int32), where=where + " none")
+    case.table[12, 1], case.table[14, 2], case.table[15, 0] = -1, case.n_blocks, 2**31 - 1
+    # NaN: of one head only, in keys some rows see and others do not
+    for which, head, key, block in ((1, 3, 0, 0), (1, 12, 20, d // 32 - 1), (0, 6, 5, 0), (1, 17, 17, 1), (0, 31, 60, 1)):
+        for r in (6, 9, 13):
+            if key < lens[r]:
+                case.scale[which][case.table[r, key // bs], key % bs, head, block] = 255
+    out, lse = run_selected(case, selection(case, 200), where=where + " NaN")
+    assert torch.isnan(out).any() and torch.isnan(lse).any() and not torch.isnan(out[-query:]).any()
+    idx = selection(case, 90)
+    first = run_selected(case, idx, where=where + " NaN, few")
+    want = case.want(lambda t, v, e: plain.positions_selected(idx[t], 1, e))
+    for how in ("scales of a slot together", "one record a slot", "scales by head", "scales at odd addresses"):
+        got = li.mx4_attend_selected(*laid_out(case, how), torch.from_numpy(idx).to(DEV), case.sm_scale)
+        check(got, want, kind, d, f"{where} {how}")
+        if how in ("scales of a slot together", "one record a slot"):    # shared there too
+            for a, b in zip(first, got):
+                assert torch.equal(a.view(torch.int16), b.view(torch.int16)), how
+
+
 def test_a_cache_of_more_than_four_gigabytes():
     """Pages whose bytes lie past 2^32: written, read back and attended to as in a small cache."""
     bs, kv, d = 64, 8, 256

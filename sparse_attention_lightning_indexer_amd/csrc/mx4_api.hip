@@ -166,7 +166,7 @@ indexer_status run_attend(lidx::Mx4Attend &a, const indexer_mx4_attend_args &g, 
     // shared scales are loaded in whole 16-byte parts, those of 8 heads one after
     // the other; the order of the sums is the same either way
     const lidx::Mx4Pages &pages = a.pages;
-    p.share = p.hp == 2 && p.head_group == 4 && (head_dim == 64 || head_dim == 128) && pages.s_sh == head_dim / 32 &&
+    p.share = selected && p.hp == 2 && p.head_group == 4 && (head_dim == 64 || head_dim == 128) && pages.s_sh == head_dim / 32 &&
               pages.s_ss % 16 == 0 && pages.s_sb % 16 == 0 && aligned(a.ks, 16) && aligned(a.vs, 16);
     // a launch holds fewer than 2^32 threads
     if (p.workgroups * 512 > UINT32_MAX || (p.n_splits > 1 && (int64_t)a.rows * a.n_heads * 256 > UINT32_MAX))
@@ -253,7 +253,10 @@ static Mx4Plan sized(Mx4Plan p, int64_t rows, int n_heads, int n_kv, int head_di
 // dimension 96, which does not share: 1024 rows x 2048 keys 363 and 457.  So from
 // two workgroups a compute unit on (three below head dimension 128), or one
 // where a wave has at most four tiles.  Workgroups that would share the scales
-// but cannot take 443 us where those that do take 390.
+// but cannot take 443 us where those that do take 390.  Under a window, whose
+// keys lie side by side, only few keys are worth it: 512 rows over 64, 128, 512
+// and 2048 keys 17, 24, 66 and 248 us with the same keys, 26, 30, 68 and 233 us
+// with different ones.
 //
 // Otherwise the 8 waves of a workgroup take the same keys of
 // several K/V heads where the workgroups that leaves still fill whole rounds of
@@ -292,7 +295,8 @@ Mx4Plan plan_mx4_attend(int n_requests, int q_len, int64_t max_keys, bool select
         if (p.prompt) return sized(p, rows, n_heads, n_kv, head_dim);
     }
     const int64_t wgs = (int64_t)p.units * (n_kv / 8);
-    if (selected && p.hp == 2 && n_kv % 8 == 0 && wgs >= (max_keys <= 128 ? kCus : (head_dim == 128 ? 2 : 3) * kCus)) {
+    if (p.hp == 2 && n_kv % 8 == 0 &&
+        (max_keys <= 128 ? wgs >= kCus : selected && wgs >= (head_dim == 128 ? 2 : 3) * kCus)) {
         p.head_group = 4;
         p.n_splits = 1;
         p.ahead = 1;

@@ -684,6 +684,26 @@ def test_shared_scales(query, heads, kv, d, bs, kind):
                 assert torch.equal(a.view(torch.int16), b.view(torch.int16)), how
 
 
+# Sizes at which they take the same keys under a window (requests * K/V heads / 8
+# >= 256, at most 128 keys)
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("query,heads,kv,d,bs", [(1, 128, 64, 128, 16), (2, 64, 64, 96, 7), (3, 128, 64, 64, 33)])
+def test_same_keys_under_a_window(query, heads, kv, d, bs, kind):
+    lens = [0, 1, 2, 31, 32, 33, 63, 64, 65, 96, 97, 127, 128, 129, 149, 150] * 2
+    case = Case(50, lens, query, heads, kv, d, bs, kind)
+    where = f"same keys {query} {heads}/{kv} {d} {kind}"
+    case.table[12, 1], case.table[31, 0] = -1, 2**31 - 1
+    for window, sinks in ((1, 0), (33, 4), (64, 64)):
+        run_window(case, window, sinks, where=f"{where} {window}+{sinks}")
+    for which, head, key, block in ((1, 3, 0, 0), (1, 12, 20, d // 32 - 1), (0, 6, 5, 0), (1, 47, 30, 1)):
+        for r in (6, 9, 13):
+            case.scale[which][case.table[r, key // bs], key % bs, head, block] = 255
+    out, lse = run_window(case, 100, 10, where=where + " NaN")
+    assert torch.isnan(out).any() and torch.isnan(lse).any() and not torch.isnan(out[16 * query:]).any()
+    case.max_seq_len = 64                                    # everything, few keys
+    run_window(case, 0, 0, where=where + " cut")
+
+
 def test_a_cache_of_more_than_four_gigabytes():
     """Pages whose bytes lie past 2^32: written, read back and attended to as in a small cache."""
     bs, kv, d = 64, 8, 256

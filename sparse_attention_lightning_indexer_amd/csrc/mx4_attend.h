@@ -39,6 +39,11 @@
 //    before) is converted, the page ids a pair of tiles further, the selected
 //    indices one more.
 //
+// Measured, 64 query heads on 8 K/V heads of 128: one row over 131072 keys 31 us
+// (bf16, 4.6 TB/s: memory); 128 rows x 2048 keys of 32 requests 68 us (bf16, 4.3
+// TB/s in gathered rows); 32 rows under a window of 1024 13.7 us and 32 rows x 512
+// keys 9.2 us (f16: the latency of dependent loads and few tiles a wave).
+//
 // Masked positions: their scores become -inf by selection, so K's NaN there
 // never spreads; V's blocks of NaN are replaced by zeros in the product, and
 // the rows that do attend to such a key get their NaN by a mask of blocks
@@ -790,6 +795,12 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
 // Per key of a buffer a word says what is unusual: bit 31 a page outside the
 // cache, bits 0-7 blocks of V that are NaN (stored as zeros; the rows that see
 // the key get their NaN at the end).
+//
+// Measured, 64 query heads on 8 K/V heads of 128: 1024 causal tokens over 16384
+// keys 511 us (f16, 1.04 PFLOP/s, where an 8192-cubed library product reaches
+// 1.19), 1000 tokens under a window of 4096 157 us (bf16, 0.87 PFLOP/s).  The
+// vector units are busy for 48% of the time and the matrix units for 43%, with
+// two waves a SIMD to overlap them.
 template <int D>
 struct PromptShape {
     static constexpr int MT = 2, W = 8, KEYS = 64, ROWS = W * 16 * MT;
@@ -1076,7 +1087,9 @@ __global__ void __launch_bounds__(512, 2) mx4_prompt_kernel(Mx4Attend a) {
 
 // Joins the shares of rows whose keys were split (at most kMx4MaxSplits): a workgroup per
 // query row and head.  Threads take 4 outputs of every 1024 / D-th share, so
-// the loads of a row's shares overlap, and add up through LDS.
+// the loads of a row's shares overlap, and add up through LDS.  Latency: 32
+// shares of 64 heads of 128 take 4.7 us, most of it the launch and two dependent
+// rounds of loads.
 template <bool BF16, int D>
 __global__ void __launch_bounds__(256) mx4_join_kernel(Mx4Attend a) {
     using T = Type<BF16>;

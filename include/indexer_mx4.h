@@ -146,9 +146,13 @@ indexer_status indexer_mx4_cache_read(const indexer_mx4_read_args *args);
  *   q            [n_requests*query_len][n_heads][head_dim] of `type` (strides
  *                in elements, multiples of 8; 16-byte aligned).  The cached
  *                values enter the products in this type: exact for a cache
- *                written from it.  Products accumulate in f32; the softmax
- *                is f32 and its weights are rounded to `type` for the
- *                product with V.
+ *                written from it.  Of values that the type does not hold (a
+ *                cache written from another) K's are infinite, and V's count
+ *                as the largest that the type's own writer stores, 6 * 2^13
+ *                or 6 * 2^125 in magnitude; neither reaches a row or head
+ *                that does not attend to the key.  Products accumulate in
+ *                f32; the softmax is f32 and its weights are rounded to
+ *                `type` for the product with V.
  *   block_table  i32 [n_requests][bt_stride], pages of each request; entries
  *                of the first ceil(max_seq_len / block_size) columns are read
  *                where a position needs them (and the first of each row)

@@ -47,7 +47,10 @@
 // Masked positions: their scores become -inf by selection, so K's NaN there
 // never spreads; V's blocks of NaN are replaced by zeros in the product, and
 // the rows that do attend to such a key get their NaN by a mask of blocks
-// (0 * NaN would otherwise reach rows that must not see the key).
+// (0 * NaN would otherwise reach rows that must not see the key).  Nor may V be
+// infinite there: where a block's scale makes values that the type does not
+// hold, its codes are written anew under the largest scale that does not, at
+// most 6 times it.
 #pragma once
 
 #include <math.h>
@@ -70,6 +73,7 @@ template <>
 struct Type<false> {
     typedef half8 vec8;
     typedef _Float16 one;
+    static constexpr uint32_t kTopScale = 140;  // 6 * 2^13 is the largest of this form the type holds
     static __device__ __forceinline__ f32x4 mfma(vec8 a, vec8 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
     }
@@ -87,6 +91,7 @@ template <>
 struct Type<true> {
     typedef bf8 vec8;
     typedef __bf16 one;
+    static constexpr uint32_t kTopScale = 252;  // 6 * 2^125
     static __device__ __forceinline__ f32x4 mfma(vec8 a, vec8 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
     }
@@ -104,6 +109,19 @@ struct Type<true> {
 // infinity, one instruction where fmaxf takes three to quiet its operands.
 __device__ __forceinline__ float larger(float a, float b) {
     return __builtin_amdgcn_fmed3f(a, b, __builtin_huge_valf());
+}
+
+// The codes of 8 values under a scale 2^steps times smaller, at most 6 times
+// it.  A step takes the magnitudes 0, .5, 1, 1.5, 2, 3 to 0, 1, 2, 3, 4, 6, which
+// is code + 2 from code 2 on and code 2 for 1, and the larger ones to 6, code 7.
+__device__ __forceinline__ uint32_t larger_codes(uint32_t w, uint32_t steps) {
+    uint32_t m = w & 0x77777777u;
+    for (uint32_t i = min(steps, 4u); i; --i) {  // .5 passes 6 in four
+        const uint32_t two = (m >> 1 | m >> 2) & 0x11111111u;  // code 2 on
+        m += 2u * two + (m & ~two & 0x11111111u);
+        m = (m | (m >> 3 & 0x11111111u) * 7u) & 0x77777777u;
+    }
+    return m | (w & 0x88888888u);
 }
 
 // Over the four lanes that share l & 15.
@@ -482,23 +500,39 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
             for (int u = 0; u < NU; ++u)
                 raw_[u].sv[0] = shared_scale(buffer, 1, b * 32 + u * KPL + krow, it.kv - first_kv + hsel, blk0);
         }
-        // V's scales: 0 for keys that do not count and blocks of NaN (rare), and
-        // a mark for the rows that do attend to such a block
+        // V's scales: 0 for keys that do not count; rarely, 0 for blocks of NaN,
+        // with a mark for the rows that do attend to such a block, and at most
+        // the type's largest
         bool bad = false;
 #pragma unroll
         for (int u = 0; u < NU; ++u)
 #pragma unroll
-            for (int n = 0; n < NB; ++n) bad |= raw_[u].sv[n] == 255u;
-        if (valid != 0xffffffffu || __ballot(bad)) {
+            for (int n = 0; n < NB; ++n) bad |= raw_[u].sv[n] > T::kTopScale;
+        if (valid != 0xffffffffu) {
 #pragma unroll
             for (int u = 0; u < NU; ++u) {
                 const bool in = (valid >> (u * KPL + krow)) & 1u;
+#pragma unroll
+                for (int n = 0; n < NB; ++n) raw_[u].sv[n] = in ? raw_[u].sv[n] : 0u;
+            }
+        }
+        if (__ballot(bad)) {
+#pragma unroll
+            for (int u = 0; u < NU; ++u) {
                 uint32_t mine = 0;  // blocks of NaN in this lane's part of its key
 #pragma unroll
                 for (int n = 0; n < NB; ++n) {
-                    const bool b = raw_[u].sv[n] == 255u;
-                    if (in && b) mine |= 1u << min(blk0 + n, D / 32 - 1);
-                    if (!in || b) raw_[u].sv[n] = 0u;
+                    if (raw_[u].sv[n] == 255u) {
+                        mine |= 1u << min(blk0 + n, D / 32 - 1);
+                        raw_[u].sv[n] = 0u;
+                    }
+                    if (raw_[u].sv[n] > T::kTopScale) {
+#pragma unroll
+                        for (int st = 0; st < KS; ++st)
+                            if (block_of(ch, st) == n)
+                                raw_[u].v[st] = larger_codes(raw_[u].v[st], raw_[u].sv[n] - T::kTopScale);
+                        raw_[u].sv[n] = T::kTopScale;
+                    }
                 }
                 if (__ballot(mine != 0u)) {
                     for (int row = 0; row < KPL; ++row) {
@@ -909,6 +943,12 @@ __global__ void __launch_bounds__(512, 2) mx4_prompt_kernel(Mx4Attend a) {
                 const bool nan = sc[n] == 255u;
                 if (seen_key && nan) word |= 1u << min(blk0 + n, D / 32 - 1);
                 if (!seen_key || nan) sc[n] = 0u;
+                if (sc[n] > T::kTopScale) {
+#pragma unroll
+                    for (int st = 0; st < KS; ++st)
+                        if ((ch * KS + st) / 4 - blk0 == n) code[st] = larger_codes(code[st], sc[n] - T::kTopScale);
+                    sc[n] = T::kTopScale;
+                }
             }
             word |= (uint32_t)dpp_move<0xb1>(0, (int)word);
             word |= (uint32_t)dpp_move<0x4e>(0, (int)word);

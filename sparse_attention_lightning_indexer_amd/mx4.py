@@ -293,7 +293,9 @@ def mx4_attend_selected(q, k_data, k_scale, v_data, v_scale, block_table, seq_le
     gives it (-1: none; an entry stands for pool_size consecutive keys), the
     cache's four tensors, block_table i32 [R, max_blocks], seq_lens i32 [R]
     -> (out like q, lse f32 [R*Q, n_heads] or None).  Keys past the block
-    table's pages are not seen.  A row with no key has out 0 and lse -inf."""
+    table's pages are not seen.  A row with no key has out 0 and lse -inf.
+    Cached values that q's type does not hold (written from another type): V's
+    count as +-6 * 2^13 (f16) or +-6 * 2^125 (bf16), K's as infinite."""
     lib = _library()
     if not isinstance(q, _torch.Tensor):
         raise TypeError("q must be a torch.Tensor")

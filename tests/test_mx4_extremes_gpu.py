@@ -1,0 +1,116 @@
+"""The attention over the 4-bit cache at the ends of its numbers, in every form
+of the kernels, against the plain 64-bit forms (bounds: test_mx4_gpu.py)."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # pragma: no cover - CPU container
+    pytest.skip("needs a GPU", allow_module_level=True)
+
+import sparse_attention_lightning_indexer_amd as li  # noqa: E402
+from oracle import mx4 as plain  # noqa: E402
+from test_mx4_gpu import DEV, Case, check, selection  # noqa: E402
+
+# (lens, query, heads, kv heads, d, block size), each a form of the kernels
+FORMS = {
+    "one tile, 64": ([90, 41], 4, 6, 2, 64, 16),
+    "one tile, 96": ([70, 37], 2, 8, 4, 96, 7),
+    "one tile, 128": ([70, 37], 4, 8, 2, 128, 16),
+    "one tile, 192": ([100, 33], 1, 16, 4, 192, 33),
+    "one tile, 256": ([64, 65], 2, 8, 2, 256, 16),
+    "two tiles, 64": ([90, 150], 3, 34, 2, 64, 32),
+    "two tiles, 96": ([90, 150], 3, 34, 2, 96, 32),
+    "two tiles, 128": ([90, 150], 3, 34, 2, 128, 32),
+    "two tiles, 192": ([90, 150], 3, 34, 2, 192, 32),
+    "two tiles, 256": ([90, 150], 3, 34, 2, 256, 32),
+    "pairs, 64": ([60, 33, 5, 70] * 16, 1, 32, 16, 64, 16),
+    "pairs, 96": ([60, 33, 5, 70] * 16, 1, 16, 16, 96, 16),
+    "pairs, 128": ([60, 33, 5, 70] * 16, 1, 64, 16, 128, 16),
+    "shared scales, 64": ([60, 33, 5, 70] * 4, 6, 64, 64, 64, 16),
+    "shared scales, 128": ([60, 33, 5, 70] * 4, 4, 64, 64, 128, 16),
+    "shares, 64": ([3300, 900], 1, 8, 2, 64, 32),
+    "shares, 128": ([3300, 900], 1, 16, 2, 128, 32),
+    "shares, 256": ([3300, 900], 1, 16, 2, 256, 32),
+    "ahead, 64": ([300, 513, 40, 90] * 4, 1, 16, 16, 64, 16),
+    "ahead, 128": ([300, 513, 40, 90] * 4, 1, 16, 16, 128, 16),
+    "prompt, 64": ([200, 64, 90, 330] * 4, 32, 64, 8, 64, 16),
+    "prompt, 96": ([200, 64, 90, 330] * 4, 37, 56, 8, 96, 7),
+    "prompt, 128": ([200, 64, 90, 330] * 4, 64, 32, 8, 128, 64),
+    "prompt shares, 64": ([9000], 650, 16, 8, 64, 64),
+}
+SAMPLE = 24   # rows of a large form compared with the plain form
+
+
+def form(name, seed, kind, **kw):
+    case = Case(seed, *FORMS[name], kind, **kw)
+    if name.startswith("ahead"):
+        case.max_seq_len = 2100
+        more = -(-2100 // case.bs) - case.table.shape[1]
+        case.table = np.concatenate([case.table, np.full((len(case.lens), more), -1, dtype=np.int32)], 1)
+    rows = case.q.shape[0]
+    case.rows = np.arange(rows) if rows <= 64 else np.sort(case.rng.permutation(rows)[:SAMPLE])
+    if rows > 64:   # the first and last rows of the first request
+        case.rows = np.unique(np.concatenate([case.rows, [0, case.query - 2, case.query - 1]]))
+    return case
+
+
+def attended(case, how, positions=None, **kw):
+    """(the call's out and lse, positions of a row) of a form of the attention."""
+    args = case.args()
+    if how == "selected":
+        idx = selection(case, min(2048, int(max(case.lens))) if positions is None else positions, holes=0.02)
+        got = li.mx4_attend_selected(*args, torch.from_numpy(idx).to(DEV), case.sm_scale, **kw)
+        return got, lambda t, v, e: plain.positions_selected(idx[t], 1, e)
+    window, sinks = (0, 0) if how == "causal" else (50, 3)
+    got = li.mx4_attend_window(*args, case.max_seq_len, case.sm_scale, window=window, sinks=sinks, **kw)
+    return got, lambda t, v, e: plain.positions_window(v, e, window, sinks)
+
+
+def expected(case, positions, v=lambda x: x):
+    """The plain form of the case's sampled rows, V's values passed through `v`."""
+    few = set(case.rows.tolist())
+    k, val = (plain.values(d, s) for d, s in zip(case.data, case.scale))
+    o, z, b = plain.attend_rows(case.q, k, v(val), case.table, case.lens, case.query, case.max_seq_len, case.sm_scale,
+                                lambda t, vis, e: positions(t, vis, e) if t in few else [])
+    return o[case.rows], z[case.rows], {n: x[case.rows] for n, x in b.items()}
+
+
+def sampled(case, got):
+    pick = torch.from_numpy(case.rows).to(DEV)
+    return tuple(x[pick] for x in got)
+
+
+# V's values end at 6 * 2^13 (f16) and 6 * 2^125 (bf16), scale bytes 140 and 252: the largest
+# that the type's own writer stores
+ENDS = {"f16": (6 * 2.0**13, (141, 142, 143, 150, 254)), "bf16": (6 * 2.0**125, (253, 254))}
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("name", list(FORMS))
+def test_values_past_the_type_stay_with_their_rows(name, kind):
+    """V's values that the query's type does not hold (a cache written from another type): rows that do not see
+    them, and other heads, are as without them; rows that do take them as the largest value the type's writer
+    stores."""
+    case = form(name, 60, kind)
+    most, scales = ENDS[kind]
+    Q, kv, blocks = case.query, case.kv, case.d // 32
+    for i, r in enumerate(range(0, len(case.lens), 3)):
+        last = int(case.lens[r]) - 1
+        # the last key (the last query alone sees it), one out of the window, one among the first
+        for p, head, block in ((last, i % kv, i % blocks), (last - 57 - Q, (i + 1) % kv, blocks - 1), (4, (i + 2) % kv, 0)):
+            if p >= 0:
+                case.scale[1][case.table[r, p // case.bs], p % case.bs, head, block] = scales[i % len(scales)]
+    hit = False
+    for how in ("causal", "window", "selected"):
+        got, positions = attended(case, how)
+        out, lse = sampled(case, got)
+        o, z, b = expected(case, positions, lambda x: np.clip(x, -most, most))
+        huge = b["plain"] >= 2.0**100           # bf16: weights times such values pass f32's range in rows that see them
+        hit |= bool((b["plain"] >= 40000).any())
+        assert torch.isfinite(out[torch.from_numpy(~huge).to(DEV)]).all(), (name, how)
+        out = torch.where(torch.from_numpy(huge).to(DEV), torch.from_numpy(o).to(DEV), out.double())
+        check((out, lse), (o, z, b), kind, case.d, f"{name} {how} {kind}")
+    assert hit

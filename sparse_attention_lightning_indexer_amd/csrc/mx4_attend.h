@@ -938,16 +938,25 @@ __global__ void __launch_bounds__(512, 2) mx4_prompt_kernel(Mx4Attend a) {
     auto store_step = [&](int buf) {
         uint32_t word = bad_page ? 0x80000000u : 0u;
         if (is_v) {
+            bool bad = false;
 #pragma unroll
             for (int n = 0; n < NB; ++n) {
-                const bool nan = sc[n] == 255u;
-                if (seen_key && nan) word |= 1u << min(blk0 + n, D / 32 - 1);
-                if (!seen_key || nan) sc[n] = 0u;
-                if (sc[n] > T::kTopScale) {
+                sc[n] = seen_key ? sc[n] : 0u;
+                bad |= sc[n] > T::kTopScale;
+            }
+            if (__ballot(bad)) {
 #pragma unroll
-                    for (int st = 0; st < KS; ++st)
-                        if ((ch * KS + st) / 4 - blk0 == n) code[st] = larger_codes(code[st], sc[n] - T::kTopScale);
-                    sc[n] = T::kTopScale;
+                for (int n = 0; n < NB; ++n) {
+                    if (sc[n] == 255u) {
+                        word |= 1u << min(blk0 + n, D / 32 - 1);
+                        sc[n] = 0u;
+                    }
+                    if (sc[n] > T::kTopScale) {
+#pragma unroll
+                        for (int st = 0; st < KS; ++st)
+                            if ((ch * KS + st) / 4 - blk0 == n) code[st] = larger_codes(code[st], sc[n] - T::kTopScale);
+                        sc[n] = T::kTopScale;
+                    }
                 }
             }
             word |= (uint32_t)dpp_move<0xb1>(0, (int)word);

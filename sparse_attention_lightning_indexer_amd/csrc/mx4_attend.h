@@ -174,6 +174,13 @@ __device__ __forceinline__ void get_words(const lds_u8 *src, uint32_t (&w)[N]) {
 
 constexpr float kNegInf = -__builtin_huge_valf();
 
+// Weights are 2^(s c - m) with one rounding, m the rounded product of a largest
+// score: the largest weight is then 2^r, r the rounding of m, which any sum of
+// weights takes along.  From this |m| on, where r may pass an eighth (and at
+// 2^32 a float's range), the product is rounded before m is taken off it, as it
+// was for m.
+constexpr float kFar = 2097152.0f;  // 2^21
+
 template <int D, int HP>
 struct Shape {
     static constexpr int KS = D / 32;               // MFMA steps over the head dimension
@@ -294,10 +301,12 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
     vec8 q[MT][KS];
     int row_end[MT], row_start[MT];
     float mx[MT], ls[MT];
+    float limit[MT];  // the score past which the reference is looked at again
     f32x4 o[MT][NT];
     uint32_t nan_blocks[MT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
+        limit[mt] = kNegInf;
         const int mc = min(it.m0 + mt * 16 + mcol, n_m - 1);
         const int token = token_of(mc);
         const uint4 *src = reinterpret_cast<const uint4 *>((const uint16_t *)a.q + (int64_t)token * a.q_st +
@@ -670,16 +679,18 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
 
         // softmax.  The reference m of a row is a maximum so far, the same in its
         // four lanes; it moves only when a score passes it by 2^8, so weights
-        // stay below 2^8 and the rescaling is rare
+        // stay below 2^8 (kFar: and an eighth) and the rescaling is rare
         vec8 p[MT];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
+#pragma clang fp contract(off)
             float top = larger(s[mt][0][0], s[mt][0][1]);
             top = larger(larger(top, s[mt][0][2]), s[mt][0][3]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) top = larger(top, s[mt][1][i]);
             top *= a.scale_log2;
-            if (__ballot(top > mx[mt] + 8.0f)) {
+            float times = a.scale_log2, plus = mx[mt] == kNegInf ? 0.0f : -mx[mt];
+            if (__ballot(top > limit[mt])) {
                 const float m_new = larger(mx[mt], quarter_max(top));
                 const float f = m_new > mx[mt] ? __builtin_amdgcn_exp2f(mx[mt] - m_new) : 1.0f;
                 mx[mt] = m_new;
@@ -688,14 +699,24 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) o[mt][n][i] *= f;
+                const bool near = fabsf(m_new) < kFar;
+                limit[mt] = near ? m_new + 8.0f : kNegInf;
+                plus = m_new == kNegInf ? 0.0f : -m_new;
+                if (__ballot(!near && m_new != kNegInf)) {
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) s[mt][u][i] = s[mt][u][i] * times + plus;
+                    times = 1.0f;
+                    plus = 0.0f;
+                }
             }
-            const float sub = mx[mt] == kNegInf ? 0.0f : mx[mt];
             float sum = 0.0f;
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[mt][u][i], a.scale_log2, -sub));
+                    const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[mt][u][i], times, plus));
                     sum += e;
                     p[mt][u * 4 + i] = (typename T::one)e;
                 }
@@ -823,8 +844,8 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
 // page id of the one after that, and the wave multiplies.  A wave passes over
 // steps that none of its rows sees.  The maximum is looked for only where the
 // weights' sum says that the reference is too low (a weight past about 2^8), or
-// no key was seen yet; otherwise weights cost one multiply-add, one exponential
-// and one addition each.
+// no key was seen yet, or the reference is past kFar; otherwise weights cost one
+// multiply-add, one exponential and one addition each.
 //
 // Per key of a buffer a word says what is unusual: bit 31 a page outside the
 // cache, bits 0-7 blocks of V that are NaN (stored as zeros; the rows that see
@@ -883,10 +904,12 @@ __global__ void __launch_bounds__(512, 2) mx4_prompt_kernel(Mx4Attend a) {
     vec8 q[MT][KS];
     int row_end[MT], row_start[MT];
     float mx[MT], ls[MT];
+    float limit[MT];  // weights' sum past which the reference is looked at again; -1: always (none yet, or past kFar)
     f32x4 o[MT][NT];
     uint32_t nan_blocks[MT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
+        limit[mt] = -1.0f;
         const int m = min(m0 + mt * 16 + col, n_m - 1), t = token_in(m);
         const uint4 *src = reinterpret_cast<const uint4 *>(
             (const uint16_t *)a.q + (int64_t)(req * a.q_len + t) * a.q_st +
@@ -1047,21 +1070,24 @@ __global__ void __launch_bounds__(512, 2) mx4_prompt_kernel(Mx4Attend a) {
         vec8 p[MT][2];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-            auto weigh = [&]() {
+#pragma clang fp contract(off)
+            auto weigh = [&](auto rounded) {
                 const float sub = mx[mt] == kNegInf ? 0.0f : mx[mt];
                 float sum = 0.0f;
 #pragma unroll
                 for (int u = 0; u < 4; ++u)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[mt][u][i], a.scale_log2, -sub));
+                        const float e = __builtin_amdgcn_exp2f(
+                            decltype(rounded)::value ? s[mt][u][i] * a.scale_log2 - sub
+                                                     : __builtin_fmaf(s[mt][u][i], a.scale_log2, -sub));
                         sum += e;
                         p[mt][u >> 1][(u & 1) * 4 + i] = (typename T::one)e;
                     }
                 return sum;
             };
-            float sum = weigh();
-            if (__ballot(sum > 256.0f || mx[mt] == kNegInf)) {
+            float sum = weigh(Set<0>{});
+            if (__ballot(sum > limit[mt])) {
                 float top = s[mt][0][0];
 #pragma unroll
                 for (int u = 0; u < 4; ++u)
@@ -1075,7 +1101,12 @@ __global__ void __launch_bounds__(512, 2) mx4_prompt_kernel(Mx4Attend a) {
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) o[mt][n][i] *= f;
-                sum = weigh();
+                const bool near = fabsf(m_new) < kFar;
+                limit[mt] = near ? 256.0f : -1.0f;
+                if (__ballot(!near && m_new != kNegInf))
+                    sum = weigh(Set<1>{});
+                else
+                    sum = weigh(Set<0>{});
             }
             ls[mt] += sum;
         }

@@ -74,6 +74,7 @@ struct Type<false> {
     typedef half8 vec8;
     typedef _Float16 one;
     static constexpr uint32_t kTopScale = 140;  // 6 * 2^13 is the largest of this form the type holds
+    static constexpr float kLift = 7.0f;
     static __device__ __forceinline__ f32x4 mfma(vec8 a, vec8 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
     }
@@ -92,6 +93,7 @@ struct Type<true> {
     typedef bf8 vec8;
     typedef __bf16 one;
     static constexpr uint32_t kTopScale = 252;  // 6 * 2^125
+    static constexpr float kLift = 0.0f;
     static __device__ __forceinline__ f32x4 mfma(vec8 a, vec8 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
     }
@@ -174,6 +176,12 @@ __device__ __forceinline__ void get_words(const lds_u8 *src, uint32_t (&w)[N]) {
 
 constexpr float kNegInf = -__builtin_huge_valf();
 
+// Weights stand against 2^kLift for the reference, of which their sum takes
+// 2^kLift off again.  They stay below 2^8 of it, so f16, which ends at 2^16 and
+// 2^-24, has room for 2^7: a weight is then lost below 2^-32 of the largest, not
+// 2^-25.  (One key that leads 131071 others by 17.5 leaves them 0.33% of the
+// weight, each 2^-25: as f16 against 1 all of them were 0.)  bf16 has f32's range.
+//
 // Weights are 2^(s c - m) with one rounding, m the rounded product of a largest
 // score: the largest weight is then 2^r, r the rounding of m, which any sum of
 // weights takes along.  From this |m| on, where r may pass an eighth (and at
@@ -679,7 +687,7 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
 
         // softmax.  The reference m of a row is a maximum so far, the same in its
         // four lanes; it moves only when a score passes it by 2^8, so weights
-        // stay below 2^8 (kFar: and an eighth) and the rescaling is rare
+        // stay below 2^(8 + kLift) (kFar: and an eighth) and the rescaling is rare
         vec8 p[MT];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
@@ -689,7 +697,7 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
 #pragma unroll
             for (int i = 0; i < 4; ++i) top = larger(top, s[mt][1][i]);
             top *= a.scale_log2;
-            float times = a.scale_log2, plus = mx[mt] == kNegInf ? 0.0f : -mx[mt];
+            float times = a.scale_log2, plus = T::kLift - (mx[mt] == kNegInf ? 0.0f : mx[mt]);
             if (__ballot(top > limit[mt])) {
                 const float m_new = larger(mx[mt], quarter_max(top));
                 const float f = m_new > mx[mt] ? __builtin_amdgcn_exp2f(mx[mt] - m_new) : 1.0f;
@@ -701,14 +709,15 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
                     for (int i = 0; i < 4; ++i) o[mt][n][i] *= f;
                 const bool near = fabsf(m_new) < kFar;
                 limit[mt] = near ? m_new + 8.0f : kNegInf;
-                plus = m_new == kNegInf ? 0.0f : -m_new;
+                const float sub = m_new == kNegInf ? 0.0f : m_new;
+                plus = T::kLift - sub;
                 if (__ballot(!near && m_new != kNegInf)) {
 #pragma unroll
                     for (int u = 0; u < 2; ++u)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) s[mt][u][i] = s[mt][u][i] * times + plus;
+                        for (int i = 0; i < 4; ++i) s[mt][u][i] = s[mt][u][i] * times - sub;
                     times = 1.0f;
-                    plus = 0.0f;
+                    plus = T::kLift;
                 }
             }
             float sum = 0.0f;
@@ -825,7 +834,7 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
                 *reinterpret_cast<vec8 *>((uint16_t *)a.out + (int64_t)token * a.out_st + (int64_t)head * a.out_sh +
                                           c * 8) = r;
                 if (c == 0 && a.lse)
-                    a.lse[th] = l_all == 0.0f ? kNegInf : (m_all + log2f(l_all)) * 0.69314718055994530942f;
+                    a.lse[th] = l_all == 0.0f ? kNegInf : (m_all + (log2f(l_all) - T::kLift)) * 0.69314718055994530942f;
             }
         }
     }
@@ -843,9 +852,9 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
 // next step into the other buffer, asks for the codes of the step after and the
 // page id of the one after that, and the wave multiplies.  A wave passes over
 // steps that none of its rows sees.  The maximum is looked for only where the
-// weights' sum says that the reference is too low (a weight past about 2^8), or
-// no key was seen yet, or the reference is past kFar; otherwise weights cost one
-// multiply-add, one exponential and one addition each.
+// weights' sum says that the reference is too low (a weight past about 2^8 of
+// it), or no key was seen yet, or the reference is past kFar; otherwise weights
+// cost one multiply-add, one exponential and one addition each.
 //
 // Per key of a buffer a word says what is unusual: bit 31 a page outside the
 // cache, bits 0-7 blocks of V that are NaN (stored as zeros; the rows that see
@@ -869,6 +878,7 @@ __global__ void __launch_bounds__(512, 2) mx4_prompt_kernel(Mx4Attend a) {
     using P = PromptShape<D>;
     typedef typename T::vec8 vec8;
     constexpr int KS = D / 32, NT = D / 16, MT = P::MT, KEYS = P::KEYS, ROW = P::ROW;
+    constexpr float kMostSum = BF16 ? 0x1p8f : 0x1p15f;  // 2^(8 + kLift)
     __shared__ __attribute__((aligned(16))) unsigned char smem[2 * P::BUFFER];
     __shared__ uint32_t unusual[2][KEYS];
     __shared__ __attribute__((aligned(16))) uint32_t any[2][4];
@@ -1072,15 +1082,15 @@ __global__ void __launch_bounds__(512, 2) mx4_prompt_kernel(Mx4Attend a) {
         for (int mt = 0; mt < MT; ++mt) {
 #pragma clang fp contract(off)
             auto weigh = [&](auto rounded) {
-                const float sub = mx[mt] == kNegInf ? 0.0f : mx[mt];
+                const float sub = mx[mt] == kNegInf ? 0.0f : mx[mt], plus = T::kLift - sub;
                 float sum = 0.0f;
 #pragma unroll
                 for (int u = 0; u < 4; ++u)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float e = __builtin_amdgcn_exp2f(
-                            decltype(rounded)::value ? s[mt][u][i] * a.scale_log2 - sub
-                                                     : __builtin_fmaf(s[mt][u][i], a.scale_log2, -sub));
+                            decltype(rounded)::value ? s[mt][u][i] * a.scale_log2 - sub + T::kLift
+                                                     : __builtin_fmaf(s[mt][u][i], a.scale_log2, plus));
                         sum += e;
                         p[mt][u >> 1][(u & 1) * 4 + i] = (typename T::one)e;
                     }
@@ -1102,7 +1112,7 @@ __global__ void __launch_bounds__(512, 2) mx4_prompt_kernel(Mx4Attend a) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) o[mt][n][i] *= f;
                 const bool near = fabsf(m_new) < kFar;
-                limit[mt] = near ? 256.0f : -1.0f;
+                limit[mt] = near ? kMostSum : -1.0f;
                 if (__ballot(!near && m_new != kNegInf))
                     sum = weigh(Set<1>{});
                 else
@@ -1160,7 +1170,7 @@ __global__ void __launch_bounds__(512, 2) mx4_prompt_kernel(Mx4Attend a) {
             a.part_ml[(th * a.n_splits + it.split) * 2] = mx[mt];
             a.part_ml[(th * a.n_splits + it.split) * 2 + 1] = l;
         } else if (a.lse) {
-            a.lse[th] = l == 0.0f ? kNegInf : (mx[mt] + log2f(l)) * 0.69314718055994530942f;
+            a.lse[th] = l == 0.0f ? kNegInf : (mx[mt] + (log2f(l) - T::kLift)) * 0.69314718055994530942f;
         }
     }
 }
@@ -1194,7 +1204,7 @@ __global__ void __launch_bounds__(256) mx4_join_kernel(Mx4Attend a) {
         weight[threadIdx.x] = f;
         if (threadIdx.x == 0) {
             total[0] = l;
-            if (a.lse) a.lse[th] = l == 0.0f ? kNegInf : (m_all + log2f(l)) * 0.69314718055994530942f;
+            if (a.lse) a.lse[th] = l == 0.0f ? kNegInf : (m_all + (log2f(l) - T::kLift)) * 0.69314718055994530942f;
         }
     }
     __syncthreads();

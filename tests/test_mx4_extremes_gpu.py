@@ -151,3 +151,41 @@ def test_scores_far_from_zero(name, power, kind):
                 assert np.all(np.abs(out[i, h] - want) <= tol), (name, how, t, h)
                 checked += 1
     assert checked > 20, checked
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("name", list(FORMS))
+@pytest.mark.parametrize("first", [True, False])
+def test_many_small_weights_beside_a_large_one(name, first, kind):
+    """One key leads all others by 17.5: each of them weighs 2^-25, less than half of f16's least number, and
+    together they are what the row's output is made of.
+
+    f16 weights stand against 2^7 for the largest, so the least number below them is 2^-31 of it, and each is off by
+    half of that: 2^-32 sum|V|, with the relative terms and the output's own roundings as in test_mx4_gpu.py."""
+    case = form(name, 62, kind)
+    case.scale = [np.full_like(s, 127) for s in case.scale]
+    case.data[0][:] = 0
+    case.data[1][:] = 0x22                       # every value 1
+    case.q_t = torch.zeros_like(case.q_t)
+    case.q_t[..., 3] = 1.0
+    case.q = case.q_t.double().numpy()
+    case.sm_scale = float(np.float32(17.5 / 4.0))
+    for r, n in enumerate(case.lens):            # the leading key: 4 in dimension 3, V 0
+        p = 0 if first else max(0, int(n) - case.query)
+        page, off = case.table[r, p // case.bs], p % case.bs
+        case.data[0][page, off, :, 1] = 0x60
+        case.data[1][page, off] = 0
+    for how in ("causal", "selected"):
+        got, positions = attended(case, how)
+        o, z, b = expected(case, positions)
+        out, lse = (x.double().cpu().numpy() for x in sampled(case, got))
+        n = b["count"][:, None]
+        unit = {"f16": 2.0**-11, "bf16": 2.0**-8}[kind]
+        delta = case.d * 2.0**-23 * b["reach"] + 2.0**-22 * (b["top"] + 1)
+        tol = (unit + 2 * delta + (n + 64) * 2.0**-23)[..., None] * b["spread"] + unit * np.abs(o)
+        tol = tol + (2.0**-32 * b["plain"] + 2.0**-25 if kind == "f16" else 2.0**-126 * (b["plain"] + 1))
+        assert np.all(np.abs(out - o) <= tol), (name, how, float(np.max(np.abs(out - o) / tol)))
+        assert (o > 0).any()
+        some = np.isfinite(z)
+        assert np.array_equal(np.isneginf(lse), ~some)
+        assert np.all(np.abs(lse[some] - z[some]) <= (delta + (n + 64) * 2.0**-23 + 2.0**-22 * 20)[some])

@@ -61,16 +61,18 @@ indexer_status check_pages(int32_t n_blocks, int32_t block_size, int32_t n_heads
     if ((n_blocks > 1 && s_sb < srow) || (block_size > 1 && s_ss < srow) || (n_heads > 1 && s_sh < srow))
         MX4_FAIL(INDEXER_EINVAL, "scale strides %lld, %lld, %lld must be >= head_dim/32 = %lld", (long long)s_sb,
                  (long long)s_ss, (long long)s_sh, (long long)srow);
-    // the kernels' address arithmetic: 32-bit block strides, 24-bit slot strides and sizes, 32 bits inside a block
-    const int64_t most = (int64_t)(block_size - 1) * d_ss + (int64_t)(n_heads - 1) * d_sh + row;
-    const int64_t smost = (int64_t)(block_size - 1) * s_ss + (int64_t)(n_heads - 1) * s_sh + srow;
-    if (block_size >= 1 << 24 || (block_size > 1 && (d_ss >= 1 << 24 || s_ss >= 1 << 24)) || most > UINT32_MAX ||
-        smost > UINT32_MAX || (n_blocks > 1 && (d_sb > UINT32_MAX || s_sb > UINT32_MAX)))
-        MX4_FAIL(INDEXER_ENOTSUP, "pages not supported (block_size and slot strides below 2^24, a block's bytes and "
-                 "block strides below 2^32)");
     if (n_blocks <= 1) d_sb = s_sb = 0;
     if (block_size == 1) d_ss = s_ss = 0;
     if (n_heads == 1) d_sh = s_sh = 0;
+    // the kernels' address arithmetic: 32-bit block and head strides, 24-bit slot strides and sizes, 32 bits inside
+    // a block; the extents are computed (in 64 bits) once the strides are known to be small
+    bool ok = block_size < 1 << 24 && d_ss < 1 << 24 && s_ss < 1 << 24 && d_sb <= UINT32_MAX && s_sb <= UINT32_MAX &&
+              d_sh <= UINT32_MAX && s_sh <= UINT32_MAX;
+    ok = ok && (block_size - 1) * d_ss + (n_heads - 1) * d_sh + row <= UINT32_MAX;
+    ok = ok && (block_size - 1) * s_ss + (n_heads - 1) * s_sh + srow <= UINT32_MAX;
+    if (!ok)
+        MX4_FAIL(INDEXER_ENOTSUP, "pages not supported (block_size and slot strides below 2^24, a block's bytes and "
+                 "block strides below 2^32)");
     *out = lidx::Mx4Pages{d_sb, d_ss, d_sh, s_sb, s_ss, s_sh, n_blocks, block_size,
                           lidx::fast_div((uint32_t)block_size), (int64_t)n_blocks * block_size, d_sb == 16 * s_sb && d_ss == 16 * s_ss};
     return INDEXER_OK;

@@ -305,3 +305,16 @@ def test_positions_by_hand():
     assert plain.positions_window(9, 6, 2, 1) == [0]           # the window lies past the last key kept
     assert plain.positions_window(6, 6, 0, 3) == list(range(6))
     assert plain.positions_window(-1, -1, 4, 4) == []
+
+
+# ------------------------------------------------- sizes at the ends of their ranges
+
+@pytest.mark.parametrize("kw", [dict(dsh=1 << 62), dict(ssh=1 << 62), dict(dsh=1 << 62, ssh=1 << 62),
+                                dict(dsh=(1 << 62) + (1 << 33)), dict(dss=1 << 60, bs=17), dict(sss=1 << 60, bs=17)])
+def test_strides_whose_extent_passes_64_bits(lib, kw):
+    """5 heads 2^62 bytes apart: their extent is 2^64, which 64 bits hold as 0."""
+    for call in (lambda: write(lib, H=5, kst=640, vst=640, **kw), lambda: read(lib, H=5, ost=640, **kw),
+                 lambda: attend(lib, "selected", H=5, KV=5, qst=640, ost=640, **kw),
+                 lambda: attend(lib, "window", H=5, KV=5, qst=640, ost=640, **kw)):
+        assert call() == li.ENOTSUP
+        assert b"pages not supported" in lib.indexer_last_error()

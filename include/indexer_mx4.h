@@ -171,7 +171,10 @@ indexer_status indexer_mx4_cache_read(const indexer_mx4_read_args *args);
  * head_dim 64, 96, 128, 192 or 256; n_heads (at most 1024) a multiple of
  * n_kv_heads; sm_scale positive and finite; pool_size in [1, 8192];
  * max_seq_len, n_sel * pool_size and n_requests * query_len * n_heads at most
- * 2^31 - 1024; window, sinks >= 0.
+ * 2^31 - 1024; window, sinks >= 0.  A launch holds fewer than 2^32 threads:
+ * with up to 32 query heads a K/V head, any call of less than 8 million
+ * n_requests * query_len * n_kv_heads (head_dim up to 128; 16 million above)
+ * fits; one that does not is INDEXER_EINVAL.
  * n_requests = 0 enqueues nothing; n_sel = 0 writes the empty rows' values.
  */
 typedef struct {

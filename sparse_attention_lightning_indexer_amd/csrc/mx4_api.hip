@@ -170,9 +170,9 @@ indexer_status run_attend(lidx::Mx4Attend &a, const indexer_mx4_attend_args &g, 
     const lidx::Mx4Pages &pages = a.pages;
     p.share = selected && p.hp == 2 && p.head_group == 4 && (head_dim == 64 || head_dim == 128) && pages.s_sh == head_dim / 32 &&
               pages.s_ss % 16 == 0 && pages.s_sb % 16 == 0 && aligned(a.ks, 16) && aligned(a.vs, 16);
-    // a launch holds fewer than 2^32 threads
-    if (p.workgroups * 512 > UINT32_MAX || (p.n_splits > 1 && (int64_t)a.rows * a.n_heads * 256 > UINT32_MAX))
-        MX4_FAIL(INDEXER_EINVAL, "problem too large for one launch: %lld workgroups", (long long)p.workgroups);
+    if (!p.fits)
+        MX4_FAIL(INDEXER_EINVAL, "problem too large for one launch: %lld workgroups of %d threads",
+                 (long long)p.workgroups, p.threads);
     if (p.workspace_bytes && (!workspace || g.workspace_bytes < p.workspace_bytes || !aligned(workspace, 256)))
         MX4_FAIL(INDEXER_EWORKSPACE, "attention needs %zu bytes of 256-byte aligned workspace, got %zu",
                  p.workspace_bytes, workspace ? g.workspace_bytes : (size_t)0);
@@ -199,6 +199,8 @@ int64_t window_keys(int32_t max_seq_len, int32_t window, int32_t sinks) {
 
 namespace lidx {
 
+static bool one_launch(int64_t workgroups, int threads) { return workgroups <= (int64_t)UINT32_MAX / threads; }
+
 // The launch size and workspace of a plan.
 static Mx4Plan sized(Mx4Plan p, int64_t rows, int n_heads, int n_kv, int head_dim) {
     const int64_t pieces = (int64_t)p.units * p.m_tiles * p.n_splits;
@@ -208,6 +210,8 @@ static Mx4Plan sized(Mx4Plan p, int64_t rows, int n_heads, int n_kv, int head_di
         p.part_o_bytes = (parts * head_dim * 4 + 255) / 256 * 256;
         p.workspace_bytes = p.part_o_bytes + (parts * 8 + 255) / 256 * 256;
     }
+    p.threads = p.prompt ? kMx4PromptThreads : mx4_wave_threads(head_dim, p.hp);
+    p.fits = one_launch(p.workgroups, p.threads) && (p.n_splits == 1 || one_launch(rows * n_heads, kMx4JoinThreads));
     return p;
 }
 
@@ -284,7 +288,11 @@ Mx4Plan plan_mx4_attend(int n_requests, int q_len, int64_t max_keys, bool select
         const int64_t apart = (int64_t)p.units * ((n_m + 31) / 32) * n_kv;  // workgroups of 32 rows
         double best = 0.79 / (4 * kCus) * (double)apart * ((double)max_keys / 32) * head_dim / 128 +
                       7.0 * (double)((apart + kCus - 1) / kCus);
+        if (!one_launch(apart, mx4_wave_threads(head_dim, 1))) best = HUGE_VAL;
         for (int s = 1; s <= 16; ++s) {
+            if (!one_launch((items + 7 * n_kv) * s, kMx4PromptThreads) ||
+                (s > 1 && !one_launch(rows * n_heads, kMx4JoinThreads)))
+                break;
             const double rounds = (double)((items * s + kCus - 1) / kCus);
             double t = 10.0 + rounds * ceil(steps / s) * a_step;
             if (s > 1) t += 5.0 + (double)rows * n_heads * s * head_dim * 8 / 4.5e6;
@@ -304,7 +312,7 @@ Mx4Plan plan_mx4_attend(int n_requests, int q_len, int64_t max_keys, bool select
         p.ahead = 1;
         return sized(p, rows, n_heads, n_kv, head_dim);
     }
-    const int waves = head_dim <= 128 && p.hp == 1 ? 8 : 4;
+    const int waves = mx4_wave_threads(head_dim, p.hp) / 64;
     const int64_t items = (int64_t)p.units * p.m_tiles * (n_kv / p.hp);
     const int64_t most = (max_keys + 32 * waves - 1) / (32 * waves);
     int64_t splits = items > 0 ? kCus / items : 1;
@@ -433,8 +441,9 @@ size_t indexer_mx4_attend_workspace_bytes(int32_t n_requests, int32_t query_len,
         n_kv_heads < 1 || n_heads % n_kv_heads || !attend_dim(head_dim) ||
         (int64_t)n_requests * query_len > kMaxKeys / n_heads)
         return (size_t)-1;
-    return lidx::plan_mx4_attend(n_requests, query_len, max_keys, selected != 0, n_heads, n_kv_heads, head_dim)
-        .workspace_bytes;
+    const lidx::Mx4Plan p =
+        lidx::plan_mx4_attend(n_requests, query_len, max_keys, selected != 0, n_heads, n_kv_heads, head_dim);
+    return p.fits ? p.workspace_bytes : (size_t)-1;
 }
 
 }  // extern "C"

@@ -195,7 +195,7 @@ struct Shape {
     static constexpr int NT = D / 16;               // 16-dimension tiles of the product
     static constexpr int UNITS = D <= 128 ? 4 : 8;  // 16-byte units of a key's codes in LDS
     static constexpr int ROW = 2 * D + 32;          // bytes of a V row in LDS
-    static constexpr int WAVES = D <= 128 && HP == 1 ? 8 : 4;
+    static constexpr int WAVES = mx4_wave_threads(D, HP) / 64;
     static constexpr int KPL = 16 / HP, NU = 2 * HP;  // keys of a load, loads of a tile
     static constexpr int OROW = D + 4;              // floats of a row of the join (padded)
     static constexpr int JOIN = WAVES * 16 * OROW * 4;
@@ -867,13 +867,13 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
 // two waves a SIMD to overlap them.
 template <int D>
 struct PromptShape {
-    static constexpr int MT = 2, W = 8, KEYS = 64, ROWS = W * 16 * MT;
+    static constexpr int MT = 2, W = kMx4PromptThreads / 64, KEYS = 64, ROWS = W * 16 * MT;
     static constexpr int ROW = 2 * D + 32;
     static constexpr int BUFFER = 2 * KEYS * ROW;  // K, then V
 };
 
 template <bool BF16, int D>
-__global__ void __launch_bounds__(512, 2) mx4_prompt_kernel(Mx4Attend a) {
+__global__ void __launch_bounds__(kMx4PromptThreads, 2) mx4_prompt_kernel(Mx4Attend a) {
     using T = Type<BF16>;
     using P = PromptShape<D>;
     typedef typename T::vec8 vec8;
@@ -1181,10 +1181,10 @@ __global__ void __launch_bounds__(512, 2) mx4_prompt_kernel(Mx4Attend a) {
 // shares of 64 heads of 128 take 4.7 us, most of it the launch and two dependent
 // rounds of loads.
 template <bool BF16, int D>
-__global__ void __launch_bounds__(256) mx4_join_kernel(Mx4Attend a) {
+__global__ void __launch_bounds__(kMx4JoinThreads) mx4_join_kernel(Mx4Attend a) {
     using T = Type<BF16>;
     typedef typename T::vec8 vec8;
-    constexpr int C = D / 4, G = 256 / C;  // chunks of 4 outputs, shares in flight
+    constexpr int C = D / 4, G = kMx4JoinThreads / C;  // chunks of 4 outputs, shares in flight
     __shared__ float weight[kMx4MaxSplits], total[1];
     static_assert(kMx4MaxSplits <= 64, "a lane per share");
     __shared__ __attribute__((aligned(16))) float part[G][D];
@@ -1246,7 +1246,7 @@ hipError_t launch_tiles(const Mx4Attend &a, const Mx4Plan &p, hipStream_t stream
         hipLaunchKernelGGL((mx4_attend_kernel<BF16, D, MT, HP, PF, kPools, SHARE>), grid, block, 0, stream, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.n_splits == 1) return e;
-    hipLaunchKernelGGL((mx4_join_kernel<BF16, D>), dim3((unsigned)(a.rows * a.n_heads)), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((mx4_join_kernel<BF16, D>), dim3((unsigned)(a.rows * a.n_heads)), dim3(kMx4JoinThreads), 0, stream, a);
     return hipGetLastError();
 }
 
@@ -1254,10 +1254,10 @@ template <bool BF16, int D>
 hipError_t launch_dim(const Mx4Attend &a, const Mx4Plan &p, hipStream_t stream) {
     if constexpr (D <= 128) {
         if (p.prompt) {
-            hipLaunchKernelGGL((mx4_prompt_kernel<BF16, D>), dim3((unsigned)p.workgroups), dim3(512), 0, stream, a);
+            hipLaunchKernelGGL((mx4_prompt_kernel<BF16, D>), dim3((unsigned)p.workgroups), dim3(kMx4PromptThreads), 0, stream, a);
             hipError_t e = hipGetLastError();
             if (e != hipSuccess || a.n_splits == 1) return e;
-            hipLaunchKernelGGL((mx4_join_kernel<BF16, D>), dim3((unsigned)(a.rows * a.n_heads)), dim3(256), 0, stream,
+            hipLaunchKernelGGL((mx4_join_kernel<BF16, D>), dim3((unsigned)(a.rows * a.n_heads)), dim3(kMx4JoinThreads), 0, stream,
                                a);
             return hipGetLastError();
         }

@@ -100,6 +100,11 @@ struct Mx4Attend {
 
 constexpr int kMx4MaxSplits = 64;
 
+// Threads of a workgroup of the wave-at-a-time form (hp K/V heads a wave), of
+// the many-rows form and of the join.
+constexpr int mx4_wave_threads(int head_dim, int hp) { return head_dim <= 128 && hp == 1 ? 512 : 256; }
+constexpr int kMx4PromptThreads = 512, kMx4JoinThreads = 256;
+
 // Launch geometry: how many 16-row tiles a wave holds and how many workgroups
 // share a row's keys; a function of sizes alone.
 struct Mx4Plan {
@@ -107,8 +112,10 @@ struct Mx4Plan {
     bool share;   // the waves of a workgroup, on 8 K/V heads of a row, share their keys' scales
     int ahead;    // tiles whose codes a wave has on the way
     int mt, hp, m_tiles, n_splits, head_group, units;
+    int threads;        // of a workgroup
     int64_t workgroups;
     size_t part_o_bytes, workspace_bytes;
+    bool fits;          // both launches hold fewer than 2^32 threads, as a launch must
 };
 Mx4Plan plan_mx4_attend(int n_requests, int q_len, int64_t max_keys, bool selected, int n_heads, int n_kv,
                         int head_dim);

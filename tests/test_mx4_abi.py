@@ -318,3 +318,49 @@ def test_strides_whose_extent_passes_64_bits(lib, kw):
                  lambda: attend(lib, "window", H=5, KV=5, qst=640, ost=640, **kw)):
         assert call() == li.ENOTSUP
         assert b"pages not supported" in lib.indexer_last_error()
+
+
+def test_workspace_bytes_of_what_no_launch_holds():
+    """The query refuses what the calls refuse for its size, and nothing else."""
+    none = ctypes.c_size_t(-1).value
+    f = mx4._library().indexer_mx4_attend_workspace_bytes
+    assert f(2_000_000, 1, 32, 1, 160, 16, 128) == none    # 32 million workgroups of 512 threads
+    assert f(2_000_000, 1, 32, 1, 32, 16, 128) == 0        # two heads a wave: 4 million workgroups of 256
+    assert f(131072, 1, 32, 1, 64, 64, 192) == 0           # 8.4 million of 256
+    assert f(262144, 1, 32, 1, 64, 64, 256) == none        # 16.8 million of 256
+    assert f(100_000, 1, 32, 1, 80, 80, 64) == 0
+    # prompts of many heads whose keys would be shared out if their join fitted: whole then
+    for keys in (1 << 21, 1 << 24, 1 << 30):
+        for tokens in (262144, 300_000, 1_000_000):
+            for d in (64, 96, 128):
+                assert f(1, tokens, keys, 0, 64, 8, d) == 0, (keys, tokens, d)
+    # rows of many requests: 512 threads take 256 of a request, or 32 of it
+    assert f(5_000_000, 256, 32, 0, 1, 1, 64) == 0
+    assert f(9_000_000, 64, 1000, 0, 1, 1, 64) == none
+
+
+def test_no_call_that_the_query_accepts_is_refused_for_its_size(lib):
+    """Random sizes: the query's refusal and the call's are one."""
+    rng = np.random.default_rng(7)
+    refused = 0
+    for _ in range(3000):
+        kv = int(rng.choice([1, 2, 8, 16, 64, 128]))
+        H = kv * int(rng.integers(1, 1 + min(1024 // kv, 40)))
+        d = int(rng.choice([64, 96, 128, 192, 256]))
+        Q = int(rng.choice([1, 1, 3, 70, 5000]))
+        R = max(1, int(2.0 ** rng.uniform(10, 31)) // (H * Q))
+        if R * Q * H > 2**31 - 1024:
+            continue
+        keys = int(2.0 ** rng.uniform(0, 24))
+        selected = int(rng.integers(2))
+        need = li.mx4_attend_workspace_bytes(R, Q, keys, bool(selected), H, kv, d)
+        shape = dict(R=R, Q=Q, H=H, KV=kv, d=d, qst=H * d, qsh=d, ost=H * d, osh=d, n=keys, idxs=keys, L=keys, bts=keys,
+                     bs=1, nb=4, dsb=kv * d // 2, dss=kv * d // 2, dsh=d // 2, ssb=kv * d // 32, sss=kv * d // 32,
+                     ssh=d // 32)
+        if need == ctypes.c_size_t(-1).value:
+            refused += 1
+            assert attend(lib, "selected" if selected else "window", **shape) == li.EINVAL
+            assert b"too large for one launch" in lib.indexer_last_error()
+        elif need:   # a workspace too small is refused after the size: nothing is launched
+            assert attend(lib, "selected" if selected else "window", wsn=need - 1, **shape) == li.EWORKSPACE
+    assert refused > 20, refused

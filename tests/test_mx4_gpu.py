@@ -988,3 +988,25 @@ def test_empty_calls():
     assert (out == 0).all() and torch.isneginf(lse).all()
     out, lse = li.mx4_attend_window(q, kd, ks, vd, vs, bt, sl, 1, 0, 0.1)
     assert (out == 0).all() and torch.isneginf(lse).all()
+
+
+def test_rows_near_the_limit_of_a_launch():
+    """131072 rows of 64 K/V heads of 192: 8.4 million workgroups of 256 threads, half of what a launch holds."""
+    rows, H, d, bs = 131072, 64, 192, 16
+    if torch.cuda.mem_get_info()[0] < 20 * 2**30:
+        pytest.skip("needs 20 GiB of free GPU memory")
+    case = Case(51, [40], 1, H, H, d, bs, "f16")
+    q, kd, ks, vd, vs, table, lens, _ = case.args()
+    idx = torch.full((rows, 2), -1, dtype=torch.int32, device=DEV)
+    idx[:, 0] = torch.arange(rows, device=DEV) % 40
+    q, table, lens = (t.expand(rows, *t.shape[1:]).contiguous() for t in (q, table, lens))
+    out, lse = li.mx4_attend_selected(q, kd, ks, vd, vs, table, lens, 1, idx, case.sm_scale)
+    # a row of one key is that key's V
+    v = plain.values(case.data[1], case.scale[1])[case.table[0][np.arange(40) // bs], np.arange(40) % bs]
+    v = torch.from_numpy(v).to(DEV).half()
+    assert torch.isfinite(lse).all()
+    for a in range(0, rows, 16384):
+        at = torch.arange(a, a + 16384, device=DEV) % 40
+        assert torch.equal(out[a:a + 16384], v[at])
+    del q, out, lse
+    torch.cuda.empty_cache()

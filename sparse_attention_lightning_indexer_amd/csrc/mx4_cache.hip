@@ -190,10 +190,12 @@ __global__ void __launch_bounds__(kThreads) mx4_read_kernel(Mx4Read a, int rows_
     }
 }
 
-// Tokens a workgroup takes: about kBatch chunks a thread, at least one token.
-int tokens_per_wg(int chunks_per_token) {
-    const int n = kBatch * kThreads / chunks_per_token;
-    return n < 1 ? 1 : n;
+// Tokens a workgroup takes: about kBatch chunks a thread, at least one token,
+// and as many as keep the launch below 2^32 threads.
+int tokens_per_wg(int64_t tokens, int chunks_per_token) {
+    const int64_t most = (int64_t)UINT32_MAX / kThreads, least = (tokens + most - 1) / most;
+    const int64_t n = kBatch * kThreads / chunks_per_token;
+    return (int)(n < least ? least : n);
 }
 
 // More values on the 16-bit side than the eight L2s hold (32 MiB): they pass
@@ -222,7 +224,7 @@ void read_launch(const Mx4Read &a, bool stream_out, dim3 grid, int per, hipStrea
 }  // namespace
 
 hipError_t launch_mx4_write(const Mx4Write &a, hipStream_t stream) {
-    const int per = tokens_per_wg((int)a.div_e.d);
+    const int per = tokens_per_wg(a.n_tokens, (int)a.div_e.d);
     const dim3 grid((unsigned)(((int64_t)a.n_tokens + per - 1) / per), (unsigned)a.n_tensors);
     const bool big = streams(a.n_tokens, a.n_heads, a.head_dim);
     a.bf16 ? write_launch<true>(a, big, grid, per, stream) : write_launch<false>(a, big, grid, per, stream);
@@ -230,7 +232,7 @@ hipError_t launch_mx4_write(const Mx4Write &a, hipStream_t stream) {
 }
 
 hipError_t launch_mx4_read(const Mx4Read &a, hipStream_t stream) {
-    const int per = tokens_per_wg((int)a.div_e.d);
+    const int per = tokens_per_wg(a.n_rows, (int)a.div_e.d);
     const dim3 grid((unsigned)(((int64_t)a.n_rows + per - 1) / per));
     const bool big = streams(a.n_rows, a.n_heads, a.head_dim);
     a.bf16 ? read_launch<true>(a, big, grid, per, stream) : read_launch<false>(a, big, grid, per, stream);

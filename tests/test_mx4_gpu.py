@@ -1010,3 +1010,27 @@ def test_rows_near_the_limit_of_a_launch():
         assert torch.equal(out[a:a + 16384], v[at])
     del q, out, lse
     torch.cuda.empty_cache()
+
+
+def test_more_tokens_than_a_launch_has_workgroups():
+    """2^24 + 300 tokens of 5120 values, where one token fills a workgroup of 256 threads: the first and the last
+    are written and read back, the others skipped."""
+    n, heads, d = 2**24 + 300, 160, 32
+    if torch.cuda.mem_get_info()[0] < 10 * 2**30:
+        pytest.skip("needs 10 GiB of free GPU memory")
+    line = torch.randn(((n + heads) * d,), device=DEV, dtype=torch.float16)
+    x = line.as_strided((n, heads, d), (d, d, 1))          # token t's head h is row t + h of one long tensor
+    some = torch.cat([torch.arange(5, device=DEV), torch.arange(n - 400, n, 7, device=DEV)])
+    slots = torch.full((n,), -1, dtype=torch.int64, device=DEV)
+    slots[some] = torch.arange(len(some), device=DEV)
+    cache, small = fresh(2, 64, heads, d), fresh(2, 64, heads, d)
+    li.mx4_cache_write(x, slots, *cache)
+    li.mx4_cache_write(x[some].contiguous(), torch.arange(len(some), device=DEV), *small)
+    assert all(torch.equal(a, b) for a, b in zip(cache, small))
+    # read: rows without a slot, zeros all, so that they may overlap
+    out = torch.full((n + 2 * heads, d), 7.0, device=DEV, dtype=torch.float16)
+    slots.fill_(-1)
+    got = li.mx4_cache_read(*cache, slots, out=out.as_strided((n, heads, d), (d, d, 1)))
+    assert (out[:n + heads - 1] == 0).all() and (out[n + heads - 1:] == 7.0).all() and got.shape == (n, heads, d)
+    del line, x, out, got
+    torch.cuda.empty_cache()

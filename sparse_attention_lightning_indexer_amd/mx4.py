@@ -219,9 +219,12 @@ def mx4_cache_read(data, scale, slots, dtype=None, out=None):
 
 def mx4_attend_workspace_bytes(n_requests: int, query_len: int, max_keys: int, selected: bool, n_heads: int,
                                n_kv_heads: int, head_dim: int) -> int:
-    """Workspace of an attention call (see include/indexer_mx4.h for max_keys)."""
-    return int(_library().indexer_mx4_attend_workspace_bytes(n_requests, query_len, max_keys, int(selected), n_heads,
-                                                             n_kv_heads, head_dim))
+    """Workspace of an attention call (see include/indexer_mx4.h for max_keys;
+    more than 2^31 - 1 of them count as that)."""
+    sizes = (n_requests, query_len, min(max_keys, 2**31 - 1), int(bool(selected)), n_heads, n_kv_heads, head_dim)
+    if not all(-2**31 <= n < 2**31 for n in sizes):   # ctypes would take their low 32 bits
+        raise ValueError(f"sizes out of the 32-bit range: {sizes}")
+    return int(_library().indexer_mx4_attend_workspace_bytes(*sizes))
 
 
 def _attend(entry, q, k_data, k_scale, v_data, v_scale, block_table, seq_lens, query_len, max_seq_len, sm_scale,

@@ -364,3 +364,16 @@ def test_no_call_that_the_query_accepts_is_refused_for_its_size(lib):
         elif need:   # a workspace too small is refused after the size: nothing is launched
             assert attend(lib, "selected" if selected else "window", wsn=need - 1, **shape) == li.EWORKSPACE
     assert refused > 20, refused
+
+
+def test_workspace_bytes_takes_no_size_by_its_low_32_bits():
+    need = li.mx4_attend_workspace_bytes(1, 1, 131072, False, 64, 8, 128)
+    most = li.mx4_attend_workspace_bytes(1, 1, 2**31 - 1, False, 64, 8, 128)
+    assert most >= need > 0
+    for keys in (2**31, 2**32 - 2, 2**32 + 32, 2**40):      # window + sinks of the largest windows
+        assert li.mx4_attend_workspace_bytes(1, 1, keys, False, 64, 8, 128) == most
+    for bad in ((2**32 + 1, 1, 131072, False, 64, 8, 128), (1, 2**32 + 1, 131072, False, 64, 8, 128),
+                (1, 1, 131072, False, 2**32 + 64, 8, 128), (1, 1, 131072, False, 64, 8, 2**32 + 128),
+                (1, 1, -2**33, False, 64, 8, 128)):
+        with pytest.raises(ValueError, match="32-bit"):
+            li.mx4_attend_workspace_bytes(*bad)

@@ -78,10 +78,11 @@ indexer_status check_pages(int32_t n_blocks, int32_t block_size, int32_t n_heads
     return INDEXER_OK;
 }
 
-indexer_status check_cache(const char *name, const void *data, const void *scale) {
-    if (!data) MX4_FAIL(INDEXER_EINVAL, "%s_data is NULL", name);
-    if (!scale) MX4_FAIL(INDEXER_EINVAL, "%s_scale is NULL", name);
-    if (!aligned(data, 16)) MX4_FAIL(INDEXER_EINVAL, "%s_data must be 16-byte aligned", name);
+// `of`: what the members' names begin with
+indexer_status check_cache(const char *of, const void *data, const void *scale) {
+    if (!data) MX4_FAIL(INDEXER_EINVAL, "%sdata is NULL", of);
+    if (!scale) MX4_FAIL(INDEXER_EINVAL, "%sscale is NULL", of);
+    if (!aligned(data, 16)) MX4_FAIL(INDEXER_EINVAL, "%sdata must be 16-byte aligned", of);
     return INDEXER_OK;
 }
 
@@ -115,8 +116,8 @@ indexer_status check_attend(const indexer_mx4_attend_args &g, lidx::Mx4Attend *a
     MX4_TRY(check_rows("q", g.q, g.q_stride_t, g.q_stride_h, g.n_heads, g.head_dim));
     MX4_TRY(check_rows("out", g.out, g.out_stride_t, g.out_stride_h, g.n_heads, g.head_dim));
     if (g.n_blocks > 0) {
-        MX4_TRY(check_cache("k", g.k_data, g.k_scale));
-        MX4_TRY(check_cache("v", g.v_data, g.v_scale));
+        MX4_TRY(check_cache("k_", g.k_data, g.k_scale));
+        MX4_TRY(check_cache("v_", g.v_data, g.v_scale));
     }
     if (!g.seq_lens) MX4_FAIL(INDEXER_EINVAL, "seq_lens is NULL");
     if (!aligned(g.seq_lens, 4) || !aligned(g.block_table, 4))
@@ -343,10 +344,10 @@ indexer_status indexer_mx4_cache_write(const indexer_mx4_write_args *args) {
     lidx::Mx4Write a{};
     MX4_TRY(check_pages(g.n_blocks, g.block_size, g.n_heads, g.head_dim, g.strides, &a.pages));
     MX4_TRY(check_rows("k", g.k, g.k_stride_t, g.k_stride_h, g.n_heads, g.head_dim));
-    if (g.n_blocks > 0) MX4_TRY(check_cache("k", g.k_data, g.k_scale));
+    if (g.n_blocks > 0) MX4_TRY(check_cache("k_", g.k_data, g.k_scale));
     if (g.v) {
         MX4_TRY(check_rows("v", g.v, g.v_stride_t, g.v_stride_h, g.n_heads, g.head_dim));
-        if (g.n_blocks > 0) MX4_TRY(check_cache("v", g.v_data, g.v_scale));
+        if (g.n_blocks > 0) MX4_TRY(check_cache("v_", g.v_data, g.v_scale));
     }
     if (!g.slots) MX4_FAIL(INDEXER_EINVAL, "slots is NULL");
     if (!aligned(g.slots, 8)) MX4_FAIL(INDEXER_EINVAL, "slots must be 8-byte aligned");
@@ -381,7 +382,7 @@ indexer_status indexer_mx4_cache_read(const indexer_mx4_read_args *args) {
     if (g.n_blocks < 1) MX4_FAIL(INDEXER_EINVAL, "n_blocks=%d must be >= 1 to read", g.n_blocks);
     lidx::Mx4Read a{};
     MX4_TRY(check_pages(g.n_blocks, g.block_size, g.n_heads, g.head_dim, g.strides, &a.pages));
-    MX4_TRY(check_cache("the cache's", g.data, g.scale));
+    MX4_TRY(check_cache("", g.data, g.scale));
     MX4_TRY(check_rows("out", g.out, g.out_stride_t, g.out_stride_h, g.n_heads, g.head_dim));
     if (!g.slots) MX4_FAIL(INDEXER_EINVAL, "slots is NULL");
     if (!aligned(g.slots, 8)) MX4_FAIL(INDEXER_EINVAL, "slots must be 8-byte aligned");

@@ -94,21 +94,22 @@ def _rows(t, name, dtype, dev, shape=None):
     return (st if n > 1 else heads * max(sh, d)), sh
 
 
-def _cache(data, scale, name, dev, heads, d):
-    """Checks one cache; its (n_blocks, block_size, strides in bytes)."""
+def _cache(data, scale, of, dev, heads, d):
+    """Checks one cache, whose arguments' names begin with `of`; its (n_blocks,
+    block_size, strides in bytes)."""
     uint8 = _torch.uint8
-    _need(data, f"{name}_data", uint8, dev, 4)
-    _need(scale, f"{name}_scale", uint8, dev, 4)
+    _need(data, of + "data", uint8, dev, 4)
+    _need(scale, of + "scale", uint8, dev, 4)
     blocks, size, h, w = data.shape
     if d % 32 or h != heads or 2 * w != d:
-        raise ValueError(f"{name}_data must be [n_blocks, block_size, {heads}, {d}/2] (head_dim a multiple of 32), got "
+        raise ValueError(f"{of}data must be [n_blocks, block_size, {heads}, {d}/2] (head_dim a multiple of 32), got "
                          f"{list(data.shape)}")
     if scale.shape != (blocks, size, heads, d // 32):
-        raise ValueError(f"{name}_scale must be {[blocks, size, heads, d // 32]}, got {list(scale.shape)}")
+        raise ValueError(f"{of}scale must be {[blocks, size, heads, d // 32]}, got {list(scale.shape)}")
     db, ds, dh, one = data.stride()
     sb, ss, sh, sone = scale.stride()
     if one != 1 or (sone != 1 and d > 32):
-        raise ValueError(f"{name}_data's and {name}_scale's last dimension must be contiguous")
+        raise ValueError(f"{of}data's and {of}scale's last dimension must be contiguous")
     # a dimension of one entry: its stride says nothing
     if heads == 1:
         dh, sh = w, d // 32
@@ -168,12 +169,12 @@ def mx4_cache_write(k, slots, k_data, k_scale, v=None, v_data=None, v_scale=None
     kind = _type_of(k.dtype)
     k_strides = _rows(k, "k", k.dtype, dev)
     n, heads, d = shape = tuple(k.shape)
-    pages = _cache(k_data, k_scale, "k", dev, heads, d)
+    pages = _cache(k_data, k_scale, "k_", dev, heads, d)
     _slots(slots, n, dev)
     v_args, v_strides = (0, 0), (0, 0)
     if v is not None and v_data is not None and v_scale is not None:
         v_strides = _rows(v, "v", k.dtype, dev, shape)
-        if not _like(v_data, v_scale, k_data, k_scale, dev) and _cache(v_data, v_scale, "v", dev, heads, d) != pages:
+        if not _like(v_data, v_scale, k_data, k_scale, dev) and _cache(v_data, v_scale, "v_", dev, heads, d) != pages:
             raise ValueError("the K and V caches must have the same shape and strides")
         v_args = (v_data.data_ptr(), v_scale.data_ptr())
     elif v is not None or v_data is not None or v_scale is not None:
@@ -198,7 +199,7 @@ def mx4_cache_read(data, scale, slots, dtype=None, out=None):
     if dtype is None:
         dtype = _torch.float16 if out is None else out.dtype
     kind = _type_of(dtype)
-    pages = _cache(data, scale, "k", dev, heads, d)
+    pages = _cache(data, scale, "", dev, heads, d)
     if not isinstance(slots, _torch.Tensor) or slots.dim() != 1:
         raise ValueError("slots must be a vector of slots")
     n = slots.shape[0]
@@ -238,8 +239,8 @@ def _attend(entry, q, k_data, k_scale, v_data, v_scale, block_table, seq_lens, q
     if not isinstance(k_data, torch.Tensor) or k_data.dim() != 4:
         raise ValueError("k_data must be [n_blocks, block_size, n_kv_heads, head_dim/2]")
     kv = k_data.shape[2]
-    pages = _cache(k_data, k_scale, "k", dev, kv, d)
-    if not _like(v_data, v_scale, k_data, k_scale, dev) and _cache(v_data, v_scale, "v", dev, kv, d) != pages:
+    pages = _cache(k_data, k_scale, "k_", dev, kv, d)
+    if not _like(v_data, v_scale, k_data, k_scale, dev) and _cache(v_data, v_scale, "v_", dev, kv, d) != pages:
         raise ValueError("the K and V caches must have the same shape and strides")
     _need(block_table, "block_table", torch.int32, dev, 2)
     _need(seq_lens, "seq_lens", torch.int32, dev, 1)

@@ -377,3 +377,19 @@ def test_workspace_bytes_takes_no_size_by_its_low_32_bits():
                 (1, 1, -2**33, False, 64, 8, 128)):
         with pytest.raises(ValueError, match="32-bit"):
             li.mx4_attend_workspace_bytes(*bad)
+
+
+def test_reading_names_its_own_arguments(lib):
+    for kw, msg in ((dict(data=None), b"data is NULL"), (dict(scale=None), b"scale is NULL"),
+                    (dict(data=A + 8), b"data must be 16-byte aligned")):
+        assert read(lib, **kw) == li.EINVAL
+        assert lib.indexer_last_error() == msg
+    torch = mx4._torch
+    data, scale = torch.zeros((2, 4, 3, 32), dtype=torch.uint8), torch.zeros((2, 4, 3, 2), dtype=torch.uint8)
+    dev = data.get_device()
+    assert mx4._cache(data, scale, "", dev, 3, 64)[:2] == (2, 4)
+    for of in ("", "k_", "v_"):
+        with pytest.raises(ValueError, match=f"^{of}scale must be"):
+            mx4._cache(data, scale[:1], of, dev, 3, 64)
+        with pytest.raises(ValueError, match=f"^{of}data must be"):
+            mx4._cache(data, scale, of, dev, 3, 96)

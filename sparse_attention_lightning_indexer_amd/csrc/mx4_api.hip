@@ -169,8 +169,8 @@ indexer_status run_attend(lidx::Mx4Attend &a, const indexer_mx4_attend_args &g, 
     // shared scales are loaded in whole 16-byte parts, those of 8 heads one after
     // the other; the order of the sums is the same either way
     const lidx::Mx4Pages &pages = a.pages;
-    p.share = selected && p.hp == 2 && p.head_group == 4 && (head_dim == 64 || head_dim == 128) && pages.s_sh == head_dim / 32 &&
-              pages.s_ss % 16 == 0 && pages.s_sb % 16 == 0 && aligned(a.ks, 16) && aligned(a.vs, 16);
+    p.share = p.share && pages.s_sh == head_dim / 32 && pages.s_ss % 16 == 0 && pages.s_sb % 16 == 0 &&
+              aligned(a.ks, 16) && aligned(a.vs, 16);
     if (!p.fits)
         MX4_FAIL(INDEXER_EINVAL, "problem too large for one launch: %lld workgroups of %d threads",
                  (long long)p.workgroups, p.threads);
@@ -309,6 +309,7 @@ Mx4Plan plan_mx4_attend(int n_requests, int q_len, int64_t max_keys, bool select
     if (p.hp == 2 && n_kv % 8 == 0 &&
         (max_keys <= 128 ? wgs >= kCus : selected && wgs >= (head_dim == 128 ? 2 : 3) * kCus)) {
         p.head_group = 4;
+        p.share = selected && (head_dim == 64 || head_dim == 128);
         p.n_splits = 1;
         p.ahead = 1;
         return sized(p, rows, n_heads, n_kv, head_dim);
@@ -445,6 +446,18 @@ size_t indexer_mx4_attend_workspace_bytes(int32_t n_requests, int32_t query_len,
     const lidx::Mx4Plan p =
         lidx::plan_mx4_attend(n_requests, query_len, max_keys, selected != 0, n_heads, n_kv_heads, head_dim);
     return p.fits ? p.workspace_bytes : (size_t)-1;
+}
+
+// The form an attention call takes, for tests that are meant for one of them:
+// many rows, shared scales (where the layout allows), tiles ahead, row tiles and
+// K/V heads of a wave, groups of heads of a workgroup, shares of a row's keys,
+// threads.  Not part of the interface.
+void lidx_mx4_attend_form(int32_t n_requests, int32_t query_len, int32_t max_keys, int32_t selected, int32_t n_heads,
+                          int32_t n_kv_heads, int32_t head_dim, int32_t form[8]) {
+    const lidx::Mx4Plan p =
+        lidx::plan_mx4_attend(n_requests, query_len, max_keys, selected != 0, n_heads, n_kv_heads, head_dim);
+    const int32_t fields[8] = {p.prompt, p.share, p.ahead, p.mt, p.hp, p.head_group, p.n_splits, p.threads};
+    for (int i = 0; i < 8; ++i) form[i] = fields[i];
 }
 
 }  // extern "C"

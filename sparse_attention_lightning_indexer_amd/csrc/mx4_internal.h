@@ -109,7 +109,7 @@ constexpr int kMx4PromptThreads = 512, kMx4JoinThreads = 256;
 // share a row's keys; a function of sizes alone.
 struct Mx4Plan {
     bool prompt;  // 256 rows of a request a workgroup, going through the keys together
-    bool share;   // the waves of a workgroup, on 8 K/V heads of a row, share their keys' scales
+    bool share;   // the waves of a workgroup, on 8 K/V heads of a row, share their keys' scales (if the layout allows)
     int ahead;    // tiles whose codes a wave has on the way
     int mt, hp, m_tiles, n_splits, head_group, units;
     int threads;        // of a workgroup

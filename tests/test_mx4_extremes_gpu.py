@@ -12,44 +12,21 @@ if not torch.cuda.is_available():  # pragma: no cover - CPU container
 
 import sparse_attention_lightning_indexer_amd as li  # noqa: E402
 from oracle import mx4 as plain  # noqa: E402
+from mx4_forms import FORMS, agrees, max_keys, meant, taken  # noqa: E402
 from test_mx4_gpu import DEV, Case, check, selection  # noqa: E402
 
-# (lens, query, heads, kv heads, d, block size), each a form of the kernels
-FORMS = {
-    "one tile, 64": ([90, 41], 4, 6, 2, 64, 16),
-    "one tile, 96": ([70, 37], 2, 8, 4, 96, 7),
-    "one tile, 128": ([70, 37], 4, 8, 2, 128, 16),
-    "one tile, 192": ([100, 33], 1, 16, 4, 192, 33),
-    "one tile, 256": ([64, 65], 2, 8, 2, 256, 16),
-    "two tiles, 64": ([90, 150], 3, 34, 2, 64, 32),
-    "two tiles, 96": ([90, 150], 3, 34, 2, 96, 32),
-    "two tiles, 128": ([90, 150], 3, 34, 2, 128, 32),
-    "two tiles, 192": ([90, 150], 3, 34, 2, 192, 32),
-    "two tiles, 256": ([90, 150], 3, 34, 2, 256, 32),
-    "pairs, 64": ([60, 33, 5, 70] * 16, 1, 32, 16, 64, 16),
-    "pairs, 96": ([60, 33, 5, 70] * 16, 1, 16, 16, 96, 16),
-    "pairs, 128": ([60, 33, 5, 70] * 16, 1, 64, 16, 128, 16),
-    "shared scales, 64": ([60, 33, 5, 70] * 4, 6, 64, 64, 64, 16),
-    "shared scales, 128": ([60, 33, 5, 70] * 4, 4, 64, 64, 128, 16),
-    "shares, 64": ([3300, 900], 1, 8, 2, 64, 32),
-    "shares, 128": ([3300, 900], 1, 16, 2, 128, 32),
-    "shares, 256": ([3300, 900], 1, 16, 2, 256, 32),
-    "ahead, 64": ([300, 513, 40, 90] * 4, 1, 16, 16, 64, 16),
-    "ahead, 128": ([300, 513, 40, 90] * 4, 1, 16, 16, 128, 16),
-    "prompt, 64": ([200, 64, 90, 330] * 4, 32, 64, 8, 64, 16),
-    "prompt, 96": ([200, 64, 90, 330] * 4, 37, 56, 8, 96, 7),
-    "prompt, 128": ([200, 64, 90, 330] * 4, 64, 32, 8, 128, 64),
-    "prompt shares, 64": ([9000], 650, 16, 8, 64, 64),
-}
-SAMPLE = 24   # rows of a large form compared with the plain form
+SAMPLE = 12   # rows of a large form compared with the plain form
 
 
-def form(name, seed, kind, **kw):
-    case = Case(seed, *FORMS[name], kind, **kw)
-    if name.startswith("ahead"):
-        case.max_seq_len = 2100
-        more = -(-2100 // case.bs) - case.table.shape[1]
-        case.table = np.concatenate([case.table, np.full((len(case.lens), more), -1, dtype=np.int32)], 1)
+def form(name, seed, kind):
+    """A case of the form's sizes; its calls take the form, which the test asserts."""
+    sizes = FORMS[name]
+    for how, want in meant(name).items():
+        assert agrees(taken(name, how), want), (name, how)
+    case = Case(seed, sizes.lens, sizes.query, sizes.heads, sizes.kv, sizes.d, sizes.bs, kind)
+    case.sizes, case.max_seq_len = sizes, sizes.max_seq_len
+    more = -(-case.max_seq_len // case.bs) - case.table.shape[1]
+    case.table = np.concatenate([case.table, np.full((len(case.lens), more), -1, dtype=np.int32)], 1)
     rows = case.q.shape[0]
     case.rows = np.arange(rows) if rows <= 64 else np.sort(case.rng.permutation(rows)[:SAMPLE])
     if rows > 64:   # the first and last rows of the first request
@@ -57,23 +34,27 @@ def form(name, seed, kind, **kw):
     return case
 
 
-def attended(case, how, positions=None, **kw):
+def attended(case, how):
     """(the call's out and lse, positions of a row) of a form of the attention."""
     args = case.args()
     if how == "selected":
-        idx = selection(case, min(2048, int(max(case.lens))) if positions is None else positions, holes=0.02)
-        got = li.mx4_attend_selected(*args, torch.from_numpy(idx).to(DEV), case.sm_scale, **kw)
+        idx = selection(case, max_keys(case.sizes, how), holes=0.02)
+        got = li.mx4_attend_selected(*args, torch.from_numpy(idx).to(DEV), case.sm_scale)
         return got, lambda t, v, e: plain.positions_selected(idx[t], 1, e)
-    window, sinks = (0, 0) if how == "causal" else (50, 3)
-    got = li.mx4_attend_window(*args, case.max_seq_len, case.sm_scale, window=window, sinks=sinks, **kw)
+    window, sinks = (0, 0) if how == "causal" else (case.sizes.window, case.sizes.sinks)
+    got = li.mx4_attend_window(*args, case.max_seq_len, case.sm_scale, window=window, sinks=sinks)
     return got, lambda t, v, e: plain.positions_window(v, e, window, sinks)
 
 
-def expected(case, positions, v=lambda x: x):
-    """The plain form of the case's sampled rows, V's values passed through `v`."""
+def numbers(case):
+    """K's and V's values."""
+    return [plain.values(d, s) for d, s in zip(case.data, case.scale)]
+
+
+def expected(case, positions, k, v):
+    """The plain form of the case's sampled rows."""
     few = set(case.rows.tolist())
-    k, val = (plain.values(d, s) for d, s in zip(case.data, case.scale))
-    o, z, b = plain.attend_rows(case.q, k, v(val), case.table, case.lens, case.query, case.max_seq_len, case.sm_scale,
+    o, z, b = plain.attend_rows(case.q, k, v, case.table, case.lens, case.query, case.max_seq_len, case.sm_scale,
                                 lambda t, vis, e: positions(t, vis, e) if t in few else [])
     return o[case.rows], z[case.rows], {n: x[case.rows] for n, x in b.items()}
 
@@ -81,6 +62,30 @@ def expected(case, positions, v=lambda x: x):
 def sampled(case, got):
     pick = torch.from_numpy(case.rows).to(DEV)
     return tuple(x[pick] for x in got)
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("name", list(FORMS))
+def test_every_form(name, kind):
+    """Ordinary numbers, pages outside the cache, and blocks of NaN that some rows and heads see and others do not."""
+    case = form(name, 63, kind)
+    kv_values = numbers(case)
+    for how in ("causal", "window", "selected"):
+        got, positions = attended(case, how)
+        check(sampled(case, got), expected(case, positions, *kv_values), kind, case.d, f"{name} {how} {kind}")
+    R, kv = len(case.lens), case.kv
+    case.table[R // 2, 0] = -1
+    case.table[R - 1, (int(case.lens[R - 1]) - 1) // case.bs // 2] = case.n_blocks
+    for i, r in enumerate(range(0, R, 2)):
+        last = int(case.lens[r]) - 1
+        for which, p, head, block in ((1, last, i % kv, 1), (0, last - 1, (i + 1) % kv, 0), (1, 3, (i + 2) % kv, 0)):
+            page = case.table[r, p // case.bs]
+            if p >= 0 and 0 <= page < case.n_blocks:
+                case.scale[which][page, p % case.bs, head, block] = 255
+    kv_values = numbers(case)
+    for how in ("causal", "window", "selected"):
+        got, positions = attended(case, how)
+        check(sampled(case, got), expected(case, positions, *kv_values), kind, case.d, f"{name} {how} {kind}, NaN and bad pages")
 
 
 # V's values end at 6 * 2^13 (f16) and 6 * 2^125 (bf16), scale bytes 140 and 252: the largest
@@ -100,14 +105,16 @@ def test_values_past_the_type_stay_with_their_rows(name, kind):
     for i, r in enumerate(range(0, len(case.lens), 3)):
         last = int(case.lens[r]) - 1
         # the last key (the last query alone sees it), one out of the window, one among the first
-        for p, head, block in ((last, i % kv, i % blocks), (last - 57 - Q, (i + 1) % kv, blocks - 1), (4, (i + 2) % kv, 0)):
+        for p, head, block in ((last, i % kv, i % blocks), (last - case.sizes.window - 7 - Q, (i + 1) % kv, blocks - 1), (4, (i + 2) % kv, 0)):
             if p >= 0:
                 case.scale[1][case.table[r, p // case.bs], p % case.bs, head, block] = scales[i % len(scales)]
     hit = False
+    k, v = numbers(case)
+    v = np.clip(v, -most, most)
     for how in ("causal", "window", "selected"):
         got, positions = attended(case, how)
         out, lse = sampled(case, got)
-        o, z, b = expected(case, positions, lambda x: np.clip(x, -most, most))
+        o, z, b = expected(case, positions, k, v)
         huge = b["plain"] >= 2.0**100           # bf16: weights times such values pass f32's range in rows that see them
         hit |= bool((b["plain"] >= 40000).any())
         assert torch.isfinite(out[torch.from_numpy(~huge).to(DEV)]).all(), (name, how)
@@ -124,10 +131,10 @@ def test_scores_far_from_zero(name, power, kind):
     case = form(name, 61, kind)
     case.sm_scale = 2.0**power
     checked = 0
+    k, val = numbers(case)
     for how in ("causal", "window", "selected"):
         got, positions = attended(case, how)
         out, lse = (x.double().cpu().numpy() for x in sampled(case, got))
-        k, val = (plain.values(d, s) for d, s in zip(case.data, case.scale))
         for i, t in enumerate(case.rows):
             r, j = divmod(int(t), case.query)
             vis = int(case.lens[r]) - case.query + 1 + j
@@ -175,9 +182,10 @@ def test_many_small_weights_beside_a_large_one(name, first, kind):
         page, off = case.table[r, p // case.bs], p % case.bs
         case.data[0][page, off, :, 1] = 0x60
         case.data[1][page, off] = 0
+    kv_values = numbers(case)
     for how in ("causal", "selected"):
         got, positions = attended(case, how)
-        o, z, b = expected(case, positions)
+        o, z, b = expected(case, positions, *kv_values)
         out, lse = (x.double().cpu().numpy() for x in sampled(case, got))
         n = b["count"][:, None]
         unit = {"f16": 2.0**-11, "bf16": 2.0**-8}[kind]

@@ -236,7 +236,8 @@ static Mx4Plan sized(Mx4Plan p, int64_t rows, int n_heads, int n_kv, int head_di
 //
 // Many rows of a request under a window go through the keys 256 at a time and
 // together (mx4_prompt_kernel) where that is the shorter of two estimates, fit
-// to head dimension 128 and 8 K/V heads of 8 query heads: 2.05 us for 64 keys
+// to head dimension 128 and 8 K/V heads of 8 query heads (other dimensions are
+// taken in proportion; which form is shorter was not measured there): 2.05 us for 64 keys
 // and 256 rows a compute unit (1.8 us half full), rounds of one workgroup a
 // compute unit and 10 us, the keys shared out where that fills the last round
 // better, at the price of a second launch and of the shares' traffic; against

@@ -10,7 +10,8 @@
 // of 32 keys of its own; the waves of a workgroup take the tiles of a row's
 // keys in turn and join their (m, l, product) through LDS at the end, and rows
 // with too few workgroups share their keys among several, joined by a second
-// kernel.  Nothing in the loop waits for another wave.
+// kernel.  Nothing in the loop waits for another wave, but for the barrier of a
+// pair of tiles where waves share scales (below).
 //
 //  - Scores: S^T = K Q^T on 16x16x32 MFMAs.  The contraction runs over the
 //    head dimension in any order both operands agree on, so a lane takes
@@ -21,28 +22,38 @@
 //  - A lane then holds 8 scores of one query row, (l & 15), which is the
 //    layout the product's P operand wants: P never leaves its lane, and
 //    neither do m, l and the rescaling of O^T = V^T P^T.
-//    The weights are rounded to the query's type there (the product takes one
-//    type; half a step of it each, averaged over the keys, is what the output's
-//    own rounding costs); their sum and everything else stays f32.
+//    The weights are rounded to the query's type there: the product takes both
+//    operands in one type, and a second product with what the rounding left
+//    would be half as many matrix instructions again.  Half a step of the type
+//    each, averaged over the keys, is no more than the output's own rounding:
+//    against 64 bits outputs are 1.1 to 1.4 times as far off as 32-bit sums
+//    rounded once.  The weights' sum and everything else stays f32.
 //  - V's rows are converted like K's, stored to the wave's own LDS rows and
 //    read back transposed (ds_read_b64_tr_b16), 16 dimensions by 4 keys each.
 //    Rows are padded by 32 bytes: the 8 consecutive rows that half a wave reads
-//    32 bytes of, or writes 16 bytes of, then lie in different banks.
+//    32 bytes of, or writes 16 bytes of, then lie in different banks.  Conflicts
+//    are still 0.39 of the cycles that LDS is active (shared scales, selected
+//    keys; 0.16 in the many-rows kernel); which accesses they belong to was not
+//    found out.
 //  - Keys picked one by one come from beyond the L2s, in lines of 128 bytes: a
 //    row of 4 bytes of scales costs what two rows of codes do.  Where the four
 //    waves of a workgroup take the same keys of 8 K/V heads (SHARE), the scales
 //    of all heads come in one load for 64 keys at a time, through LDS, one
 //    barrier for them: 10 lines a key instead of up to 16.  1024 rows x 2048 of
 //    131072 keys, 8 heads of 128: 450 us apart, 390-410 us shared, when 2.6 GB
-//    pass the L2s at 6.5 TB/s, as fast as this card reads memory.
+//    pass the L2s at 6.4 TB/s; a plain read of 143 MB, the cache's size, which
+//    the Infinity Cache holds, reaches 6.75, one of 4 GiB 6.3.
 //  - Loads run ahead: a tile's codes from when the one before (PF = 2: two
 //    before) is converted, the page ids a pair of tiles further, the selected
 //    indices one more.
 //
 // Measured, 64 query heads on 8 K/V heads of 128: one row over 131072 keys 31 us
-// (bf16, 4.6 TB/s: memory); 128 rows x 2048 keys of 32 requests 68 us (bf16, 4.3
-// TB/s in gathered rows); 32 rows under a window of 1024 13.7 us and 32 rows x 512
-// keys 9.2 us (f16: the latency of dependent loads and few tiles a wave).
+// (bf16, 4.6 TB/s: memory, with the loads of a pair of tiles drained once a pair,
+// where the scale bytes are widened); 128 rows x 2048 keys of 32 requests 64 us
+// (bf16, 4.5 TB/s in gathered rows); 32 rows under a window of 1024 13.3 us and
+// 32 rows x 512 keys 9.5 us (f16: the latency of dependent loads and few tiles a
+// wave; the first product also waits for the indices and page ids of a second
+// pair of tiles, which rows of two tiles a wave do not have).
 //
 // Masked positions: their scores become -inf by selection, so K's NaN there
 // never spreads; V's blocks of NaN are replaced by zeros in the product, and
@@ -233,7 +244,9 @@ __device__ __forceinline__ Item item_of(const Mx4Attend &a, int mt, int hp) {
 // runs of `pool` keys.
 enum Mode { kWindow = 0, kKeys = 1, kPools = 2 };
 
-// Waves per SIMD the registers have to leave room for.
+// Waves per SIMD the registers have to leave room for.  Three (168 registers) are
+// not quite enough for two K/V heads a wave at head dimension 128 with selected
+// keys of their own in f16 (8 bytes a lane in scratch) and at 96 (8 to 16 bytes).
 template <int D, int MT, int HP, int PF>
 constexpr int waves_per_simd() {
     if (PF == 2) return 2;
@@ -351,8 +364,9 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
 
     // The steps from a pair of tiles to its offsets.  Each loads from a place
     // that exists whatever the lane's key (a clamped entry, page 0 of the table,
-    // slot 0 of the cache), so none branches and the loads of a step overlap; a
-    // position of -1 and the bits of `found` say what counts.
+    // slot 0 of the cache), so none branches on a key and the loads of a step
+    // overlap (`congruent` is one branch of the whole wave); a position of -1 and
+    // the bits of `found` say what counts.
     // 1: the entry's selected index
     auto load_index = [&](int tile) -> int {
         const uint32_t e = ((uint32_t)tile + own_tile) * 32u + own_key;
@@ -862,9 +876,11 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
 //
 // Measured, 64 query heads on 8 K/V heads of 128: 1024 causal tokens over 16384
 // keys 511 us (f16, 1.04 PFLOP/s, where an 8192-cubed library product reaches
-// 1.19), 1000 tokens under a window of 4096 157 us (bf16, 0.87 PFLOP/s).  The
-// vector units are busy for 48% of the time and the matrix units for 43%, with
-// two waves a SIMD to overlap them.
+// 1.19), 1000 tokens under a window of 4096 157-161 us back to back and 149 us a
+// call with other inputs between (bf16, 0.85-0.91 PFLOP/s: the longer the
+// products run without a pause, the lower the clock).  The vector units are busy
+// for 49% of the time and the matrix units for 43%, with two waves a SIMD to
+// overlap them.
 template <int D>
 struct PromptShape {
     static constexpr int MT = 2, W = kMx4PromptThreads / 64, KEYS = 64, ROWS = W * 16 * MT;

@@ -48,12 +48,13 @@
 //    indices one more.
 //
 // Measured, 64 query heads on 8 K/V heads of 128: one row over 131072 keys 31 us
-// (bf16, 4.6 TB/s: memory, with the loads of a pair of tiles drained once a pair,
-// where the scale bytes are widened); 128 rows x 2048 keys of 32 requests 64 us
-// (bf16, 4.5 TB/s in gathered rows); 32 rows under a window of 1024 13.3 us and
-// 32 rows x 512 keys 9.5 us (f16: the latency of dependent loads and few tiles a
-// wave; the first product also waits for the indices and page ids of a second
-// pair of tiles, which rows of two tiles a wave do not have).
+// (bf16, 4.6 TB/s: memory); 128 rows x 2048 keys of 32 requests 64 us (bf16, 4.5
+// TB/s in gathered rows); 32 rows under a window of 1024 13.3 us and 32 rows x 512
+// keys 9.5 us (f16: the latency of dependent loads and few tiles a wave).  In the
+// code as compiled the scale bytes of the next tile are widened at the end of a
+// tile (of a pair of them where two are on the way), which waits for all loads on
+// the way, and the first product waits for the indices and page ids of a second
+// pair of tiles, which rows of two tiles a wave do not have.
 //
 // Masked positions: their scores become -inf by selection, so K's NaN there
 // never spreads; V's blocks of NaN are replaced by zeros in the product, and

@@ -126,6 +126,62 @@ def test_values_past_the_type_stay_with_their_rows(name, kind):
 
 @pytest.mark.parametrize("kind", ["f16", "bf16"])
 @pytest.mark.parametrize("name", list(FORMS))
+def test_keys_past_the_type_stay_with_their_rows(name, kind):
+    """K's values that the query's type does not hold are infinite: rows that do not see them, and other heads, are as
+    without them (whatever the rows are that do)."""
+    case = form(name, 64, kind)
+    _, scales = ENDS[kind]
+    kv, blocks = case.kv, case.d // 32
+    clean = numbers(case)
+    k = clean[0].copy()
+    for i, r in enumerate(range(0, len(case.lens), 3)):
+        last = int(case.lens[r]) - 1
+        for p, head, block in ((last, i % kv, i % blocks), (last - case.sizes.window - 7 - case.query, (i + 1) % kv, blocks - 1),
+                               (4, (i + 2) % kv, 0)):
+            if p >= 0:
+                at = case.table[r, p // case.bs], p % case.bs, head
+                case.scale[0][at + (block,)] = scales[i % len(scales)]
+                k[at + (slice(32 * block, 32 * block + 32),)] = np.nan
+    seen = 0
+    for how in ("causal", "window", "selected"):
+        got, positions = attended(case, how)
+        out, lse = (x.double().cpu() for x in sampled(case, got))
+        o, z, b = expected(case, positions, k, clean[1])
+        theirs = torch.from_numpy(np.isnan(z))            # rows and heads that attend to such a key
+        seen += int(theirs.sum())
+        out[theirs], lse[theirs] = float("nan"), float("nan")
+        o[np.isnan(z)] = np.nan
+        for n in ("reach", "top"):
+            b[n] = np.nan_to_num(b[n])
+        check((out, lse), (o, z, b), kind, case.d, f"{name} {how} {kind}")
+    assert seen
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("name", list(FORMS))
+def test_queries_of_nan_and_infinity_stay_alone(name, kind):
+    """Rows of a padded batch may hold anything: q of NaN, infinity and the largest number changes its own row and head."""
+    case = form(name, 65, kind)
+    k, v = numbers(case)
+    big = float(torch.finfo(case.q_t.dtype).max)
+    theirs = np.zeros(case.q.shape[:2], dtype=bool)
+    for i, t in enumerate(case.rows[::2]):
+        for h in range(i % 3, case.heads, 5):
+            case.q_t[t, h, i % case.d:] = (float("nan"), float("inf"), -float("inf"), big)[(i + h) % 4]
+            theirs[t, h] = True
+    case.q = np.where(theirs[..., None], 0.0, case.q)
+    theirs = theirs[case.rows]
+    for how in ("causal", "window", "selected"):
+        got, positions = attended(case, how)
+        out, lse = (x.double().cpu() for x in sampled(case, got))
+        o, z, b = expected(case, positions, k, v)
+        out[torch.from_numpy(theirs)], lse[torch.from_numpy(theirs)] = float("nan"), float("nan")
+        o[theirs], z[theirs] = np.nan, np.nan
+        check((out, lse), (o, z, b), kind, case.d, f"{name} {how} {kind}")
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("name", list(FORMS))
 def test_scores_far_from_zero(name, kind):
     """Scores past 2^20: where one key leads by more than the scores' own error, the row is its V, and lse its score."""
     case = form(name, 61, kind)

@@ -1,0 +1,332 @@
+"""The page operators on the GPU against the plain forms on lists, bit for bit."""
+import copy
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # pragma: no cover - CPU container
+    pytest.skip("needs a GPU", allow_module_level=True)
+
+import sparse_attention_lightning_indexer_amd as li  # noqa: E402
+from oracle import pages as plain  # noqa: E402
+
+DEV = torch.device("cuda:0")
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+class Pool:
+    """The state on the GPU and on lists."""
+
+    def __init__(self, n_pages, rows, cols, bs, seed=0, shapes=((16, 3, 32), (16, 3, 4), (5,), (16, 24)),
+                 dtypes=(torch.uint8, torch.uint8, torch.uint8, torch.float16)):
+        self.rng = np.random.default_rng(seed)
+        self.bs = bs
+        self.gpu = [torch.from_numpy(self.rng.integers(0, 100, (n_pages,) + s)).to(t).to(DEV)
+                    for s, t in zip(shapes, dtypes)]
+        self.set = li.PageSet(self.gpu)
+        self.caches = [t.cpu().numpy() for t in self.gpu]
+        self.refs, self.table, self.lens = [0] * n_pages, [[-1] * cols for _ in range(rows)], [0] * rows
+        self.g_refs = torch.zeros(n_pages, dtype=torch.int32, device=DEV)
+        self.g_table = torch.full((rows, cols + 3), -1, dtype=torch.int32, device=DEV)[:, :cols]
+        self.g_lens = torch.zeros(rows, dtype=torch.int32, device=DEV)
+
+    def put(self):
+        """The lists' state onto the GPU."""
+        self.g_refs.copy_(ints(self.refs))
+        self.g_table.copy_(ints(self.table))
+        self.g_lens.copy_(ints(self.lens))
+
+    def same(self, where=""):
+        assert self.g_refs.tolist() == self.refs, where
+        assert self.g_table.tolist() == self.table, where
+        assert self.g_lens.tolist() == self.lens, where
+        for a, b in zip(self.gpu, self.caches):
+            assert np.array_equal(a.cpu().numpy(), b), where
+
+    def grow(self, rows, tokens, new=None):
+        got = li.pages_grow(self.g_refs, self.g_table, self.g_lens, ints(rows), tokens, self.bs,
+                            None if new is None else ints(new))
+        want = plain.grow(self.refs, self.table, self.lens, rows, tokens, self.bs, new)
+        assert got.tolist() == want
+        return got
+
+    def fork(self, parents, children):
+        got = li.pages_fork(self.set, self.g_refs, self.g_table, self.g_lens, ints(parents), ints(children), self.bs)
+        want = plain.fork(self.caches, self.refs, self.table, self.lens, parents, children, self.bs)
+        assert got.tolist() == want
+
+    def free(self, rows):
+        li.pages_free(self.g_refs, self.g_table, self.g_lens, ints(rows))
+        plain.free(self.refs, self.table, self.lens, rows)
+
+    def compact(self):
+        place, live = li.pages_compact(self.set, self.g_refs, self.g_table)
+        want = plain.compact(self.caches, self.refs, self.table)
+        assert place.tolist() == want[0] and live.tolist() == [want[1]]
+
+
+@pytest.mark.parametrize("n_pages,rows,cols,bs,steps", [
+    (60, 12, 9, 4, 60), (7, 5, 4, 3, 40), (300, 40, 30, 1, 30), (400, 9, 300, 16, 30), (2000, 70, 20, 5, 25),
+    (1, 2, 2, 2, 10), (20000, 30, 700, 16, 12),
+])
+def test_a_life_of_requests(n_pages, rows, cols, bs, steps):
+    """Random calls one after the other, pools that run out among them; padding and rows named twice in the lists."""
+    p = Pool(n_pages, rows, cols, bs, seed=n_pages)
+    rng = p.rng
+
+    def some(n, extra=True):
+        out = rng.permutation(rows)[:n].tolist()
+        if extra and rng.random() < 0.5:
+            out += [-1, rows, out[0] if out else -7]
+        return out
+    for step in range(steps):
+        what = rng.integers(0, 5)
+        if what == 0:
+            tokens = int(rng.integers(1, max(2, cols * bs // 2)))
+            members = some(int(rng.integers(1, max(2, rows // 2))))
+            new = None if rng.random() < 0.5 else rng.integers(-1, tokens + 2, len(members)).tolist()
+            p.grow(members, tokens, new)
+        elif what == 1:
+            p.grow(some(rows), 1)
+        elif what == 2:
+            order = rng.permutation(rows).tolist()
+            parents, children = order[:max(1, rows // 3)], order[max(1, rows // 3):]
+            p.free(children)
+            pick = [parents[i] for i in rng.integers(0, len(parents), len(children))]
+            if rng.random() < 0.5 and children:
+                pick += [rows + 3, parents[0], -1]
+                children += [children[0], children[-1], parents[0]]
+            p.fork(pick, children)
+        elif what == 3:
+            p.free(some(int(rng.integers(1, rows))))
+        else:
+            p.compact()
+        p.same((step, int(what)))
+    # nothing is lost: without requests every page is free again
+    p.free(list(range(rows)))
+    p.same()
+    assert not any(p.refs)
+
+
+def test_children_of_one_parent_and_of_several():
+    """64 children in any order of three parents, one of whole pages, one empty."""
+    p = Pool(500, 70, 40, 8, seed=4)
+    p.grow([0, 1, 2], 300, [299, 160, 0])
+    p.fork([int(i) for i in p.rng.integers(0, 3, 64)], list(range(3, 67)))
+    p.same()
+    p.grow(list(range(70)), 9)
+    p.same()
+
+
+def test_long_slots():
+    """A prompt's worth of slots, which a second launch writes; rows that cannot grow among them."""
+    p = Pool(3000, 5, 900, 16, seed=5)
+    p.grow([3, 1, -1, 4, 3], 14000, [14000, 3001, 5, 0, 9])
+    p.same()
+    p.grow([0, 2, 4], 14397, [14397, 14001, 14400])   # the second finds too few pages
+    p.same()
+
+
+@pytest.mark.parametrize("n_pages", [40000, 16384, 16385])
+def test_large_pools(n_pages):
+    """More pages than the decision looks at in one step: free ones only far behind, and compaction of all."""
+    p = Pool(n_pages, 6, 20, 4, seed=6, shapes=((3,),), dtypes=(torch.uint8,))
+    p.refs = [1] * (n_pages - 60) + [0] * 60
+    for i in range(0, n_pages - 60, 4001):
+        p.refs[i] = 0
+    p.put()
+    p.grow([0, 1, 2], 70)
+    p.fork([0, 0, 1, 2], [3, 4, 4, 5])
+    p.same()
+    p.refs = [int(r > 0 and p.rng.random() < 0.5) for r in p.refs]   # whatever they were, half of them go
+    p.table = [[e if e >= 0 and p.refs[e] else -1 for e in row] for row in p.table]
+    p.put()
+    p.compact()
+    p.same()
+
+
+def test_copies():
+    """Pages in any order; pairs outside the pool or of one page are skipped."""
+    p = Pool(50, 1, 1, 4, seed=8)
+    order = p.rng.permutation(50).tolist()
+    source, target = order[:20] + [-1, 3, 50, 7], order[20:40] + [4, 50, 5, 7]
+    target[20] = order[45]
+    li.pages_copy(p.set, ints(source), ints(target))
+    plain.copy(p.caches, source, target)
+    p.same()
+    li.pages_copy(p.gpu, ints(source[:1] * 3), ints(order[41:44]))     # one page to several, the caches as a list
+    plain.copy(p.caches, source[:1] * 3, order[41:44])
+    p.same()
+
+
+def test_pages_of_any_size_and_place():
+    """Pages of 1 to 70001 bytes, strided, at odd addresses, heads before slots; more caches than one launch takes."""
+    rng = np.random.default_rng(9)
+    n = 30
+    tensors = []
+    for i, size in enumerate([1, 3, 4, 16, 17, 64, 255, 256, 257, 1024, 4095, 4096, 4097, 16384, 70001] * 6):
+        room = torch.from_numpy(rng.integers(0, 256, (n, size + 40)).astype(np.uint8)).to(DEV)
+        tensors.append(room[:, (i % 5) * 4 + (i % 3):][:, :size])
+    tensors.append(torch.randn((n, 4, 6, 32), device=DEV).half().transpose(1, 2))     # heads before slots
+    tensors.append(torch.randn((n, 8), device=DEV)[:, None].double())
+    assert len(tensors) > 64
+    want = [t.clone() for t in tensors]
+    around = [t._base.clone() if t._base is not None else None for t in tensors]
+    order = rng.permutation(n)
+    a, b = order[:12], order[12:24]
+    li.pages_copy(tensors, ints(a.tolist()), ints(b.tolist()))
+    at, bt = torch.from_numpy(a).to(DEV), torch.from_numpy(b).to(DEV)
+    for t, w in zip(tensors, want):
+        w[bt] = w[at]
+        assert torch.equal(t, w), t.shape
+    # nothing between the pages has moved
+    for t, base in zip(tensors[:90], around):
+        off = t.storage_offset() % base.shape[1]
+        assert torch.equal(t._base[:, :off], base[:, :off])
+        assert torch.equal(t._base[:, off + t.shape[1]:], base[:, off + t.shape[1]:])
+
+
+def test_a_cache_past_2_to_the_32_bytes():
+    t = torch.zeros((70, 1 << 26), dtype=torch.uint8, device=DEV)
+    t[68, 5], t[69, -1] = 3, 4
+    li.pages_copy([t], ints([68, 69]), ints([1, 66]))
+    assert int(t[1, 5]) == 3 and int(t[66, -1]) == 4 and int(t.sum(dtype=torch.long)) == 14
+
+
+def test_bad_entries_are_passed_over():
+    """Tables with pages that are not there: never followed, and not handed on."""
+    p = Pool(20, 4, 5, 4, seed=10)
+    p.grow([0], 14)
+    p.table[0][1], p.table[0][3] = 99, 20
+    p.table[2] = [-5, 3, 20, -1, -1]
+    p.refs[3] += 1
+    p.put()
+    p.fork([0], [1])
+    p.same()
+    p.free([2, 0])
+    p.same()
+    p.table[3] = [77, -9, -1, 2**31 - 1, -2**31]
+    p.put()
+    p.compact()
+    p.same()
+
+
+def test_no_bytes_and_empty_calls():
+    p = Pool(30, 4, 6, 4, seed=11)
+    p.grow([0], 9)
+    before = [t.clone() for t in p.gpu]
+    fresh = li.pages_fork(None, p.g_refs, p.g_table, p.g_lens, ints([0]), ints([2]), p.bs)
+    assert fresh.tolist() == plain.fork([], p.refs, p.table, p.lens, [0], [2], p.bs)
+    p.free([0])
+    place, live = li.pages_compact(None, p.g_refs, p.g_table)
+    assert (place.tolist(), live.tolist()[0]) == plain.compact([], p.refs, p.table)
+    assert all(torch.equal(a, b) for a, b in zip(p.gpu, before))
+    none = ints([])
+    li.pages_copy(p.set, none, none)
+    li.pages_free(p.g_refs, p.g_table, p.g_lens, none)
+    assert li.pages_fork(p.set, p.g_refs, p.g_table, p.g_lens, none, none, 4).shape == (0,)
+    assert li.pages_grow(p.g_refs, p.g_table, p.g_lens, none, 3, 4).shape == (0, 3)
+    assert li.pages_grow(p.g_refs, p.g_table, p.g_lens, ints([1]), 0, 4).shape == (1, 0)
+    p.same()
+    # a pool without pages, a table without columns, a table without rows
+    empty = torch.empty(0, dtype=torch.int32, device=DEV)
+    place, live = li.pages_compact(None, empty, p.g_table.new_empty((0, 4)))
+    assert place.shape == (0,) and live.tolist() == [0]
+    lens = ints([3, 4])
+    li.pages_free(p.g_refs, p.g_table.new_empty((2, 0)), lens, ints([1]))
+    assert lens.tolist() == [3, 0]
+    lens = ints([3, 0])
+    table = ints([[-1, -1], [-1, -1]])
+    assert li.pages_grow(empty, table, lens, ints([0, 1]), 1, 4).tolist() == [[-1], [-1]]
+    lens = ints([3, 0])
+    assert li.pages_fork(None, empty, table, lens, ints([0]), ints([1]), 4).tolist() == [-2]
+    assert li.pages_grow(p.g_refs, p.g_table.new_empty((0, 4)), empty, ints([0, -1]), 2, 4).tolist() == [[-1, -1]] * 2
+
+
+def test_refusals():
+    p = Pool(10, 3, 4, 4)
+    state = (p.g_refs, p.g_table, p.g_lens)
+    rows = ints([0])
+    for error, call in [
+        (ValueError, lambda: li.PageSet([])),
+        (ValueError, lambda: li.PageSet([torch.zeros(4, 4)])),
+        (ValueError, lambda: li.PageSet([p.gpu[0], p.gpu[1][:5]])),
+        (ValueError, lambda: li.PageSet([p.gpu[0][..., :16]])),
+        (ValueError, lambda: li.PageSet([p.gpu[0][:, :0]])),
+        (li.IndexerError, lambda: li.pages_copy([torch.zeros(1, 8, device=DEV).expand(9, 8)], rows, rows)),
+        (TypeError, lambda: li.pages_copy(p.set, rows.long(), rows)),
+        (ValueError, lambda: li.pages_copy(p.set, rows, ints([1, 2]))),
+        (ValueError, lambda: li.pages_copy(p.set, rows.cpu(), rows)),
+        (ValueError, lambda: li.pages_fork(p.set, p.g_refs[:5], p.g_table, p.g_lens, rows, rows, 4)),
+        (ValueError, lambda: li.pages_fork(p.set, *state, rows, ints([1, 2]), 4)),
+        (li.IndexerError, lambda: li.pages_fork(p.set, *state, rows, rows, 0)),
+        (ValueError, lambda: li.pages_grow(p.g_refs, p.g_table, p.g_lens[:2], rows, 1, 4)),
+        (ValueError, lambda: li.pages_grow(*state, rows, -1, 4)),
+        (ValueError, lambda: li.pages_grow(*state, rows, 1, 4, ints([1, 2]))),
+        (ValueError, lambda: li.pages_grow(*state, rows, 1, 4, slots=torch.zeros((1, 2), dtype=torch.long, device=DEV))),
+        (ValueError, lambda: li.pages_free(p.g_refs, p.g_table.t(), p.g_lens, rows)),
+        (TypeError, lambda: li.pages_free(p.g_refs.float(), p.g_table, p.g_lens, rows)),
+        (ValueError, lambda: li.pages_compact(p.set, p.g_refs, p.g_table, place=ints([1]))),
+        (li.IndexerError, lambda: li.pages_compact(p.set, p.g_refs, p.g_table,
+                                                   workspace=torch.zeros(8, dtype=torch.uint8, device=DEV))),
+    ]:
+        with pytest.raises(error):
+            call()
+    p.same()
+
+
+def test_a_stream_and_a_graph():
+    """A step of a server captured once and replayed: free, fork, grow and compact, with eager calls between."""
+    p = Pool(200, 12, 8, 4, seed=12)
+    p.grow([0, 1], 27, [27, 13])
+    parents, children = [0, 1, 0, 0], [4, 5, 6, 11]
+    args = (ints(parents), ints(children))
+    fresh, slots = torch.empty(4, dtype=torch.int32, device=DEV), torch.empty((4, 3), dtype=torch.long, device=DEV)
+    place, live = torch.empty(200, dtype=torch.int32, device=DEV), torch.empty(1, dtype=torch.int32, device=DEV)
+    workspace = torch.empty(li.pages_compact_workspace_bytes(200), dtype=torch.uint8, device=DEV)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):      # another stream than the tensors' own
+        li.pages_fork(p.set, p.g_refs, p.g_table, p.g_lens, *args, p.bs)
+    torch.cuda.current_stream().wait_stream(side)
+    plain.fork(p.caches, p.refs, p.table, p.lens, parents, children, p.bs)
+    p.same()
+    state = (p.g_refs, p.g_table, p.g_lens)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        li.pages_free(*state, args[1])
+        li.pages_fork(p.set, *state, *args, p.bs, fresh=fresh)
+        li.pages_grow(*state, args[1], 3, p.bs, slots=slots)
+        li.pages_compact(p.set, p.g_refs, p.g_table, place, live, workspace)
+    for step in range(4):
+        p.grow([0, 1, 2], 1)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        plain.free(p.refs, p.table, p.lens, children)
+        assert fresh.tolist() == plain.fork(p.caches, p.refs, p.table, p.lens, parents, children, p.bs)
+        assert slots.tolist() == plain.grow(p.refs, p.table, p.lens, children, 3, p.bs)
+        assert (place.tolist(), live.item()) == plain.compact(p.caches, p.refs, p.table)
+        p.same(step)
+
+
+def test_the_same_pages_every_time():
+    """What a call does depends on its state alone."""
+    p = Pool(800, 64, 30, 4, seed=13)
+    p.grow([0, 1, 2], 110, [110, 57, 84])
+    start = copy.deepcopy((p.refs, p.table, p.lens))
+    results = []
+    for _ in range(5):
+        p.refs, p.table, p.lens = copy.deepcopy(start)
+        p.put()
+        p.fork([i % 3 for i in range(50)], list(range(5, 55)))
+        p.grow(list(range(64)), 5)
+        results.append((p.g_refs.clone(), p.g_table.clone()))
+    assert all(torch.equal(a, b) for r in results[1:] for a, b in zip(r, results[0]))

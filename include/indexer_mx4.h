@@ -203,6 +203,49 @@ indexer_status indexer_mx4_attend_selected(const indexer_mx4_attend_args *args);
 indexer_status indexer_mx4_attend_window(const indexer_mx4_attend_args *args);
 
 /*
+ * indexer_mx4_attend_shared -- attention of requests to every key they see,
+ * where groups of requests begin with the same tokens: those keys are read
+ * once for the rows of all requests of a group.
+ *
+ * Requests group_starts[g] .. group_starts[g + 1] - 1 are group g, whose first
+ * prefix_lens[g] positions (taken as 0..max_prefix_len) have their pages in
+ * block_table's row group_starts[g], the group's first request's; the entries
+ * of other requests for pages that lie wholly inside the prefix are not read.
+ * Positions behind the prefix, also those that share its last page, have their
+ * pages in each request's own row.  With tables that name the same pages (as
+ * indexer_pages_fork leaves them) the result is that of
+ * indexer_mx4_attend_window with window 0, up to the order of the sums.
+ *
+ *   attend        the members of indexer_mx4_attend_args (those from idx to
+ *                 sinks are ignored); the workspace is that of
+ *                 indexer_mx4_attend_shared_workspace_bytes, never NULL
+ *   prefix_lens   i32 [n_groups]
+ *   group_starts  i32 [n_groups + 1], ascending, or NULL: one group of all
+ *                 requests.  Requests outside 0..n_requests are not there;
+ *                 requests before the first start or from the last one on
+ *                 share nothing.  Of starts that do not ascend, results are
+ *                 undefined (nothing outside the arguments is touched)
+ *   max_group     the most requests of a group, in 0..n_requests.  Rows of a
+ *                 group's requests past it have undefined results
+ *
+ * Limits and errors are those of the other attention calls, and
+ * n_groups * max_group * query_len * n_heads at most 2^31 - 1024.
+ */
+typedef struct {
+    indexer_mx4_attend_args attend;
+    const int32_t *prefix_lens;
+    const int32_t *group_starts;
+    int32_t n_groups, max_group, max_prefix_len;
+} indexer_mx4_shared_args;
+
+indexer_status indexer_mx4_attend_shared(const indexer_mx4_shared_args *args);
+
+/* Its workspace, from sizes alone; (size_t)-1 for sizes no call accepts. */
+size_t indexer_mx4_attend_shared_workspace_bytes(
+    int32_t n_requests, int32_t query_len, int32_t max_seq_len, int32_t n_groups, int32_t max_group,
+    int32_t max_prefix_len, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim);
+
+/*
  * Bytes of workspace an attention call needs (0 if none): the partial results
  * of rows whose keys are shared out over several workgroups.  max_keys is the
  * most keys a row can attend to: n_sel * pool_size for the selected form; for

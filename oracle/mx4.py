@@ -107,3 +107,21 @@ def attend_rows(q, rows_k, rows_v, block_table, seq_lens, query_len, max_seq_len
                 reach[t, h] = sm_scale * np.max(np.abs(k[:, h // g]) @ np.abs(q[t, h]))
                 top[t, h] = np.max(np.abs(z))
     return out, lse, {"spread": spread, "reach": reach, "top": top, "count": count, "plain": plain}
+
+
+def attend_shared(q, rows_k, rows_v, block_table, seq_lens, query_len, max_seq_len, sm_scale, starts, prefixes):
+    """Attention to every key a row sees, as attend_rows, where positions of a
+    group's prefix are those of its first request's pages: through a table of
+    single slots, put together for each request."""
+    n_blocks, bs, kv, d = rows_k.shape
+    requests, cols = block_table.shape
+    slots = np.full((requests, cols * bs), -1, dtype=np.int64)
+    for r in range(requests):
+        group = [g for g in range(len(prefixes)) if starts[g] <= r < starts[g + 1]]
+        first, prefix = (starts[group[0]], max(prefixes[group[0]], 0)) if group else (r, 0)
+        for p in range(cols * bs):
+            page = int(block_table[first if p < prefix else r, p // bs])
+            slots[r, p] = page * bs + p % bs if 0 <= page < n_blocks else -1
+    flat_k, flat_v = rows_k.reshape(-1, 1, kv, d), rows_v.reshape(-1, 1, kv, d)
+    return attend_rows(q, flat_k, flat_v, slots, seq_lens, query_len, max_seq_len, sm_scale,
+                       lambda t, v, seen: range(max(seen, 0)))

@@ -20,7 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libindexer.so")
 SOURCES = ["indexer_api.hip", "score_kernel.hip", "decode_kernel.hip", "topk_kernel.hip", "pool_kernel.hip", "stream_topk.hip",
-           "mx4_api.hip", "mx4_cache.hip", "mx4_attend_f16.hip", "mx4_attend_bf16.hip", "rope_api.hip", "rope_kernel.hip",
+           "mx4_api.hip", "mx4_cache.hip", "mx4_attend_f16.hip", "mx4_attend_bf16.hip", "mx4_shared_f16.hip", "mx4_shared_bf16.hip", "rope_api.hip", "rope_kernel.hip",
            "pages_api.hip", "pages_kernel.hip"]
 PROBE_SOURCES = ["peak_probe.hip"]
 PROBE_LIB = os.path.join(PKG, "libpeak_probe.so")

@@ -16,6 +16,7 @@ bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 static_assert(sizeof(indexer_mx4_write_args) == 18 * 8 + 6 * 4 && sizeof(indexer_mx4_read_args) == 13 * 8 + 6 * 4 &&
                   sizeof(indexer_mx4_attend_args) == 25 * 8 + 14 * 4,
               "members without padding: the binding packs them");
+static_assert(sizeof(indexer_mx4_shared_args) == sizeof(indexer_mx4_attend_args) + 2 * 8 + 4 * 4, "the binding packs the members");
 
 constexpr int32_t kMaxKeys = INT32_MAX - 1023;  // room for positions of a last, partly filled tile
 
@@ -333,7 +334,55 @@ Mx4Plan plan_mx4_attend(int n_requests, int q_len, int64_t max_keys, bool select
     return sized(p, rows, n_heads, n_kv, head_dim);
 }
 
+// The two parts are planned as attention of their own: groups as requests of
+// their most rows, and requests with the keys that the longest has behind the
+// longest prefix (others may have more; that is a matter of time alone).  Their
+// shares together are at most what the join takes.
+Mx4SharedPlan plan_mx4_shared(int n_requests, int q_len, int max_seq_len, int n_groups, int max_group, int max_prefix,
+                              int n_heads, int n_kv, int head_dim) {
+    Mx4SharedPlan p{};
+    const int64_t rows = (int64_t)n_requests * q_len;
+    p.own = plan_mx4_attend(n_requests, q_len, max_seq_len > max_prefix ? max_seq_len - max_prefix : 1, false, n_heads, n_kv,
+                            head_dim);
+    const bool prefix = n_groups > 0 && max_group > 0 && max_prefix > 0 && max_seq_len > 0;
+    if (prefix) {
+        p.prefix = plan_mx4_attend(n_groups, max_group * q_len, max_prefix < max_seq_len ? max_prefix : max_seq_len, false,
+                                   n_heads, n_kv, head_dim);
+        const int64_t prefix_rows = (int64_t)n_groups * max_group * q_len;
+        if (p.own.n_splits > kMx4MaxSplits / 2) {
+            p.own.n_splits = kMx4MaxSplits / 2;
+            p.own = sized(p.own, rows, n_heads, n_kv, head_dim);
+        }
+        if (p.prefix.n_splits > kMx4MaxSplits - p.own.n_splits) {
+            p.prefix.n_splits = kMx4MaxSplits - p.own.n_splits;
+            p.prefix = sized(p.prefix, prefix_rows, n_heads, n_kv, head_dim);
+        }
+    }
+    p.shares = p.prefix.n_splits + p.own.n_splits;
+    const size_t parts = (size_t)rows * n_heads * p.shares;
+    p.part_o_bytes = (parts * head_dim * 4 + 255) / 256 * 256;
+    p.workspace_bytes = p.part_o_bytes + (parts * 8 + 255) / 256 * 256;
+    p.fits = p.own.fits && (!prefix || p.prefix.fits) && one_launch(rows * n_heads, kMx4JoinThreads);
+    return p;
+}
+
 }  // namespace lidx
+
+namespace {
+
+// Sizes of the groups of requests that share a prefix.
+indexer_status check_groups(int32_t n_requests, int32_t n_groups, int32_t max_group, int32_t max_prefix, int32_t query_len,
+                            int32_t n_heads) {
+    if (n_groups < 0 || max_group < 0 || max_group > n_requests)
+        MX4_FAIL(INDEXER_EINVAL, "n_groups=%d must be >= 0 and max_group=%d in 0..n_requests=%d", n_groups, max_group,
+                 n_requests);
+    if (max_prefix < 0) MX4_FAIL(INDEXER_EINVAL, "max_prefix_len=%d must be >= 0", max_prefix);
+    if ((int64_t)n_groups * max_group > kMaxKeys / ((int64_t)query_len * n_heads))
+        MX4_FAIL(INDEXER_EINVAL, "n_groups*max_group*query_len*n_heads exceeds the int32 range (%d)", kMaxKeys);
+    return INDEXER_OK;
+}
+
+}  // namespace
 
 extern "C" {
 
@@ -438,6 +487,56 @@ indexer_status indexer_mx4_attend_window(const indexer_mx4_attend_args *args) {
     return run_attend(a, g, window_keys(g.max_seq_len, g.window, g.sinks));
 }
 
+indexer_status indexer_mx4_attend_shared(const indexer_mx4_shared_args *args) {
+    if (!args) MX4_FAIL(INDEXER_EINVAL, "args is NULL");
+    const indexer_mx4_shared_args &s = *args;
+    const indexer_mx4_attend_args &g = s.attend;
+    lidx::Mx4Attend a;
+    MX4_TRY(check_attend(g, &a));
+    MX4_TRY(check_groups(g.n_requests, s.n_groups, s.max_group, s.max_prefix_len, g.query_len, g.n_heads));
+    if (s.n_groups > 0) {
+        if (!s.prefix_lens) MX4_FAIL(INDEXER_EINVAL, "prefix_lens is NULL");
+        if (!s.group_starts && s.n_groups > 1) MX4_FAIL(INDEXER_EINVAL, "group_starts is NULL with n_groups=%d", s.n_groups);
+        if (!s.group_starts && s.max_group < g.n_requests)
+            MX4_FAIL(INDEXER_EINVAL, "max_group=%d is not all of n_requests=%d", s.max_group, g.n_requests);
+        if (!aligned(s.prefix_lens, 4) || !aligned(s.group_starts, 4))
+            MX4_FAIL(INDEXER_EINVAL, "prefix_lens and group_starts must be 4-byte aligned");
+    }
+    const lidx::Mx4SharedPlan p = lidx::plan_mx4_shared(g.n_requests, g.query_len, g.max_seq_len, s.n_groups, s.max_group,
+                                                        s.max_prefix_len, g.n_heads, g.n_kv_heads, g.head_dim);
+    if (!p.fits) MX4_FAIL(INDEXER_EINVAL, "problem too large for one launch");
+    if (a.rows > 0 && (!g.workspace || g.workspace_bytes < p.workspace_bytes || !aligned(g.workspace, 256)))
+        MX4_FAIL(INDEXER_EWORKSPACE, "attention needs %zu bytes of 256-byte aligned workspace, got %zu", p.workspace_bytes,
+                 g.workspace ? g.workspace_bytes : (size_t)0);
+    if (a.rows == 0) return done(hipSuccess, "");
+    a.prefix_lens = s.prefix_lens;
+    a.group_starts = s.group_starts;
+    a.n_groups = s.n_groups;
+    a.max_prefix = s.max_prefix_len;
+    a.shares = p.shares;
+    a.prefix_shares = p.prefix.n_splits;
+    a.div_q = lidx::fast_div((uint32_t)g.query_len);
+    a.part_o = (float *)g.workspace;
+    a.part_ml = (float *)((char *)g.workspace + p.part_o_bytes);
+    hipStream_t stream = (hipStream_t)g.stream;
+    return done(g.type == INDEXER_MX4_BF16 ? lidx::launch_mx4_shared_bf16(a, p, g.head_dim, stream)
+                                           : lidx::launch_mx4_shared_f16(a, p, g.head_dim, stream),
+                "shared attention kernel launch");
+}
+
+size_t indexer_mx4_attend_shared_workspace_bytes(int32_t n_requests, int32_t query_len, int32_t max_seq_len, int32_t n_groups,
+                                                 int32_t max_group, int32_t max_prefix_len, int32_t n_heads,
+                                                 int32_t n_kv_heads, int32_t head_dim) {
+    if (n_requests < 0 || query_len < 1 || max_seq_len < 0 || max_seq_len > kMaxKeys || n_heads < 1 ||
+        n_heads > lidx::kMaxHeads || n_kv_heads < 1 || n_heads % n_kv_heads || !attend_dim(head_dim) ||
+        (int64_t)n_requests * query_len > kMaxKeys / n_heads || n_groups < 0 || max_group < 0 || max_group > n_requests ||
+        max_prefix_len < 0 || (int64_t)n_groups * max_group > kMaxKeys / ((int64_t)query_len * n_heads))
+        return (size_t)-1;
+    const lidx::Mx4SharedPlan p = lidx::plan_mx4_shared(n_requests, query_len, max_seq_len, n_groups, max_group,
+                                                        max_prefix_len, n_heads, n_kv_heads, head_dim);
+    return p.fits ? p.workspace_bytes : (size_t)-1;
+}
+
 size_t indexer_mx4_attend_workspace_bytes(int32_t n_requests, int32_t query_len, int32_t max_keys, int32_t selected,
                                           int32_t n_heads, int32_t n_kv_heads, int32_t head_dim) {
     if (n_requests < 0 || query_len < 1 || max_keys < 0 || n_heads < 1 || n_heads > lidx::kMaxHeads ||
@@ -459,6 +558,17 @@ void lidx_mx4_attend_form(int32_t n_requests, int32_t query_len, int32_t max_key
         lidx::plan_mx4_attend(n_requests, query_len, max_keys, selected != 0, n_heads, n_kv_heads, head_dim);
     const int32_t fields[8] = {p.prompt, p.share, p.ahead, p.mt, p.hp, p.head_group, p.n_splits, p.threads};
     for (int i = 0; i < 8; ++i) form[i] = fields[i];
+}
+
+// The same of the two parts of a call for requests that share prefixes.
+void lidx_mx4_shared_form(const int32_t sizes[9], int32_t form[16]) {
+    const lidx::Mx4SharedPlan p = lidx::plan_mx4_shared(sizes[0], sizes[1], sizes[2], sizes[3], sizes[4], sizes[5], sizes[6],
+                                                        sizes[7], sizes[8]);
+    for (int part = 0; part < 2; ++part) {
+        const lidx::Mx4Plan &q = part ? p.own : p.prefix;
+        const int32_t fields[8] = {q.prompt, q.share, q.ahead, q.mt, q.hp, q.head_group, q.n_splits, q.threads};
+        for (int i = 0; i < 8; ++i) form[8 * part + i] = fields[i];
+    }
 }
 
 }  // extern "C"

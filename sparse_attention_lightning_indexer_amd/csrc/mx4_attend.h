@@ -242,8 +242,37 @@ __device__ __forceinline__ Item item_of(const Mx4Attend &a, int mt, int hp) {
 }
 
 // What a row attends to: a window (or everything), selected keys, selected
-// runs of `pool` keys.
-enum Mode { kWindow = 0, kKeys = 1, kPools = 2 };
+// runs of `pool` keys; of requests that share a prefix, their own keys behind
+// it, or the prefix's (a unit is then a group of requests).
+enum Mode { kWindow = 0, kKeys = 1, kPools = 2, kOwn = 3, kPrefix = 4 };
+
+// The requests of a group that share a prefix, and the prefix's length.
+struct Group {
+    int first, count, prefix;
+};
+__device__ __forceinline__ Group group_at(const Mx4Attend &a, int g) {
+    Group r{0, a.n_requests, min(max(a.prefix_lens[g], 0), a.max_prefix)};
+    if (a.group_starts) {
+        r.first = min(max(a.group_starts[g], 0), a.n_requests);
+        r.count = min(max(a.group_starts[g + 1], r.first), a.n_requests) - r.first;
+    }
+    return r;
+}
+// The group of a request, or -1: the last that begins at or before it, if it does not end before.
+__device__ __forceinline__ int group_of(const Mx4Attend &a, int request) {
+    if (!a.group_starts) return a.n_groups - 1;  // one group of all, or none
+    int lo = -1, hi = a.n_groups;  // group_starts[lo] <= request < group_starts[hi + 1] or beyond
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a.group_starts[mid] <= request) lo = mid;
+        else hi = mid;
+    }
+    return lo >= 0 && request < a.group_starts[lo + 1] ? lo : -1;
+}
+__device__ __forceinline__ int prefix_before(const Mx4Attend &a, int request) {
+    const int g = group_of(a, request);
+    return g < 0 ? 0 : min(max(a.prefix_lens[g], 0), a.max_prefix);
+}
 
 // Waves per SIMD the registers have to leave room for.  Three (168 registers) are
 // not quite enough for two K/V heads a wave at head dimension 128 with selected
@@ -263,12 +292,12 @@ template <bool BF16, int D, int MT, int HP, int PF, int MODE, bool SHARE>
 __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D, MT, HP, PF>())) mx4_attend_kernel(Mx4Attend a) {
     static_assert(HP == 1 || MT == 1, "pairs of heads have one tile of rows");
     static_assert(HP == 1 || PF == 1, "a pair's second 16 keys are asked for late");
-    static_assert(!SHARE || (HP == 2 && MODE != kWindow && (D == 64 || D == 128)), "shared scales: pairs of heads of selected rows");
+    static_assert(!SHARE || (HP == 2 && (MODE == kKeys || MODE == kPools) && (D == 64 || D == 128)), "shared scales: pairs of heads of selected rows");
     using T = Type<BF16>;
     using S = Shape<D, HP>;
     typedef typename T::vec8 vec8;
     constexpr int KS = S::KS, NT = S::NT, W = S::WAVES, NU = S::NU, KPL = S::KPL;
-    constexpr bool SELECTED = MODE != kWindow;
+    constexpr bool SELECTED = MODE == kKeys || MODE == kPools;
     __shared__ __attribute__((aligned(16))) unsigned char smem[S::LDS];
     // SHARE: the scales of a pair of tiles and of the one after, of all the
     // workgroup's heads: 16-byte parts of K's, then of V's, each for the 64 keys
@@ -288,24 +317,36 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
     const int hcol = HP == 2 ? col >> 3 : 0, mcol = HP == 2 ? col & 7 : col;
 
     // the unit's request, query rows and visible keys
-    const int req = SELECTED ? it.unit / a.q_len : it.unit;
+    Group group{};
+    if (MODE == kPrefix) group = group_at(a, it.unit);
+    if (MODE == kPrefix && it.m0 >= group.count * a.q_len * a.group) return;
+    const int req = SELECTED ? it.unit / a.q_len : (MODE == kPrefix ? group.first : it.unit);
     const int seq = a.seq_lens[req];
-    const int n_m = SELECTED ? a.group : a.q_len * a.group;  // query rows of the unit at this K/V head
+    // query rows of the unit at this K/V head
+    const int n_m = SELECTED ? a.group : (MODE == kPrefix ? group.count * a.q_len * a.group : a.q_len * a.group);
+    const int prefix = MODE == kOwn ? prefix_before(a, req) : group.prefix;
     auto token_of = [&](int m) { return SELECTED ? it.unit : req * a.q_len + (int)quotient((uint32_t)m, a.div_group); };
     auto head_in = [&](int kv, int m) {
         return kv * a.group + (SELECTED ? m : m - (int)quotient((uint32_t)m, a.div_group) * a.group);
     };
     // keys a token sees, before the cap by max_seq_len
-    auto seen_of = [&](int token) { return (int64_t)seq - a.q_len + 1 + (token - req * a.q_len); };
-    const int64_t first_seen = seen_of(token_of(it.m0));
-    const int64_t last_seen = seen_of(token_of(min(it.m0 + 16 * MT, n_m) - 1));
-    const int cap_first = (int)max((int64_t)0, min(first_seen, (int64_t)a.max_seq_len));
+    auto seen_of = [&](int token) -> int64_t {
+        if (MODE != kPrefix) return (int64_t)seq - a.q_len + 1 + (token - req * a.q_len);
+        const int r = (int)quotient((uint32_t)token, a.div_q);
+        return min((int64_t)a.seq_lens[r] - a.q_len + 1 + (token - r * a.q_len), (int64_t)prefix);
+    };
+    const int64_t first_seen = MODE == kPrefix ? 0 : seen_of(token_of(it.m0));
+    const int64_t last_seen = MODE == kPrefix ? prefix : seen_of(token_of(min(it.m0 + 16 * MT, n_m) - 1));
+    int cap_first = (int)max((int64_t)0, min(first_seen, (int64_t)a.max_seq_len));  // kPrefix: known below
     const int cap_last = (int)max((int64_t)0, min(last_seen, (int64_t)a.max_seq_len));
 
     // tiles of 32 keys: selected entries in order; or the first tokens, then the window
     int n_tiles, sink_tiles = 0, base = 0;
     if (SELECTED) {
         n_tiles = cap_last > 0 ? (int)(((int64_t)a.n_sel * a.pool + 31) / 32) : 0;
+    } else if (MODE >= kOwn) {
+        if (MODE == kOwn) base = min(prefix, cap_last) & ~31;
+        n_tiles = (cap_last - base + 31) / 32;
     } else {
         int64_t lo = a.window ? first_seen - a.window : 0;
         base = lo > 0 ? (int)min(lo, (int64_t)cap_last) & ~31 : 0;
@@ -338,11 +379,17 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
         const int64_t seen = seen_of(token);
         row_end[mt] = (int)max((int64_t)0, min(seen, (int64_t)a.max_seq_len));
         row_start[mt] = a.window ? (int)min(max((int64_t)0, seen - a.window), (int64_t)row_end[mt]) : 0;
+        if (MODE >= kOwn) row_start[mt] = MODE == kOwn ? prefix : 0;
         mx[mt] = kNegInf;
         ls[mt] = 0.0f;
         nan_blocks[mt] = 0u;
 #pragma unroll
         for (int n = 0; n < NT; ++n) o[mt][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    if (MODE == kPrefix) {
+        uint32_t least = (uint32_t)row_end[0];
+        if (MT == 2) least = min(least, (uint32_t)row_end[MT - 1]);
+        cap_first = (int)wave_min_u32(least);
     }
 
     // A tile's 32 keys are the rows of score tiles 0 and 1 (keys `row` and 16 +
@@ -513,7 +560,9 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
         const uint32_t valid = have[SET];
         const int p0 = SELECTED ? 0 : (tile < sink_tiles ? tile * 32 : base + (tile - sink_tiles) * 32);
         bool whole = valid == 0xffffffffu;
-        if (!SELECTED) {
+        if (MODE >= kOwn) {
+            whole = whole && p0 + 32 <= cap_first && (MODE == kPrefix || p0 >= prefix);
+        } else if (!SELECTED) {
             whole = whole && p0 + 32 <= cap_first &&
                     (!a.window || p0 + 32 <= a.sinks || (int64_t)p0 >= last_seen - a.window);
         }
@@ -833,13 +882,14 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
             }
             const int token = token_of(m), head = head_in(first_kv + hg * HP + (HP == 2 ? row >> 3 : 0), m);
             const int64_t th = (int64_t)token * a.n_heads + head;
-            if (a.n_splits > 1) {
-                float *dst2 = a.part_o + (th * a.n_splits + it.split) * D + c * 8;
+            if (MODE >= kOwn || a.n_splits > 1) {
+                const int64_t share = MODE >= kOwn ? th * a.shares + a.first_share + it.split : th * a.n_splits + it.split;
+                float *dst2 = a.part_o + share * D + c * 8;
                 *reinterpret_cast<f32x4 *>(dst2) = f32x4{acc[0], acc[1], acc[2], acc[3]};
                 *reinterpret_cast<f32x4 *>(dst2 + 4) = f32x4{acc[4], acc[5], acc[6], acc[7]};
                 if (c == 0) {
-                    a.part_ml[(th * a.n_splits + it.split) * 2] = m_all;
-                    a.part_ml[(th * a.n_splits + it.split) * 2 + 1] = l_all;
+                    a.part_ml[share * 2] = m_all;
+                    a.part_ml[share * 2 + 1] = l_all;
                 }
             } else {
                 const float inv = l_all == 0.0f ? 0.0f : 1.0f / l_all;
@@ -889,7 +939,7 @@ struct PromptShape {
     static constexpr int BUFFER = 2 * KEYS * ROW;  // K, then V
 };
 
-template <bool BF16, int D>
+template <bool BF16, int D, int MODE = kWindow>
 __global__ void __launch_bounds__(kMx4PromptThreads, 2) mx4_prompt_kernel(Mx4Attend a) {
     using T = Type<BF16>;
     using P = PromptShape<D>;
@@ -905,18 +955,27 @@ __global__ void __launch_bounds__(kMx4PromptThreads, 2) mx4_prompt_kernel(Mx4Att
     it.m0 = (a.m_tiles - 1) * P::ROWS - it.m0;  // the rows with the most keys first
     const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
     const int col = lane & 15, qd = lane >> 4;
-    const int req = it.unit, seq = a.seq_lens[req];
-    const int n_m = a.q_len * a.group;
-    auto token_in = [&](int m) { return (int)quotient((uint32_t)m, a.div_group); };  // of the request
-    auto seen_of = [&](int m) { return (int64_t)seq - a.q_len + 1 + token_in(min(m, n_m - 1)); };
+    Group group{};
+    if (MODE == kPrefix) group = group_at(a, it.unit);
+    const int req = MODE == kPrefix ? group.first : it.unit;
+    const int n_m = MODE == kPrefix ? group.count * a.q_len * a.group : a.q_len * a.group;
+    if (MODE == kPrefix && it.m0 >= n_m) return;
+    const int seq = a.seq_lens[req];
+    const int prefix = MODE == kOwn ? prefix_before(a, req) : group.prefix;
+    auto token_in = [&](int m) { return (int)quotient((uint32_t)m, a.div_group); };  // of the request, or its group
+    auto seen_of = [&](int m) -> int64_t {
+        if (MODE != kPrefix) return (int64_t)seq - a.q_len + 1 + token_in(min(m, n_m - 1));
+        const int t = token_in(min(m, n_m - 1)), r = (int)quotient((uint32_t)t, a.div_q);
+        return min((int64_t)a.seq_lens[req + r] - a.q_len + 1 + (t - r * a.q_len), (int64_t)prefix);
+    };
     auto capped = [&](int64_t v) { return (int)max((int64_t)0, min(v, (int64_t)a.max_seq_len)); };
 
     // the workgroup's keys: steps of 64, the first tokens and then the window
-    const int64_t first_seen = seen_of(it.m0);
-    const int cap_last = capped(seen_of(it.m0 + P::ROWS - 1));
-    const int64_t lo = a.window ? first_seen - a.window : 0;
+    const int64_t first_seen = MODE >= kOwn ? 0 : seen_of(it.m0);
+    const int cap_last = capped(MODE == kPrefix ? prefix : seen_of(it.m0 + P::ROWS - 1));
+    const int64_t lo = MODE >= kOwn ? (MODE == kOwn ? prefix : 0) : (a.window ? first_seen - a.window : 0);
     const int base = lo > 0 ? (int)min(lo, (int64_t)cap_last) & ~(KEYS - 1) : 0;
-    const int sink_steps = a.window ? (min(a.sinks, base) + KEYS - 1) / KEYS : 0;
+    const int sink_steps = MODE < kOwn && a.window ? (min(a.sinks, base) + KEYS - 1) / KEYS : 0;
     int n_steps = sink_steps + (cap_last - base + KEYS - 1) / KEYS;
     if (a.pages.n_blocks == 0) n_steps = 0;
     const int per = (n_steps + a.n_splits - 1) / a.n_splits;
@@ -925,9 +984,10 @@ __global__ void __launch_bounds__(kMx4PromptThreads, 2) mx4_prompt_kernel(Mx4Att
 
     // the wave's rows
     const int m0 = it.m0 + wave * 16 * MT;
-    const int cap_first_w = capped(seen_of(m0));
-    const int cap_last_w = m0 < n_m ? capped(seen_of(m0 + 16 * MT - 1)) : 0;
-    const int64_t first_w = seen_of(m0) - a.window, last_w = seen_of(m0 + 16 * MT - 1) - a.window;
+    int cap_first_w = MODE == kPrefix ? 0 : capped(seen_of(m0));  // kPrefix: known below
+    const int cap_last_w = m0 < n_m ? capped(MODE == kPrefix ? prefix : seen_of(m0 + 16 * MT - 1)) : 0;
+    const int64_t first_w = MODE >= kOwn ? 0 : seen_of(m0) - a.window;
+    const int64_t last_w = MODE >= kOwn ? 0 : seen_of(m0 + 16 * MT - 1) - a.window;
     vec8 q[MT][KS];
     int row_end[MT], row_start[MT];
     float mx[MT], ls[MT];
@@ -946,12 +1006,15 @@ __global__ void __launch_bounds__(kMx4PromptThreads, 2) mx4_prompt_kernel(Mx4Att
         const int64_t seen = seen_of(m);
         row_end[mt] = capped(seen);
         row_start[mt] = a.window ? (int)min(max((int64_t)0, seen - a.window), (int64_t)row_end[mt]) : 0;
+        if (MODE >= kOwn) row_start[mt] = MODE == kOwn ? prefix : 0;
         mx[mt] = kNegInf;
         ls[mt] = 0.0f;
         nan_blocks[mt] = 0u;
 #pragma unroll
         for (int n = 0; n < NT; ++n) o[mt][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
+
+    if (MODE == kPrefix) cap_first_w = (int)wave_min_u32((uint32_t)min(row_end[0], row_end[1]));
 
     // the thread's part of a step: quarter ch of one key's K (waves 0-3) or V
     const bool is_v = wave >= 4;
@@ -1049,12 +1112,13 @@ __global__ void __launch_bounds__(kMx4PromptThreads, 2) mx4_prompt_kernel(Mx4Att
         }
         const int p0 = start_of(step);
         // none of the wave's rows sees a key of this step
-        if (p0 >= cap_last_w || (a.window && p0 + KEYS <= first_w && p0 >= a.sinks)) continue;
+        if (p0 >= cap_last_w || (MODE < kOwn && a.window && p0 + KEYS <= first_w && p0 >= a.sinks)) continue;
         const lds_u8 *kb = (const lds_u8 *)smem + buf * P::BUFFER;
         const uint32_t odd = any[buf][0] | any[buf][1] | any[buf][2] | any[buf][3];
         const bool strange = uni((int)odd) != 0;
         const bool whole = !strange && p0 + KEYS <= cap_first_w &&
-                           (!a.window || p0 + KEYS <= a.sinks || (int64_t)p0 >= last_w);
+                           (MODE >= kOwn ? MODE == kPrefix || p0 >= prefix
+                                         : !a.window || p0 + KEYS <= a.sinks || (int64_t)p0 >= last_w);
         auto counts = [&](int mt, int k) -> bool {
             const int p = p0 + k;
             return p < row_end[mt] && (p >= row_start[mt] || p < a.sinks) && !(unusual[buf][k] >> 31);
@@ -1163,15 +1227,17 @@ __global__ void __launch_bounds__(kMx4PromptThreads, 2) mx4_prompt_kernel(Mx4Att
         if (m >= n_m) continue;
         const int t = token_in(m), token = req * a.q_len + t, head = it.kv * a.group + m - t * a.group;
         const int64_t th = (int64_t)token * a.n_heads + head;
-        const float inv = a.n_splits > 1 ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
+        const int64_t share = MODE >= kOwn ? th * a.shares + a.first_share + it.split : th * a.n_splits + it.split;
+        const bool partial = MODE >= kOwn || a.n_splits > 1;
+        const float inv = partial ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             f32x4 v = o[mt][n];
             if ((nan_blocks[mt] >> (n / 2)) & 1u) v = f32x4{NAN, NAN, NAN, NAN};
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] *= inv;
-            if (a.n_splits > 1) {
-                *reinterpret_cast<f32x4 *>(a.part_o + (th * a.n_splits + it.split) * D + n * 16 + qd * 4) = v;
+            if (partial) {
+                *reinterpret_cast<f32x4 *>(a.part_o + share * D + n * 16 + qd * 4) = v;
             } else {
                 typename T::one r[4];
 #pragma unroll
@@ -1183,9 +1249,9 @@ __global__ void __launch_bounds__(kMx4PromptThreads, 2) mx4_prompt_kernel(Mx4Att
             }
         }
         if (qd) continue;
-        if (a.n_splits > 1) {
-            a.part_ml[(th * a.n_splits + it.split) * 2] = mx[mt];
-            a.part_ml[(th * a.n_splits + it.split) * 2 + 1] = l;
+        if (partial) {
+            a.part_ml[share * 2] = mx[mt];
+            a.part_ml[share * 2 + 1] = l;
         } else if (a.lse) {
             a.lse[th] = l == 0.0f ? kNegInf : (mx[mt] + (log2f(l) - T::kLift)) * 0.69314718055994530942f;
         }
@@ -1197,7 +1263,7 @@ __global__ void __launch_bounds__(kMx4PromptThreads, 2) mx4_prompt_kernel(Mx4Att
 // the loads of a row's shares overlap, and add up through LDS.  Latency: 32
 // shares of 64 heads of 128 take 4.7 us, most of it the launch and two dependent
 // rounds of loads.
-template <bool BF16, int D>
+template <bool BF16, int D, bool SHARED = false>
 __global__ void __launch_bounds__(kMx4JoinThreads) mx4_join_kernel(Mx4Attend a) {
     using T = Type<BF16>;
     typedef typename T::vec8 vec8;
@@ -1206,11 +1272,18 @@ __global__ void __launch_bounds__(kMx4JoinThreads) mx4_join_kernel(Mx4Attend a) 
     static_assert(kMx4MaxSplits <= 64, "a lane per share");
     __shared__ __attribute__((aligned(16))) float part[G][D];
     const int64_t th = blockIdx.x;
+    // SHARED: the prefix's shares, of a row whose request has one, then its own keys'
+    int n_shares = a.n_splits, skip = 0;
+    if (SHARED) {
+        n_shares = a.shares;
+        const int64_t request = th / a.n_heads / a.q_len;
+        if (group_of(a, (int)request) < 0) skip = a.prefix_shares;
+    }
     const int c = threadIdx.x % C, g = threadIdx.x / C;
-    const float *po = a.part_o + th * a.n_splits * D + c * 4;
+    const float *po = a.part_o + th * n_shares * D + c * 4;
     if (threadIdx.x < 64) {
-        const float *ml = a.part_ml + th * a.n_splits * 2;
-        const bool has = (int)threadIdx.x < a.n_splits;
+        const float *ml = a.part_ml + th * n_shares * 2;
+        const bool has = (int)threadIdx.x < n_shares && (int)threadIdx.x >= skip;
         const float m = has ? ml[2 * threadIdx.x] : kNegInf;
         float l = has ? ml[2 * threadIdx.x + 1] : 0.0f;
         float m_all = m;
@@ -1228,7 +1301,7 @@ __global__ void __launch_bounds__(kMx4JoinThreads) mx4_join_kernel(Mx4Attend a) 
     f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
     if (g < G) {
 #pragma unroll 4
-        for (int s = g; s < a.n_splits; s += G) {
+        for (int s = skip + g; s < n_shares; s += G) {
             const f32x4 x = *reinterpret_cast<const f32x4 *>(po + (int64_t)s * D);
             const float f = weight[s];
 #pragma unroll
@@ -1288,6 +1361,70 @@ hipError_t launch_dim(const Mx4Attend &a, const Mx4Plan &p, hipStream_t stream) 
     }
     if (p.mt == 1) return launch_tiles<BF16, D, 1, 1, 1>(a, p, stream);
     return launch_tiles<BF16, D, 2, 1, 1>(a, p, stream);
+}
+
+// Requests that share a prefix: the keys of one of the two parts of a row.
+template <bool BF16, int D, int MODE>
+hipError_t launch_part(const Mx4Attend &a, const Mx4Plan &p, hipStream_t stream) {
+    const dim3 grid((unsigned)p.workgroups);
+    if constexpr (D <= 128) {
+        if (p.prompt) {
+            hipLaunchKernelGGL((mx4_prompt_kernel<BF16, D, MODE>), grid, dim3(kMx4PromptThreads), 0, stream, a);
+            return hipGetLastError();
+        }
+        if (p.hp == 2) {
+            hipLaunchKernelGGL((mx4_attend_kernel<BF16, D, 1, 2, 1, MODE, false>), grid, dim3(Shape<D, 2>::WAVES * 64), 0,
+                               stream, a);
+            return hipGetLastError();
+        }
+        if (p.ahead == 2) {
+            hipLaunchKernelGGL((mx4_attend_kernel<BF16, D, 1, 1, 2, MODE, false>), grid, dim3(Shape<D, 1>::WAVES * 64), 0,
+                               stream, a);
+            return hipGetLastError();
+        }
+    }
+    if (p.mt == 1)
+        hipLaunchKernelGGL((mx4_attend_kernel<BF16, D, 1, 1, 1, MODE, false>), grid, dim3(Shape<D, 1>::WAVES * 64), 0, stream, a);
+    else
+        hipLaunchKernelGGL((mx4_attend_kernel<BF16, D, 2, 1, 1, MODE, false>), grid, dim3(Shape<D, 1>::WAVES * 64), 0, stream, a);
+    return hipGetLastError();
+}
+
+// The launch fields of one part.
+inline Mx4Attend part_of(Mx4Attend a, const Mx4Plan &p, int first_share) {
+    a.units = p.units;
+    a.m_tiles = p.m_tiles;
+    a.n_splits = p.n_splits;
+    a.head_group = p.head_group;
+    a.div_kv = fast_div((uint32_t)(a.n_kv / (p.hp * p.head_group)));
+    a.div_items = fast_div((uint32_t)(p.m_tiles * p.n_splits));
+    a.first_share = first_share;
+    return a;
+}
+
+template <bool BF16, int D>
+hipError_t launch_shared_dim(const Mx4Attend &a, const Mx4SharedPlan &p, hipStream_t stream) {
+    if (a.prefix_shares) {
+        const hipError_t e = launch_part<BF16, D, kPrefix>(part_of(a, p.prefix, 0), p.prefix, stream);
+        if (e != hipSuccess) return e;
+    }
+    const hipError_t e = launch_part<BF16, D, kOwn>(part_of(a, p.own, a.prefix_shares), p.own, stream);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((mx4_join_kernel<BF16, D, true>), dim3((unsigned)(a.rows * a.n_heads)), dim3(kMx4JoinThreads), 0, stream,
+                       a);
+    return hipGetLastError();
+}
+
+template <bool BF16>
+hipError_t launch_shared(const Mx4Attend &a, const Mx4SharedPlan &p, int head_dim, hipStream_t stream) {
+    switch (head_dim) {
+        case 64: return launch_shared_dim<BF16, 64>(a, p, stream);
+        case 96: return launch_shared_dim<BF16, 96>(a, p, stream);
+        case 128: return launch_shared_dim<BF16, 128>(a, p, stream);
+        case 192: return launch_shared_dim<BF16, 192>(a, p, stream);
+        case 256: return launch_shared_dim<BF16, 256>(a, p, stream);
+        default: return hipErrorInvalidValue;
+    }
 }
 
 template <bool BF16>

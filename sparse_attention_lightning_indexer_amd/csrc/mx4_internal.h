@@ -96,6 +96,12 @@ struct Mx4Attend {
     int32_t head_group; // groups of hp K/V heads a workgroup's waves are shared out to
     float *part_o;      // [rows][n_heads][n_splits][head_dim]
     float *part_ml;     // [rows][n_heads][n_splits][2]
+    // requests that share prefixes: a row's partial results are shares of the
+    // prefix's keys, then of its request's own
+    const int32_t *prefix_lens, *group_starts;
+    int32_t n_groups, max_prefix;
+    int32_t shares, prefix_shares, first_share;
+    FastDiv div_q;
 };
 
 constexpr int kMx4MaxSplits = 64;
@@ -119,6 +125,19 @@ struct Mx4Plan {
 };
 Mx4Plan plan_mx4_attend(int n_requests, int q_len, int64_t max_keys, bool selected, int n_heads, int n_kv,
                         int head_dim);
+
+// Requests that share prefixes: the prefixes' keys for all rows of a group of
+// requests, each request's own keys, and a join of the two parts' shares.
+struct Mx4SharedPlan {
+    Mx4Plan prefix, own;
+    int shares;  // of a row, the prefix's first
+    size_t part_o_bytes, workspace_bytes;
+    bool fits;
+};
+Mx4SharedPlan plan_mx4_shared(int n_requests, int q_len, int max_seq_len, int n_groups, int max_group, int max_prefix,
+                              int n_heads, int n_kv, int head_dim);
+hipError_t launch_mx4_shared_f16(const Mx4Attend &a, const Mx4SharedPlan &p, int head_dim, hipStream_t stream);
+hipError_t launch_mx4_shared_bf16(const Mx4Attend &a, const Mx4SharedPlan &p, int head_dim, hipStream_t stream);
 hipError_t launch_mx4_attend_f16(const Mx4Attend &a, const Mx4Plan &p, int head_dim, hipStream_t stream);
 hipError_t launch_mx4_attend_bf16(const Mx4Attend &a, const Mx4Plan &p, int head_dim, hipStream_t stream);
 

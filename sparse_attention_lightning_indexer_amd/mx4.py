@@ -24,7 +24,8 @@ _pkg = sys.modules[__package__]
 
 MX4_EXPORTS = (
     "indexer_mx4_cache_write", "indexer_mx4_cache_read", "indexer_mx4_attend_selected",
-    "indexer_mx4_attend_window", "indexer_mx4_attend_workspace_bytes",
+    "indexer_mx4_attend_window", "indexer_mx4_attend_shared", "indexer_mx4_attend_workspace_bytes",
+    "indexer_mx4_attend_shared_workspace_bytes",
 )
 MX4_F16, MX4_BF16 = 0, 1
 MAX_KEYS = 2**31 - 1024
@@ -34,6 +35,7 @@ MAX_KEYS = 2**31 - 1024
 WRITE = struct.Struct("=18q6i")
 READ = struct.Struct("=13q6i")
 ATTEND = struct.Struct("=25q13if")
+SHARED = struct.Struct("=2q3i4x")      # what follows ATTEND's members
 
 _lib = None        # the library with these entry points' signatures declared
 _torch = None
@@ -45,11 +47,13 @@ def _library():
     if _lib is not None:
         return _lib
     lib = _pkg.load_library()
-    for name in MX4_EXPORTS[:4]:
+    for name in MX4_EXPORTS[:5]:
         f = getattr(lib, name)
         f.argtypes, f.restype = [ctypes.c_char_p], ctypes.c_int   # a packed argument structure
     lib.indexer_mx4_attend_workspace_bytes.argtypes = [ctypes.c_int32] * 7
     lib.indexer_mx4_attend_workspace_bytes.restype = ctypes.c_size_t
+    lib.indexer_mx4_attend_shared_workspace_bytes.argtypes = [ctypes.c_int32] * 9
+    lib.indexer_mx4_attend_shared_workspace_bytes.restype = ctypes.c_size_t
     if _torch is None:
         _torch = _pkg._torch()
         _types.update({_torch.float16: MX4_F16, _torch.bfloat16: MX4_BF16})
@@ -229,7 +233,7 @@ def mx4_attend_workspace_bytes(n_requests: int, query_len: int, max_keys: int, s
 
 
 def _attend(entry, q, k_data, k_scale, v_data, v_scale, block_table, seq_lens, query_len, max_seq_len, sm_scale,
-            selected, max_keys, form, out, lse, with_lse, workspace):
+            selected, max_keys, form, out, lse, with_lse, workspace, groups=None):
     torch = _torch
     dev = _gpu(q, "q")
     dtype = q.dtype
@@ -274,16 +278,21 @@ def _attend(entry, q, k_data, k_scale, v_data, v_scale, block_table, seq_lens, q
     if rows == 0:  # nothing to compute
         return out, lse
     if workspace is None:
-        need = _lib.indexer_mx4_attend_workspace_bytes(requests, query_len, max_keys, selected, heads, kv, d)
+        if groups is None:
+            need = _lib.indexer_mx4_attend_workspace_bytes(requests, query_len, max_keys, selected, heads, kv, d)
+        else:
+            need = _lib.indexer_mx4_attend_shared_workspace_bytes(requests, query_len, max_seq_len, *groups[2:], heads, kv,
+                                                                  d)
         if 0 < need < 2**63:  # sizes the library refuses have none: the call below names them
             workspace = q.new_empty(need, dtype=torch.uint8)
     blocks, size, *strides = pages
+    more = b"" if groups is None else _pack(SHARED, *groups)
     _call(dev, entry, _pack(
         ATTEND, q.data_ptr(), *q_strides, k_data.data_ptr(), k_scale.data_ptr(), v_data.data_ptr(),
         v_scale.data_ptr(), *strides, block_table.data_ptr(), bt_stride if bt_rows > 1 else bt_cols,
         seq_lens.data_ptr(), out.data_ptr(), *out_strides, 0 if lse is None else lse.data_ptr(),
         0 if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(), _stream(dev),
-        *form, kind, blocks, size, requests, query_len, max_seq_len, heads, kv, d, sm_scale))
+        *form, kind, blocks, size, requests, query_len, max_seq_len, heads, kv, d, sm_scale) + more)
     return out, lse
 
 
@@ -339,3 +348,58 @@ def mx4_attend_window(q, k_data, k_scale, v_data, v_scale, block_table, seq_lens
                    max_seq_len, sm_scale, 0, max(0, min(keys, 2**31 - 1)),
                    (0, 0, 0, 0, window, sinks), out, lse, with_lse,
                    workspace)
+
+
+def _groups(prefix_lens, max_prefix_len, group_starts, max_group, requests, dev):
+    """Checks the groups; their members of the argument structure."""
+    _need(prefix_lens, "prefix_lens", _torch.int32, dev, 1)
+    groups = prefix_lens.shape[0]
+    if groups > 1 and prefix_lens.stride(0) != 1:
+        raise ValueError("prefix_lens must be contiguous")
+    if group_starts is None:
+        if groups > 1:
+            raise ValueError("several groups need group_starts")
+        max_group, starts = requests, 0
+    else:
+        _need(group_starts, "group_starts", _torch.int32, dev, 1)
+        if group_starts.shape[0] != groups + 1 or group_starts.stride(0) != 1:
+            raise ValueError(f"group_starts must hold the groups' starts and the last one's end ({groups + 1}, "
+                             f"contiguous), got {group_starts.shape[0]}")
+        starts = group_starts.data_ptr()
+        if max_group is None:
+            max_group = requests
+    if not (0 <= max_prefix_len < 2**31 and 0 <= max_group <= requests):   # ctypes would take their low 32 bits
+        raise ValueError(f"max_prefix_len={max_prefix_len} or max_group={max_group} (of {requests} requests) out of range")
+    return prefix_lens.data_ptr(), starts, groups, max_group, max_prefix_len
+
+
+def mx4_attend_shared(q, k_data, k_scale, v_data, v_scale, block_table, seq_lens, query_len: int, max_seq_len: int,
+                      sm_scale: float, prefix_lens, max_prefix_len: int, group_starts=None, max_group=None, out=None,
+                      lse=None, with_lse: bool = True, workspace=None) -> Tuple:
+    """Attention of each query row to every key it sees, where groups of
+    requests begin with the same prefix: its keys are read once for a group.
+
+    Requests group_starts[g] to group_starts[g + 1] - 1 (i32 [n_groups + 1],
+    ascending; None: all are one group, of at most max_group each) share their
+    first prefix_lens[g] (i32 [n_groups], at most max_prefix_len) positions,
+    whose pages the group's first request's row of block_table names; later
+    positions are read through each request's own row, as pages_fork makes
+    them.  Other arguments and results as in mx4_attend_window without a
+    window."""
+    lib = _library()
+    if not isinstance(q, _torch.Tensor):
+        raise TypeError("q must be a torch.Tensor")
+    if not isinstance(seq_lens, _torch.Tensor) or seq_lens.dim() != 1:
+        raise ValueError("seq_lens must be a vector of lengths")
+    groups = _groups(prefix_lens, max_prefix_len, group_starts, max_group, seq_lens.shape[0], _gpu(q, "q"))
+    return _attend(lib.indexer_mx4_attend_shared, q, k_data, k_scale, v_data, v_scale, block_table, seq_lens, query_len,
+                   max_seq_len, sm_scale, 0, 0, (0, 0, 0, 0, 0, 0), out, lse, with_lse, workspace, groups)
+
+
+def mx4_attend_shared_workspace_bytes(n_requests: int, query_len: int, max_seq_len: int, n_groups: int, max_group: int,
+                                      max_prefix_len: int, n_heads: int, n_kv_heads: int, head_dim: int) -> int:
+    """Workspace of mx4_attend_shared."""
+    sizes = (n_requests, query_len, max_seq_len, n_groups, max_group, max_prefix_len, n_heads, n_kv_heads, head_dim)
+    if not all(-2**31 <= n < 2**31 for n in sizes):   # ctypes would take their low 32 bits
+        raise ValueError(f"sizes out of the 32-bit range: {sizes}")
+    return int(_library().indexer_mx4_attend_shared_workspace_bytes(*sizes))

@@ -218,7 +218,7 @@ indexer_status indexer_mx4_attend_window(const indexer_mx4_attend_args *args);
  *
  *   attend        the members of indexer_mx4_attend_args (those from idx to
  *                 sinks are ignored); the workspace is that of
- *                 indexer_mx4_attend_shared_workspace_bytes, never NULL
+ *                 indexer_mx4_attend_shared_workspace_bytes, NULL when that is 0
  *   prefix_lens   i32 [n_groups]
  *   group_starts  i32 [n_groups + 1], ascending, or NULL: one group of all
  *                 requests.  Requests outside 0..n_requests are not there;

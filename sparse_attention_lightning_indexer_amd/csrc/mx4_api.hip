@@ -334,10 +334,43 @@ Mx4Plan plan_mx4_attend(int n_requests, int q_len, int64_t max_keys, bool select
     return sized(p, rows, n_heads, n_kv, head_dim);
 }
 
-// The two parts are planned as attention of their own: groups as requests of
-// their most rows, and requests with the keys that the longest has behind the
-// longest prefix (others may have more; that is a matter of time alone).  Their
-// shares together are at most what the join takes.
+// The prefixes' part: rows of a group in tiles, keys in shares, each a
+// workgroup, at most one a compute unit where that can be (two results of a
+// row cost the traffic of both).  Many rows of a tile are taken 256 at a time
+// and together, few by waves of 32 rows of their own, whichever an estimate
+// has shorter (PREFIX_FIGURES)
+static Mx4Plan plan_prefix(int n_groups, int rows_of, int keys, int n_heads, int n_kv, int head_dim, int most_shares) {
+    constexpr int kCus = 256;
+    Mx4Plan p = plan_mx4_attend(n_groups, rows_of, keys, false, n_heads, n_kv, head_dim);
+    const int64_t rows = (int64_t)n_groups * rows_of, n_m = (int64_t)rows_of * (n_heads / n_kv);
+    if (p.n_splits > most_shares) p.n_splits = most_shares;
+    if (head_dim > 128 || n_m <= 32 || p.hp == 2) return sized(p, rows, n_heads, n_kv, head_dim);
+    const double part = (double)rows * n_heads * head_dim * 8 / 4.5e6, wide = head_dim / 128.0;
+    double best = HUGE_VAL;
+    Mx4Plan q{};
+    q.units = n_groups, q.mt = 2, q.hp = q.head_group = q.ahead = 1;
+    for (int prompt = 0; prompt < 2; ++prompt) {
+        const int64_t tiles = prompt ? (n_m + 255) / 256 : (n_m + 31) / 32, items = n_groups * tiles * n_kv;
+        const double fill = (double)n_m / (double)(tiles * 256);
+        const int steps = (keys + (prompt ? 63 : 255)) / (prompt ? 64 : 256);  // of a workgroup: 8 waves of 32 keys, or 64 keys
+        for (int s = 1; s <= most_shares && s <= steps; ++s) {
+            if (!one_launch((items + 7 * n_kv) * s, kMx4PromptThreads)) break;
+            const double rounds = (double)((items * s + kCus - 1) / kCus);
+            const double each = prompt ? 2.05 * (0.76 + 0.24 * fill) : 1.7;
+            const double t = 10.0 + rounds * (double)((steps + s - 1) / s) * each * wide + s * part;
+            if (t >= best) continue;
+            best = t;
+            q.prompt = prompt != 0;
+            q.n_splits = s;
+            q.m_tiles = (int)tiles;
+        }
+    }
+    return best < HUGE_VAL ? sized(q, rows, n_heads, n_kv, head_dim) : sized(p, rows, n_heads, n_kv, head_dim);
+}
+
+// Requests' own keys are planned as attention under the keys that the longest
+// has behind the longest prefix (others may have more; that is a matter of time
+// alone).  The shares together are at most what the join takes.
 Mx4SharedPlan plan_mx4_shared(int n_requests, int q_len, int max_seq_len, int n_groups, int max_group, int max_prefix,
                               int n_heads, int n_kv, int head_dim) {
     Mx4SharedPlan p{};
@@ -345,24 +378,20 @@ Mx4SharedPlan plan_mx4_shared(int n_requests, int q_len, int max_seq_len, int n_
     p.own = plan_mx4_attend(n_requests, q_len, max_seq_len > max_prefix ? max_seq_len - max_prefix : 1, false, n_heads, n_kv,
                             head_dim);
     const bool prefix = n_groups > 0 && max_group > 0 && max_prefix > 0 && max_seq_len > 0;
-    if (prefix) {
-        p.prefix = plan_mx4_attend(n_groups, max_group * q_len, max_prefix < max_seq_len ? max_prefix : max_seq_len, false,
-                                   n_heads, n_kv, head_dim);
-        const int64_t prefix_rows = (int64_t)n_groups * max_group * q_len;
-        if (p.own.n_splits > kMx4MaxSplits / 2) {
-            p.own.n_splits = kMx4MaxSplits / 2;
-            p.own = sized(p.own, rows, n_heads, n_kv, head_dim);
-        }
-        if (p.prefix.n_splits > kMx4MaxSplits - p.own.n_splits) {
-            p.prefix.n_splits = kMx4MaxSplits - p.own.n_splits;
-            p.prefix = sized(p.prefix, prefix_rows, n_heads, n_kv, head_dim);
-        }
+    if (prefix && p.own.n_splits > kMx4MaxSplits / 4) {
+        p.own.n_splits = kMx4MaxSplits / 4;
+        p.own = sized(p.own, rows, n_heads, n_kv, head_dim);
     }
-    p.shares = p.prefix.n_splits + p.own.n_splits;
+    p.finish = !p.own.prompt && p.own.n_splits == 1;
+    const int own_shares = p.finish ? 0 : p.own.n_splits;
+    if (prefix)
+        p.prefix = plan_prefix(n_groups, max_group * q_len, max_prefix < max_seq_len ? max_prefix : max_seq_len, n_heads, n_kv,
+                               head_dim, kMx4MaxSplits - p.own.n_splits);
+    p.shares = p.prefix.n_splits + own_shares;
     const size_t parts = (size_t)rows * n_heads * p.shares;
     p.part_o_bytes = (parts * head_dim * 4 + 255) / 256 * 256;
     p.workspace_bytes = p.part_o_bytes + (parts * 8 + 255) / 256 * 256;
-    p.fits = p.own.fits && (!prefix || p.prefix.fits) && one_launch(rows * n_heads, kMx4JoinThreads);
+    p.fits = p.own.fits && (!prefix || p.prefix.fits) && (p.finish || one_launch(rows * n_heads, kMx4JoinThreads));
     return p;
 }
 
@@ -505,7 +534,7 @@ indexer_status indexer_mx4_attend_shared(const indexer_mx4_shared_args *args) {
     const lidx::Mx4SharedPlan p = lidx::plan_mx4_shared(g.n_requests, g.query_len, g.max_seq_len, s.n_groups, s.max_group,
                                                         s.max_prefix_len, g.n_heads, g.n_kv_heads, g.head_dim);
     if (!p.fits) MX4_FAIL(INDEXER_EINVAL, "problem too large for one launch");
-    if (a.rows > 0 && (!g.workspace || g.workspace_bytes < p.workspace_bytes || !aligned(g.workspace, 256)))
+    if (p.workspace_bytes && (!g.workspace || g.workspace_bytes < p.workspace_bytes || !aligned(g.workspace, 256)))
         MX4_FAIL(INDEXER_EWORKSPACE, "attention needs %zu bytes of 256-byte aligned workspace, got %zu", p.workspace_bytes,
                  g.workspace ? g.workspace_bytes : (size_t)0);
     if (a.rows == 0) return done(hipSuccess, "");
@@ -515,6 +544,7 @@ indexer_status indexer_mx4_attend_shared(const indexer_mx4_shared_args *args) {
     a.max_prefix = s.max_prefix_len;
     a.shares = p.shares;
     a.prefix_shares = p.prefix.n_splits;
+    a.finish = p.finish;
     a.div_q = lidx::fast_div((uint32_t)g.query_len);
     a.part_o = (float *)g.workspace;
     a.part_ml = (float *)((char *)g.workspace + p.part_o_bytes);

@@ -844,6 +844,7 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
 
     // join the waves: each writes its product, m and l; every thread then adds
     // up a share of the outputs
+    const int ahead_shares = MODE == kOwn && a.finish && group_of(a, req) >= 0 ? a.prefix_shares : 0;
     float *jo = reinterpret_cast<float *>(smem);
     float *jml = reinterpret_cast<float *>(smem + (S::STAGE > S::JOIN ? S::STAGE : S::JOIN));
 #pragma unroll
@@ -871,6 +872,14 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
             const int step = a.head_group * 16;  // to the next wave of this head
             float m_all = kNegInf;
             for (int w = 0; w < stride; ++w) m_all = fmaxf(m_all, ml[w * step * 2]);
+            const int token = token_of(m), head = head_in(first_kv + hg * HP + (HP == 2 ? row >> 3 : 0), m);
+            const int64_t th = (int64_t)token * a.n_heads + head;
+            // kOwn with all of a request's own keys: the prefix's shares, computed before, come in here
+            const float *pml = a.part_ml + th * a.shares * 2, *po = a.part_o + th * a.shares * D + c * 8;
+            if (MODE == kOwn) {
+#pragma unroll 8
+                for (int s = 0; s < ahead_shares; ++s) m_all = fmaxf(m_all, pml[s * 2]);
+            }
             const float sub = m_all == kNegInf ? 0.0f : m_all;
             float l_all = 0.0f, acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
@@ -880,9 +889,18 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
 #pragma unroll
                 for (int i = 0; i < 8; ++i) acc[i] += f * src[w * step * S::OROW + i];
             }
-            const int token = token_of(m), head = head_in(first_kv + hg * HP + (HP == 2 ? row >> 3 : 0), m);
-            const int64_t th = (int64_t)token * a.n_heads + head;
-            if (MODE >= kOwn || a.n_splits > 1) {
+            if (MODE == kOwn) {
+#pragma unroll 4
+                for (int s = 0; s < ahead_shares; ++s) {
+                    const float f = __builtin_amdgcn_exp2f(pml[s * 2] - sub);
+                    l_all += f * pml[s * 2 + 1];
+                    const f32x4 x = *reinterpret_cast<const f32x4 *>(po + (int64_t)s * D);
+                    const f32x4 y = *reinterpret_cast<const f32x4 *>(po + (int64_t)s * D + 4);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[i] += f * x[i], acc[4 + i] += f * y[i];
+                }
+            }
+            if (MODE == kPrefix || (MODE == kOwn ? !a.finish : a.n_splits > 1)) {
                 const int64_t share = MODE >= kOwn ? th * a.shares + a.first_share + it.split : th * a.n_splits + it.split;
                 float *dst2 = a.part_o + share * D + c * 8;
                 *reinterpret_cast<f32x4 *>(dst2) = f32x4{acc[0], acc[1], acc[2], acc[3]};
@@ -1409,7 +1427,7 @@ hipError_t launch_shared_dim(const Mx4Attend &a, const Mx4SharedPlan &p, hipStre
         if (e != hipSuccess) return e;
     }
     const hipError_t e = launch_part<BF16, D, kOwn>(part_of(a, p.own, a.prefix_shares), p.own, stream);
-    if (e != hipSuccess) return e;
+    if (e != hipSuccess || a.finish) return e;
     hipLaunchKernelGGL((mx4_join_kernel<BF16, D, true>), dim3((unsigned)(a.rows * a.n_heads)), dim3(kMx4JoinThreads), 0, stream,
                        a);
     return hipGetLastError();

@@ -101,6 +101,7 @@ struct Mx4Attend {
     const int32_t *prefix_lens, *group_starts;
     int32_t n_groups, max_prefix;
     int32_t shares, prefix_shares, first_share;
+    bool finish;        // the launch of the own keys joins a row's shares and its own
     FastDiv div_q;
 };
 
@@ -127,10 +128,13 @@ Mx4Plan plan_mx4_attend(int n_requests, int q_len, int64_t max_keys, bool select
                         int head_dim);
 
 // Requests that share prefixes: the prefixes' keys for all rows of a group of
-// requests, each request's own keys, and a join of the two parts' shares.
+// requests, then each request's own keys, and a join of the two parts' shares,
+// by the second launch where it has all of a row's own keys in one workgroup,
+// else by a third.
 struct Mx4SharedPlan {
     Mx4Plan prefix, own;
-    int shares;  // of a row, the prefix's first
+    bool finish;
+    int shares;  // of a row, the prefix's first; without the own where they are joined at once
     size_t part_o_bytes, workspace_bytes;
     bool fits;
 };

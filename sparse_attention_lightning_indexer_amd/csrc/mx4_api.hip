@@ -339,7 +339,8 @@ Mx4Plan plan_mx4_attend(int n_requests, int q_len, int64_t max_keys, bool select
 // row cost the traffic of both).  Many rows of a tile are taken 256 at a time
 // and together, few by waves of 32 rows of their own, whichever an estimate
 // has shorter (PREFIX_FIGURES)
-static Mx4Plan plan_prefix(int n_groups, int rows_of, int keys, int n_heads, int n_kv, int head_dim, int most_shares) {
+static Mx4Plan plan_prefix(int n_groups, int rows_of, int64_t all_rows, int keys, int n_heads, int n_kv, int head_dim,
+                           int most_shares) {
     constexpr int kCus = 256;
     Mx4Plan p = plan_mx4_attend(n_groups, rows_of, keys, false, n_heads, n_kv, head_dim);
     const int64_t rows = (int64_t)n_groups * rows_of, n_m = (int64_t)rows_of * (n_heads / n_kv);
@@ -350,11 +351,14 @@ static Mx4Plan plan_prefix(int n_groups, int rows_of, int keys, int n_heads, int
     Mx4Plan q{};
     q.units = n_groups, q.mt = 2, q.hp = q.head_group = q.ahead = 1;
     for (int prompt = 0; prompt < 2; ++prompt) {
-        const int64_t tiles = prompt ? (n_m + 255) / 256 : (n_m + 31) / 32, items = n_groups * tiles * n_kv;
+        const int64_t rows_a = prompt ? 256 : 32, tiles = (n_m + rows_a - 1) / rows_a;
+        // tiles that there are: groups are smaller than the largest, if there are that few rows
+        const int64_t real = all_rows * (n_heads / n_kv) / rows_a + n_groups;
+        const int64_t items = (n_groups * tiles < real ? n_groups * tiles : real) * n_kv;
         const double fill = (double)n_m / (double)(tiles * 256);
         const int steps = (keys + (prompt ? 63 : 255)) / (prompt ? 64 : 256);  // of a workgroup: 8 waves of 32 keys, or 64 keys
         for (int s = 1; s <= most_shares && s <= steps; ++s) {
-            if (!one_launch((items + 7 * n_kv) * s, kMx4PromptThreads)) break;
+            if (!one_launch((n_groups * tiles + 7) * n_kv * s, kMx4PromptThreads)) break;
             const double rounds = (double)((items * s + kCus - 1) / kCus);
             const double each = prompt ? 2.05 * (0.76 + 0.24 * fill) : 1.7;
             const double t = 10.0 + rounds * (double)((steps + s - 1) / s) * each * wide + s * part;
@@ -385,7 +389,7 @@ Mx4SharedPlan plan_mx4_shared(int n_requests, int q_len, int max_seq_len, int n_
     p.finish = !p.own.prompt && p.own.n_splits == 1;
     const int own_shares = p.finish ? 0 : p.own.n_splits;
     if (prefix)
-        p.prefix = plan_prefix(n_groups, max_group * q_len, max_prefix < max_seq_len ? max_prefix : max_seq_len, n_heads, n_kv,
+        p.prefix = plan_prefix(n_groups, max_group * q_len, rows, max_prefix < max_seq_len ? max_prefix : max_seq_len, n_heads, n_kv,
                                head_dim, kMx4MaxSplits - p.own.n_splits);
     p.shares = p.prefix.n_splits + own_shares;
     const size_t parts = (size_t)rows * n_heads * p.shares;

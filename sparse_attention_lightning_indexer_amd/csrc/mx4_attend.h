@@ -386,6 +386,31 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
 #pragma unroll
         for (int n = 0; n < NT; ++n) o[mt][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
+    if (MODE == kOwn && a.finish && group_of(a, req) >= 0) {
+        // the prefix's shares of a row, computed before: the waves that take its keys begin with
+        // some of them each, instead of with nothing
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            const int mc = min(it.m0 + mt * 16 + mcol, n_m - 1);
+            const int64_t th = (int64_t)token_of(mc) * a.n_heads + head_in(it.kv + hcol, mc);
+            const float *ml = a.part_ml + th * a.shares * 2, *po = a.part_o + th * a.shares * D + qd * 4;
+            for (int s = turn; s < a.prefix_shares; s += stride) {
+                const float m = ml[s * 2], l = ml[s * 2 + 1];
+                f32x4 x[NT];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) x[n] = *reinterpret_cast<const f32x4 *>(po + (int64_t)s * D + n * 16);
+                const float top = fmaxf(mx[mt], m), sub = top == kNegInf ? 0.0f : top;
+                const float f = __builtin_amdgcn_exp2f(mx[mt] - sub), g = __builtin_amdgcn_exp2f(m - sub);
+                mx[mt] = top;
+                ls[mt] = ls[mt] * f + (qd == 0 ? l * g : 0.0f);  // the lanes' sums are added at the end
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[mt][n][i] = o[mt][n][i] * f + x[n][i] * g;
+            }
+            if (mx[mt] != kNegInf && fabsf(mx[mt]) < kFar) limit[mt] = mx[mt] + 8.0f;
+        }
+    }
     if (MODE == kPrefix) {
         uint32_t least = (uint32_t)row_end[0];
         if (MT == 2) least = min(least, (uint32_t)row_end[MT - 1]);
@@ -844,7 +869,6 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
 
     // join the waves: each writes its product, m and l; every thread then adds
     // up a share of the outputs
-    const int ahead_shares = MODE == kOwn && a.finish && group_of(a, req) >= 0 ? a.prefix_shares : 0;
     float *jo = reinterpret_cast<float *>(smem);
     float *jml = reinterpret_cast<float *>(smem + (S::STAGE > S::JOIN ? S::STAGE : S::JOIN));
 #pragma unroll
@@ -874,12 +898,6 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
             for (int w = 0; w < stride; ++w) m_all = fmaxf(m_all, ml[w * step * 2]);
             const int token = token_of(m), head = head_in(first_kv + hg * HP + (HP == 2 ? row >> 3 : 0), m);
             const int64_t th = (int64_t)token * a.n_heads + head;
-            // kOwn with all of a request's own keys: the prefix's shares, computed before, come in here
-            const float *pml = a.part_ml + th * a.shares * 2, *po = a.part_o + th * a.shares * D + c * 8;
-            if (MODE == kOwn) {
-#pragma unroll 8
-                for (int s = 0; s < ahead_shares; ++s) m_all = fmaxf(m_all, pml[s * 2]);
-            }
             const float sub = m_all == kNegInf ? 0.0f : m_all;
             float l_all = 0.0f, acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
@@ -888,17 +906,6 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
                 l_all += f * ml[w * step * 2 + 1];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) acc[i] += f * src[w * step * S::OROW + i];
-            }
-            if (MODE == kOwn) {
-#pragma unroll 4
-                for (int s = 0; s < ahead_shares; ++s) {
-                    const float f = __builtin_amdgcn_exp2f(pml[s * 2] - sub);
-                    l_all += f * pml[s * 2 + 1];
-                    const f32x4 x = *reinterpret_cast<const f32x4 *>(po + (int64_t)s * D);
-                    const f32x4 y = *reinterpret_cast<const f32x4 *>(po + (int64_t)s * D + 4);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[i] += f * x[i], acc[4 + i] += f * y[i];
-                }
             }
             if (MODE == kPrefix || (MODE == kOwn ? !a.finish : a.n_splits > 1)) {
                 const int64_t share = MODE >= kOwn ? th * a.shares + a.first_share + it.split : th * a.n_splits + it.split;

@@ -109,19 +109,21 @@ def attend_rows(q, rows_k, rows_v, block_table, seq_lens, query_len, max_seq_len
     return out, lse, {"spread": spread, "reach": reach, "top": top, "count": count, "plain": plain}
 
 
-def attend_shared(q, rows_k, rows_v, block_table, seq_lens, query_len, max_seq_len, sm_scale, starts, prefixes):
+def attend_shared(q, rows_k, rows_v, block_table, seq_lens, query_len, max_seq_len, sm_scale, starts, prefixes,
+                  rows=None):
     """Attention to every key a row sees, as attend_rows, where positions of a
     group's prefix are those of its first request's pages: through a table of
-    single slots, put together for each request."""
+    single slots, put together for each request.  rows: those computed."""
     n_blocks, bs, kv, d = rows_k.shape
     requests, cols = block_table.shape
+    at = np.arange(cols * bs)
     slots = np.full((requests, cols * bs), -1, dtype=np.int64)
     for r in range(requests):
         group = [g for g in range(len(prefixes)) if starts[g] <= r < starts[g + 1]]
         first, prefix = (starts[group[0]], max(prefixes[group[0]], 0)) if group else (r, 0)
-        for p in range(cols * bs):
-            page = int(block_table[first if p < prefix else r, p // bs])
-            slots[r, p] = page * bs + p % bs if 0 <= page < n_blocks else -1
+        page = np.where(at < prefix, block_table[first, at // bs], block_table[r, at // bs]).astype(np.int64)
+        slots[r] = np.where((page >= 0) & (page < n_blocks), page * bs + at % bs, -1)
     flat_k, flat_v = rows_k.reshape(-1, 1, kv, d), rows_v.reshape(-1, 1, kv, d)
+    wanted = set(range(len(q)) if rows is None else [int(t) for t in rows])
     return attend_rows(q, flat_k, flat_v, slots, seq_lens, query_len, max_seq_len, sm_scale,
-                       lambda t, v, seen: range(max(seen, 0)))
+                       lambda t, v, seen: range(max(seen, 0)) if t in wanted else ())

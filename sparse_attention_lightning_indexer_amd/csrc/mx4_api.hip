@@ -335,33 +335,39 @@ Mx4Plan plan_mx4_attend(int n_requests, int q_len, int64_t max_keys, bool select
 }
 
 // The prefixes' part: rows of a group in tiles, keys in shares, each a
-// workgroup, at most one a compute unit where that can be (two results of a
-// row cost the traffic of both).  Many rows of a tile are taken 256 at a time
-// and together, few by waves of 32 rows of their own, whichever an estimate
-// has shorter (PREFIX_FIGURES)
+// workgroup, about one a compute unit (a share of a row costs the traffic of a
+// result there and back, and a round of loads in the launch that joins it).
+// Tiles of 256 rows that go through the keys together or waves with 32 rows of
+// their own, whichever is shorter by estimate.  Measured, 64 query heads on 8
+// K/V heads of 128, the whole call with one own key each, together and apart, of
+// their best shares: 8 requests over 131072 keys 125 and 70 us, 16 128 and 116,
+// 32 160 and 213, 64 293 and 407; 32 over 8192 38 and 31, 64 over 8192 47 and 46,
+// 128 over 8192 64 and 73.
 static Mx4Plan plan_prefix(int n_groups, int rows_of, int64_t all_rows, int keys, int n_heads, int n_kv, int head_dim,
                            int most_shares) {
     constexpr int kCus = 256;
     Mx4Plan p = plan_mx4_attend(n_groups, rows_of, keys, false, n_heads, n_kv, head_dim);
     const int64_t rows = (int64_t)n_groups * rows_of, n_m = (int64_t)rows_of * (n_heads / n_kv);
     if (p.n_splits > most_shares) p.n_splits = most_shares;
-    if (head_dim > 128 || n_m <= 32 || p.hp == 2) return sized(p, rows, n_heads, n_kv, head_dim);
-    const double part = (double)rows * n_heads * head_dim * 8 / 4.5e6, wide = head_dim / 128.0;
+    if (n_m <= 16 || p.hp == 2) return sized(p, rows, n_heads, n_kv, head_dim);
+    const int waves = mx4_wave_threads(head_dim, 1) / 64;
+    const double wide = head_dim / 128.0, part = (double)all_rows * n_heads * head_dim * 8 / 4.5e6;
     double best = HUGE_VAL;
     Mx4Plan q{};
     q.units = n_groups, q.mt = 2, q.hp = q.head_group = q.ahead = 1;
-    for (int prompt = 0; prompt < 2; ++prompt) {
+    for (int prompt = 0; prompt < (head_dim <= 128 ? 2 : 1); ++prompt) {
         const int64_t rows_a = prompt ? 256 : 32, tiles = (n_m + rows_a - 1) / rows_a;
         // tiles that there are: groups are smaller than the largest, if there are that few rows
         const int64_t real = all_rows * (n_heads / n_kv) / rows_a + n_groups;
         const int64_t items = (n_groups * tiles < real ? n_groups * tiles : real) * n_kv;
         const double fill = (double)n_m / (double)(tiles * 256);
-        const int steps = (keys + (prompt ? 63 : 255)) / (prompt ? 64 : 256);  // of a workgroup: 8 waves of 32 keys, or 64 keys
+        const int step = prompt ? 64 : 32 * waves, steps = (keys + step - 1) / step;  // of a workgroup
         for (int s = 1; s <= most_shares && s <= steps; ++s) {
             if (!one_launch((n_groups * tiles + 7) * n_kv * s, kMx4PromptThreads)) break;
             const double rounds = (double)((items * s + kCus - 1) / kCus);
             const double each = prompt ? 2.05 * (0.76 + 0.24 * fill) : 1.7;
-            const double t = 10.0 + rounds * (double)((steps + s - 1) / s) * each * wide + s * part;
+            const double t = 10.0 + rounds * (double)((steps + s - 1) / s) * each * wide + s * part +
+                             (double)((s + waves - 1) / waves) * 0.8 * wide;
             if (t >= best) continue;
             best = t;
             q.prompt = prompt != 0;
@@ -372,30 +378,97 @@ static Mx4Plan plan_prefix(int n_groups, int rows_of, int64_t all_rows, int keys
     return best < HUGE_VAL ? sized(q, rows, n_heads, n_kv, head_dim) : sized(p, rows, n_heads, n_kv, head_dim);
 }
 
+// About how long attention of `units` units of n_m rows to `keys` keys takes in
+// a form, in us: the launch and its first loads, then the rate of the vector
+// and matrix units or, with few tiles, the chain of a wave's tiles; and the
+// join of shares, unless another launch does it.
+static double estimate(const Mx4Plan &p, int64_t units, int64_t rows, int64_t n_m, int64_t keys, int n_heads, int n_kv,
+                       int head_dim, bool join) {
+    constexpr int kCus = 256;
+    const double wide = head_dim / 128.0;
+    double t;
+    if (p.prompt) {
+        const int64_t tiles = (n_m + 255) / 256;
+        const double fill = (double)n_m / (double)(tiles * 256);
+        t = 10.0 + (double)((units * tiles * n_kv * p.n_splits + kCus - 1) / kCus) *
+                       ceil((double)((keys + 63) / 64) / p.n_splits) * 2.05 * (0.76 + 0.24 * fill) * wide;
+    } else {
+        const int64_t waves = mx4_wave_threads(head_dim, p.hp) / 64 / p.head_group * p.n_splits;
+        const double tiles = (double)units * (double)((n_m + 16 * p.mt - 1) / (16 * p.mt)) * (n_kv / p.hp) *
+                             (double)((keys + 31) / 32);
+        const double rate = tiles / (4 * kCus) * (p.hp == 2 ? 1.4 : p.mt == 1 ? 0.68 : 0.85);
+        const double chain = (double)((keys + 32 * waves - 1) / (32 * waves)) * (p.hp == 2 || p.mt == 2 ? 1.7 : 0.95);
+        t = 7.0 + (rate > chain ? rate : chain) * wide;
+    }
+    if (join && p.n_splits > 1) t += 4.5 + (double)rows * n_heads * (1.2e-3 + p.n_splits * head_dim * 8 / 4.5e6);
+    return t;
+}
+
+// A request's keys by one workgroup after all, where sharing them out is not
+// worth the join.
+static Mx4Plan unless_joined(const Mx4Plan &p, int64_t units, int64_t rows, int64_t n_m, int64_t keys, int n_heads, int n_kv,
+                             int head_dim) {
+    if (p.n_splits == 1 || p.prompt) return p;
+    Mx4Plan q = p;
+    q.n_splits = q.ahead = 1;
+    q = sized(q, rows, n_heads, n_kv, head_dim);
+    return estimate(q, units, rows, n_m, keys, n_heads, n_kv, head_dim, true) <
+                   estimate(p, units, rows, n_m, keys, n_heads, n_kv, head_dim, true)
+               ? q
+               : p;
+}
+
 // Requests' own keys are planned as attention under the keys that the longest
 // has behind the longest prefix (others may have more; that is a matter of time
 // alone).  The shares together are at most what the join takes.
+//
+// A short prefix, few requests, or requests of many rows (whose tiles a group
+// does not fill better) are not worth the launch of the prefix's part: then
+// each request reads the prefix's keys itself.  Measured with and without, 64
+// query heads on 8 K/V heads of 128, 32 own keys: 2 requests over 16384 shared
+// keys 21.0 and 16.1 us, 8 over 2048 18.1 and 13.4, over 16384 25.5 and 33.5, 32
+// over 1024 18.9 and 13.0, over 4096 23.9 and 29.7, over 16384 44 and 94, 128
+// over 512 22.6 and 20.8, over 4096 46 and 98.
 Mx4SharedPlan plan_mx4_shared(int n_requests, int q_len, int max_seq_len, int n_groups, int max_group, int max_prefix,
                               int n_heads, int n_kv, int head_dim) {
     Mx4SharedPlan p{};
-    const int64_t rows = (int64_t)n_requests * q_len;
-    p.own = plan_mx4_attend(n_requests, q_len, max_seq_len > max_prefix ? max_seq_len - max_prefix : 1, false, n_heads, n_kv,
-                            head_dim);
-    const bool prefix = n_groups > 0 && max_group > 0 && max_prefix > 0 && max_seq_len > 0;
-    if (prefix && p.own.n_splits > kMx4MaxSplits / 4) {
-        p.own.n_splits = kMx4MaxSplits / 4;
-        p.own = sized(p.own, rows, n_heads, n_kv, head_dim);
+    const int64_t rows = (int64_t)n_requests * q_len, n_m = (int64_t)q_len * (n_heads / n_kv);
+    auto alone = [&](int keys) {
+        return unless_joined(plan_mx4_attend(n_requests, q_len, keys, false, n_heads, n_kv, head_dim), n_requests, rows, n_m,
+                             keys, n_heads, n_kv, head_dim);
+    };
+    const int own_keys = max_seq_len > max_prefix ? max_seq_len - max_prefix : 1;
+    const int prefix_keys = max_prefix < max_seq_len ? max_prefix : max_seq_len;
+    p.own = alone(own_keys);
+    if (n_groups > 0 && max_group > 0 && prefix_keys > 0) {
+        if (p.own.n_splits > kMx4MaxSplits / 4) {
+            p.own.n_splits = kMx4MaxSplits / 4;
+            p.own = sized(p.own, rows, n_heads, n_kv, head_dim);
+        }
+        p.prefix = plan_prefix(n_groups, max_group * q_len, rows, prefix_keys, n_heads, n_kv, head_dim,
+                               kMx4MaxSplits - p.own.n_splits);
+        const int64_t group_rows = n_m * ((n_requests + n_groups - 1) / n_groups);
+        const bool joined = !p.own.prompt && p.own.n_splits == 1;
+        const double apart =
+            estimate(p.prefix, n_groups, rows, group_rows, prefix_keys, n_heads, n_kv, head_dim, false) +
+            (double)rows * n_heads * p.prefix.n_splits * head_dim * 8 / 4.5e6 +
+            ceil(p.prefix.n_splits * 64.0 / mx4_wave_threads(head_dim, 1)) * 0.8 * head_dim / 128 +
+            estimate(p.own, n_requests, rows, n_m, own_keys, n_heads, n_kv, head_dim, true) +
+            (joined || p.own.n_splits > 1 ? 0.0 : 4.5 + (double)rows * n_heads * 1.2e-3);
+        const Mx4Plan all = alone(max_seq_len);
+        p.whole = all.fits && estimate(all, n_requests, rows, n_m, max_seq_len, n_heads, n_kv, head_dim, true) < apart;
+        if (p.whole) {
+            p.own = all;
+            p.prefix = Mx4Plan{};
+        }
     }
     p.finish = !p.own.prompt && p.own.n_splits == 1;
     const int own_shares = p.finish ? 0 : p.own.n_splits;
-    if (prefix)
-        p.prefix = plan_prefix(n_groups, max_group * q_len, rows, max_prefix < max_seq_len ? max_prefix : max_seq_len, n_heads, n_kv,
-                               head_dim, kMx4MaxSplits - p.own.n_splits);
     p.shares = p.prefix.n_splits + own_shares;
     const size_t parts = (size_t)rows * n_heads * p.shares;
     p.part_o_bytes = (parts * head_dim * 4 + 255) / 256 * 256;
     p.workspace_bytes = p.part_o_bytes + (parts * 8 + 255) / 256 * 256;
-    p.fits = p.own.fits && (!prefix || p.prefix.fits) && (p.finish || one_launch(rows * n_heads, kMx4JoinThreads));
+    p.fits = p.own.fits && (!p.prefix.n_splits || p.prefix.fits) && (p.finish || one_launch(rows * n_heads, kMx4JoinThreads));
     return p;
 }
 
@@ -548,6 +621,7 @@ indexer_status indexer_mx4_attend_shared(const indexer_mx4_shared_args *args) {
     a.max_prefix = s.max_prefix_len;
     a.shares = p.shares;
     a.prefix_shares = p.prefix.n_splits;
+    a.whole = p.whole;
     a.finish = p.finish;
     a.div_q = lidx::fast_div((uint32_t)g.query_len);
     a.part_o = (float *)g.workspace;

@@ -50,11 +50,10 @@
 // Measured, 64 query heads on 8 K/V heads of 128: one row over 131072 keys 31 us
 // (bf16, 4.6 TB/s: memory); 128 rows x 2048 keys of 32 requests 64 us (bf16, 4.5
 // TB/s in gathered rows); 32 rows under a window of 1024 13.3 us and 32 rows x 512
-// keys 9.5 us (f16: the latency of dependent loads and few tiles a wave).  In the
-// code as compiled the scale bytes of the next tile are widened at the end of a
-// tile (of a pair of them where two are on the way), which waits for all loads on
-// the way, and the first product waits for the indices and page ids of a second
-// pair of tiles, which rows of two tiles a wave do not have.
+// keys 9.5 us (f16: the latency of dependent loads and few tiles a wave).  What is
+// loaded ahead is used as loaded, in a later tile (scale bytes as bytes), and q is
+// known to have arrived before the loop: a value widened at once, or first used
+// in the loop, has the compiler wait there for every load on the way.
 //
 // Masked positions: their scores become -inf by selection, so K's NaN there
 // never spreads; V's blocks of NaN are replaced by zeros in the product, and
@@ -258,20 +257,28 @@ __device__ __forceinline__ Group group_at(const Mx4Attend &a, int g) {
     }
     return r;
 }
-// The group of a request, or -1: the last that begins at or before it, if it does not end before.
-__device__ __forceinline__ int group_of(const Mx4Attend &a, int request) {
-    if (!a.group_starts) return a.n_groups - 1;  // one group of all, or none
-    int lo = -1, hi = a.n_groups;  // group_starts[lo] <= request < group_starts[hi + 1] or beyond
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a.group_starts[mid] <= request) lo = mid;
-        else hi = mid;
+// The group of a request: the last that begins at or before it; of no request
+// and no prefix if there is none or it ends before.  Lanes look at a start
+// each, with the length and the end that may be wanted, so this is one round
+// trip to memory.  All lanes are active.
+__device__ __forceinline__ Group group_of(const Mx4Attend &a, int request) {
+    if (!a.group_starts) return a.n_groups ? group_at(a, 0) : Group{request, 0, 0};
+    Group r{request, 0, 0};
+    const int lane = threadIdx.x & 63;
+    for (int base = 0; base < a.n_groups; base += 64) {
+        const int g = min(base + lane, a.n_groups - 1);
+        const int start = a.group_starts[g], end = a.group_starts[g + 1], prefix = a.prefix_lens[g];
+        const int upto = __popcll(__ballot(base + lane < a.n_groups && start <= request));
+        if (upto) {
+            r.first = max(__builtin_amdgcn_readlane(start, upto - 1), 0);
+            r.count = min(__builtin_amdgcn_readlane(end, upto - 1), a.n_requests) - r.first;
+            r.prefix = min(max(__builtin_amdgcn_readlane(prefix, upto - 1), 0), a.max_prefix);
+        }
+        if (upto < 64) break;
     }
-    return lo >= 0 && request < a.group_starts[lo + 1] ? lo : -1;
-}
-__device__ __forceinline__ int prefix_before(const Mx4Attend &a, int request) {
-    const int g = group_of(a, request);
-    return g < 0 ? 0 : min(max(a.prefix_lens[g], 0), a.max_prefix);
+    // (of starts that do not ascend the first one may lie past the request)
+    if (r.count <= 0 || request < r.first || request - r.first >= r.count) r = Group{request, 0, 0};
+    return r;
 }
 
 // Waves per SIMD the registers have to leave room for.  Three (168 registers) are
@@ -324,7 +331,9 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
     const int seq = a.seq_lens[req];
     // query rows of the unit at this K/V head
     const int n_m = SELECTED ? a.group : (MODE == kPrefix ? group.count * a.q_len * a.group : a.q_len * a.group);
-    const int prefix = MODE == kOwn ? prefix_before(a, req) : group.prefix;
+    if (MODE == kOwn) group = group_of(a, req);
+    const int prefix = group.prefix;
+    const int own_from = MODE == kOwn && !a.whole ? prefix : 0;  // where the row's keys begin
     auto token_of = [&](int m) { return SELECTED ? it.unit : req * a.q_len + (int)quotient((uint32_t)m, a.div_group); };
     auto head_in = [&](int kv, int m) {
         return kv * a.group + (SELECTED ? m : m - (int)quotient((uint32_t)m, a.div_group) * a.group);
@@ -345,7 +354,7 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
     if (SELECTED) {
         n_tiles = cap_last > 0 ? (int)(((int64_t)a.n_sel * a.pool + 31) / 32) : 0;
     } else if (MODE >= kOwn) {
-        if (MODE == kOwn) base = min(prefix, cap_last) & ~31;
+        if (MODE == kOwn) base = min(own_from, cap_last) & ~31;
         n_tiles = (cap_last - base + 31) / 32;
     } else {
         int64_t lo = a.window ? first_seen - a.window : 0;
@@ -379,14 +388,14 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
         const int64_t seen = seen_of(token);
         row_end[mt] = (int)max((int64_t)0, min(seen, (int64_t)a.max_seq_len));
         row_start[mt] = a.window ? (int)min(max((int64_t)0, seen - a.window), (int64_t)row_end[mt]) : 0;
-        if (MODE >= kOwn) row_start[mt] = MODE == kOwn ? prefix : 0;
+        if (MODE >= kOwn) row_start[mt] = own_from;
         mx[mt] = kNegInf;
         ls[mt] = 0.0f;
         nan_blocks[mt] = 0u;
 #pragma unroll
         for (int n = 0; n < NT; ++n) o[mt][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    if (MODE == kOwn && a.finish && group_of(a, req) >= 0) {
+    if (MODE == kOwn && a.finish && group.count) {
         // the prefix's shares of a row, computed before: the waves that take its keys begin with
         // some of them each, instead of with nothing
 #pragma unroll
@@ -459,7 +468,11 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
         return mine < (uint32_t)t_end && p < (uint32_t)cap_last ? (int)p : -1;
     };
     // 3: its page's id
-    auto load_page = [&](int p) -> int { return table[quotient((uint32_t)max(p, 0), a.pages.div_bs)]; };
+    const int32_t *shared_table = a.block_table + (int64_t)group.first * a.bt_stride;
+    auto load_page = [&](int p) -> int {
+        if (MODE == kOwn) return (p < prefix ? shared_table : table)[quotient((uint32_t)max(p, 0), a.pages.div_bs)];
+        return table[quotient((uint32_t)max(p, 0), a.pages.div_bs)];
+    };
     // 4: where its row begins, in data and (unless that is a sixteenth of it) scale bytes
     uint64_t at = 0, sat = 0, found = 0;
     auto locate = [&](int p, int page) {
@@ -484,7 +497,7 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
     constexpr int ALIGN = KS % 4 == 0 ? 16 : (KS % 2 == 0 ? 8 : 4);
     struct Raw {
         uint32_t k[KS], v[KS];
-        uint32_t sk[NB], sv[NB];
+        uint8_t sk[NB], sv[NB];  // bytes until they are used: widening them at once would wait for them there
     };
     const int blk0 = ch * KS / 4;
     const uint64_t chunk = (uint64_t)((uint32_t)hsel * (uint32_t)a.pages.d_sh) + (uint32_t)(ch * KS * 4);
@@ -549,10 +562,17 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
     };
 
     int id = -1, pos = -1, page = -1;
-    if (t_begin < t_end) {
+    const bool any_tile = t_begin < t_end;
+    if (any_tile) {
         if (SELECTED) id = load_index(t_begin);
         pos = position(t_begin, id);
         page = load_page(pos);
+    }
+    // q, asked for before, has arrived when the first page's id has.  Said here,
+    // else its first use, which is in the loop, waits there for all loads on the
+    // way in every tile
+    wait_vmem_all_known();
+    if (any_tile) {
         locate(pos, page);
         if (SHARE) load_part();
 #pragma unroll
@@ -586,7 +606,7 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
         const int p0 = SELECTED ? 0 : (tile < sink_tiles ? tile * 32 : base + (tile - sink_tiles) * 32);
         bool whole = valid == 0xffffffffu;
         if (MODE >= kOwn) {
-            whole = whole && p0 + 32 <= cap_first && (MODE == kPrefix || p0 >= prefix);
+            whole = whole && p0 + 32 <= cap_first && p0 >= own_from;
         } else if (!SELECTED) {
             whole = whole && p0 + 32 <= cap_first &&
                     (!a.window || p0 + 32 <= a.sinks || (int64_t)p0 >= last_seen - a.window);
@@ -601,10 +621,15 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
             return in;
         };
 
+        uint32_t sv[NU][NB];
+#pragma unroll
+        for (int u = 0; u < NU; ++u)
+#pragma unroll
+            for (int n = 0; n < NB; ++n) sv[u][n] = SHARE ? 0u : raw_[u].sv[n];
         if (SHARE) {
 #pragma unroll
             for (int u = 0; u < NU; ++u)
-                raw_[u].sv[0] = shared_scale(buffer, 1, b * 32 + u * KPL + krow, it.kv - first_kv + hsel, blk0);
+                sv[u][0] = shared_scale(buffer, 1, b * 32 + u * KPL + krow, it.kv - first_kv + hsel, blk0);
         }
         // V's scales: 0 for keys that do not count; rarely, 0 for blocks of NaN,
         // with a mark for the rows that do attend to such a block, and at most
@@ -613,13 +638,13 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
 #pragma unroll
         for (int u = 0; u < NU; ++u)
 #pragma unroll
-            for (int n = 0; n < NB; ++n) bad |= raw_[u].sv[n] > T::kTopScale;
+            for (int n = 0; n < NB; ++n) bad |= sv[u][n] > T::kTopScale;
         if (valid != 0xffffffffu) {
 #pragma unroll
             for (int u = 0; u < NU; ++u) {
                 const bool in = (valid >> (u * KPL + krow)) & 1u;
 #pragma unroll
-                for (int n = 0; n < NB; ++n) raw_[u].sv[n] = in ? raw_[u].sv[n] : 0u;
+                for (int n = 0; n < NB; ++n) sv[u][n] = in ? sv[u][n] : 0u;
             }
         }
         if (__ballot(bad)) {
@@ -628,16 +653,16 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
                 uint32_t mine = 0;  // blocks of NaN in this lane's part of its key
 #pragma unroll
                 for (int n = 0; n < NB; ++n) {
-                    if (raw_[u].sv[n] == 255u) {
+                    if (sv[u][n] == 255u) {
                         mine |= 1u << min(blk0 + n, D / 32 - 1);
-                        raw_[u].sv[n] = 0u;
+                        sv[u][n] = 0u;
                     }
-                    if (raw_[u].sv[n] > T::kTopScale) {
+                    if (sv[u][n] > T::kTopScale) {
 #pragma unroll
                         for (int st = 0; st < KS; ++st)
                             if (block_of(ch, st) == n)
-                                raw_[u].v[st] = larger_codes(raw_[u].v[st], raw_[u].sv[n] - T::kTopScale);
-                        raw_[u].sv[n] = T::kTopScale;
+                                raw_[u].v[st] = larger_codes(raw_[u].v[st], sv[u][n] - T::kTopScale);
+                        sv[u][n] = T::kTopScale;
                     }
                 }
                 if (__ballot(mine != 0u)) {
@@ -678,7 +703,7 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
         for (int n = 0; n < (SHARE ? 0 : NB); ++n) {
             pack[n] = raw_[0].sk[n];
 #pragma unroll
-            for (int u = 1; u < NU; ++u) pack[n] |= raw_[u].sk[n] << (8 * u);
+            for (int u = 1; u < NU; ++u) pack[n] |= (uint32_t)raw_[u].sk[n] << (8 * u);
         }
 
         // scores: of each head with all columns, then each column its head's
@@ -734,9 +759,9 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
         auto store_v = [&](int u) {
 #pragma unroll
             for (int st = 0; st < KS; ++st) {
-                uint32_t sb = raw_[u].sv[0];
+                uint32_t sb = sv[u][0];
 #pragma unroll
-                for (int b = 1; b < NB; ++b) sb = block_of(ch, st) == b ? raw_[u].sv[b] : sb;
+                for (int b = 1; b < NB; ++b) sb = block_of(ch, st) == b ? sv[u][b] : sb;
                 const vec8 vv = T::from4(raw_[u].v[st], __builtin_bit_cast(float, sb << 23));
                 lds_u8 *row = stage + (HP == 2 ? hsel * S::SECOND + ((u & 1) * KPL + krow) * S::ROW
                                                : (u * KPL + krow) * S::ROW);
@@ -951,12 +976,15 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
 // the key get their NaN at the end).
 //
 // Measured, 64 query heads on 8 K/V heads of 128: 1024 causal tokens over 16384
-// keys 511 us (f16, 1.04 PFLOP/s, where an 8192-cubed library product reaches
-// 1.19), 1000 tokens under a window of 4096 157-161 us back to back and 149 us a
-// call with other inputs between (bf16, 0.85-0.91 PFLOP/s: the longer the
-// products run without a pause, the lower the clock).  The vector units are busy
-// for 49% of the time and the matrix units for 43%, with two waves a SIMD to
-// overlap them.
+// keys 482 us (f16, 1.11 PFLOP/s, where an 8192-cubed library product reaches
+// 1.14), 1000 tokens under a window of 4096 141 us a call with other inputs between
+// (bf16, 0.96 PFLOP/s).  Before the loads of a step ran through the step (see
+// above) and K's rows were read 16 keys ahead of their products: 511 and 149 us.
+// 32 requests of 64 heads over 131072 keys that they share: 64 steps in 130 us,
+// 1.95 GHz, the matrix units busy for 44% of the cycles and the vector units for
+// 40 to 50%, with two waves a SIMD to overlap them; half of the waves a product
+// behind the others, so that they would meet different units, is slower (155 us
+// where all together take 150).
 template <int D>
 struct PromptShape {
     static constexpr int MT = 2, W = kMx4PromptThreads / 64, KEYS = 64, ROWS = W * 16 * MT;
@@ -986,7 +1014,9 @@ __global__ void __launch_bounds__(kMx4PromptThreads, 2) mx4_prompt_kernel(Mx4Att
     const int n_m = MODE == kPrefix ? group.count * a.q_len * a.group : a.q_len * a.group;
     if (MODE == kPrefix && it.m0 >= n_m) return;
     const int seq = a.seq_lens[req];
-    const int prefix = MODE == kOwn ? prefix_before(a, req) : group.prefix;
+    if (MODE == kOwn) group = group_of(a, req);
+    const int prefix = group.prefix;
+    const int own_from = MODE == kOwn && !a.whole ? prefix : 0;
     auto token_in = [&](int m) { return (int)quotient((uint32_t)m, a.div_group); };  // of the request, or its group
     auto seen_of = [&](int m) -> int64_t {
         if (MODE != kPrefix) return (int64_t)seq - a.q_len + 1 + token_in(min(m, n_m - 1));
@@ -998,7 +1028,7 @@ __global__ void __launch_bounds__(kMx4PromptThreads, 2) mx4_prompt_kernel(Mx4Att
     // the workgroup's keys: steps of 64, the first tokens and then the window
     const int64_t first_seen = MODE >= kOwn ? 0 : seen_of(it.m0);
     const int cap_last = capped(MODE == kPrefix ? prefix : seen_of(it.m0 + P::ROWS - 1));
-    const int64_t lo = MODE >= kOwn ? (MODE == kOwn ? prefix : 0) : (a.window ? first_seen - a.window : 0);
+    const int64_t lo = MODE >= kOwn ? own_from : (a.window ? first_seen - a.window : 0);
     const int base = lo > 0 ? (int)min(lo, (int64_t)cap_last) & ~(KEYS - 1) : 0;
     const int sink_steps = MODE < kOwn && a.window ? (min(a.sinks, base) + KEYS - 1) / KEYS : 0;
     int n_steps = sink_steps + (cap_last - base + KEYS - 1) / KEYS;
@@ -1031,7 +1061,7 @@ __global__ void __launch_bounds__(kMx4PromptThreads, 2) mx4_prompt_kernel(Mx4Att
         const int64_t seen = seen_of(m);
         row_end[mt] = capped(seen);
         row_start[mt] = a.window ? (int)min(max((int64_t)0, seen - a.window), (int64_t)row_end[mt]) : 0;
-        if (MODE >= kOwn) row_start[mt] = MODE == kOwn ? prefix : 0;
+        if (MODE >= kOwn) row_start[mt] = own_from;
         mx[mt] = kNegInf;
         ls[mt] = 0.0f;
         nan_blocks[mt] = 0u;
@@ -1050,14 +1080,19 @@ __global__ void __launch_bounds__(kMx4PromptThreads, 2) mx4_prompt_kernel(Mx4Att
     const uint8_t *src_d = (is_v ? a.vd : a.kd) + (uint64_t)((uint32_t)it.kv * (uint32_t)a.pages.d_sh);
     const uint8_t *src_s = (is_v ? a.vs : a.ks) + (uint64_t)((uint32_t)it.kv * (uint32_t)a.pages.s_sh);
     const int32_t *table = a.block_table + (int64_t)req * a.bt_stride;
-    uint32_t code[KS], sc[NB];
+    uint32_t code[KS];
+    uint8_t loaded_sc[NB];  // bytes until they are used: widening them at once would wait for them there
     bool seen_key = false, bad_page = false;
     // position of the thread's key in a step; -1 past the end
     auto position = [&](int step) {
         const int64_t p = (int64_t)start_of(step) + key;
         return step < s_end && p < cap_last ? (int)p : -1;
     };
-    auto load_page = [&](int p) -> int { return table[quotient((uint32_t)max(p, 0), a.pages.div_bs)]; };
+    const int32_t *shared_table = a.block_table + (int64_t)group.first * a.bt_stride;
+    auto load_page = [&](int p) -> int {
+        if (MODE == kOwn) return (p < prefix ? shared_table : table)[quotient((uint32_t)max(p, 0), a.pages.div_bs)];
+        return table[quotient((uint32_t)max(p, 0), a.pages.div_bs)];
+    };
     auto load_codes = [&](int p, int page) {
         const bool in = (uint32_t)page < (uint32_t)a.pages.n_blocks;
         seen_key = p >= 0 && in;
@@ -1069,12 +1104,14 @@ __global__ void __launch_bounds__(kMx4PromptThreads, 2) mx4_prompt_kernel(Mx4Att
         const uint64_t sb = (uint64_t)pg * (uint32_t)a.pages.s_sb + __umul24(at, (uint32_t)a.pages.s_ss);
         __builtin_memcpy(code, __builtin_assume_aligned(src_d + d, ALIGN), KS * 4);
 #pragma unroll
-        for (int n = 0; n < NB; ++n) sc[n] = src_s[sb + (uint32_t)min(blk0 + n, D / 32 - 1)];
+        for (int n = 0; n < NB; ++n) loaded_sc[n] = src_s[sb + (uint32_t)min(blk0 + n, D / 32 - 1)];
     };
     typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
     typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
     auto store_step = [&](int buf) {
-        uint32_t word = bad_page ? 0x80000000u : 0u;
+        uint32_t word = bad_page ? 0x80000000u : 0u, sc[NB];
+#pragma unroll
+        for (int n = 0; n < NB; ++n) sc[n] = loaded_sc[n];
         if (is_v) {
             bool bad = false;
 #pragma unroll
@@ -1114,10 +1151,17 @@ __global__ void __launch_bounds__(kMx4PromptThreads, 2) mx4_prompt_kernel(Mx4Att
         }
     };
 
+    // q, asked for before the first page's id, has arrived when that has.  Said
+    // here, else its first use, which is in the loop, waits there in every step
+    // for all loads on the way, the codes of the next among them
     int pos = -1, page = -1;
-    if (s_begin < s_end) {
+    const bool any_step = s_begin < s_end;
+    if (any_step) {
         pos = position(s_begin);
         page = load_page(pos);
+    }
+    wait_vmem_all_known();
+    if (any_step) {
         load_codes(pos, page);
         pos = position(s_begin + 1);
         page = load_page(pos);
@@ -1139,10 +1183,32 @@ __global__ void __launch_bounds__(kMx4PromptThreads, 2) mx4_prompt_kernel(Mx4Att
         // none of the wave's rows sees a key of this step
         if (p0 >= cap_last_w || (MODE < kOwn && a.window && p0 + KEYS <= first_w && p0 >= a.sinks)) continue;
         const lds_u8 *kb = (const lds_u8 *)smem + buf * P::BUFFER;
+        // scores, the operands of 16 keys read while the products of the 16 before run
+        f32x4 s[MT][4];
+        u32x4 kf[2][KS];
+        auto read_keys = [&](int u) {
+#pragma unroll
+            for (int st = 0; st < KS; ++st)
+                kf[u & 1][st] = *(const lds_u32x4 *)(kb + (u * 16 + col) * ROW + (st * 4 + qd) * 16);
+        };
+        read_keys(0);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            if (u < 3) read_keys(u + 1);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) s[mt][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int st = 0; st < KS; ++st)
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+                    s[mt][u] = T::mfma(__builtin_bit_cast(vec8, kf[u & 1][st]), q[mt][st], s[mt][u]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
         const uint32_t odd = any[buf][0] | any[buf][1] | any[buf][2] | any[buf][3];
         const bool strange = uni((int)odd) != 0;
         const bool whole = !strange && p0 + KEYS <= cap_first_w &&
-                           (MODE >= kOwn ? MODE == kPrefix || p0 >= prefix
+                           (MODE >= kOwn ? p0 >= own_from
                                          : !a.window || p0 + KEYS <= a.sinks || (int64_t)p0 >= last_w);
         auto counts = [&](int mt, int k) -> bool {
             const int p = p0 + k;
@@ -1158,20 +1224,6 @@ __global__ void __launch_bounds__(kMx4PromptThreads, 2) mx4_prompt_kernel(Mx4Att
             }
         }
 
-        // scores
-        f32x4 s[MT][4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) s[mt][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int st = 0; st < KS; ++st) {
-                const u32x4 w = *(const lds_u32x4 *)(kb + (u * 16 + col) * ROW + (st * 4 + qd) * 16);
-                const vec8 kv = __builtin_bit_cast(vec8, w);
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) s[mt][u] = T::mfma(kv, q[mt][st], s[mt][u]);
-            }
-        }
         if (!whole) {
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
@@ -1301,8 +1353,7 @@ __global__ void __launch_bounds__(kMx4JoinThreads) mx4_join_kernel(Mx4Attend a) 
     int n_shares = a.n_splits, skip = 0;
     if (SHARED) {
         n_shares = a.shares;
-        const int64_t request = th / a.n_heads / a.q_len;
-        if (group_of(a, (int)request) < 0) skip = a.prefix_shares;
+        if (a.prefix_shares && !group_of(a, (int)(th / a.n_heads / a.q_len)).count) skip = a.prefix_shares;
     }
     const int c = threadIdx.x % C, g = threadIdx.x / C;
     const float *po = a.part_o + th * n_shares * D + c * 4;

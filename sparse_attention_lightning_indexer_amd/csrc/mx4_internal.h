@@ -101,6 +101,7 @@ struct Mx4Attend {
     const int32_t *prefix_lens, *group_starts;
     int32_t n_groups, max_prefix;
     int32_t shares, prefix_shares, first_share;
+    bool whole;         // no prefix's shares: requests read its keys themselves
     bool finish;        // the launch of the own keys joins a row's shares and its own
     FastDiv div_q;
 };
@@ -133,6 +134,7 @@ Mx4Plan plan_mx4_attend(int n_requests, int q_len, int64_t max_keys, bool select
 // else by a third.
 struct Mx4SharedPlan {
     Mx4Plan prefix, own;
+    bool whole;  // no part of the prefix's own: its keys are few, and cost less than a launch
     bool finish;
     int shares;  // of a row, the prefix's first; without the own where they are joined at once
     size_t part_o_bytes, workspace_bytes;

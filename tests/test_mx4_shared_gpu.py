@@ -12,23 +12,50 @@ if not torch.cuda.is_available():  # pragma: no cover - CPU container
     pytest.skip("needs a GPU", allow_module_level=True)
 
 import sparse_attention_lightning_indexer_amd as li  # noqa: E402
-from mx4_shared_forms import Sizes, lens  # noqa: E402
+from mx4_shared_forms import FORMS, Sizes, lens, of_form, taken  # noqa: E402
+from mx4_shared_forms import kind as form_kind  # noqa: E402
 from oracle import mx4 as plain  # noqa: E402
-from test_mx4_gpu import DEV, Case, check  # noqa: E402
+from test_mx4_gpu import DEV, Case, check, typed  # noqa: E402
+
+
+SAMPLE = 8    # rows of a large case compared with the plain form
 
 
 class Shared(Case):
-    """Requests in groups; the rows of all but a group's first name no page that lies wholly inside the prefix."""
+    """Requests in groups.  The rows of all but a group's first name no page that lies wholly inside the prefix (or,
+    hide=False, the first's)."""
 
     def __init__(self, seed, sizes, kind, hide=True, spread=1.0):
         s = self.sizes = sizes
-        super().__init__(seed, lens(s), s.query, s.heads, s.kv, s.d, s.bs, kind, spread)
+        rng = self.rng = np.random.default_rng(seed)
+        self.lens = np.array(lens(s), dtype=np.int32)
+        self.query, self.heads, self.kv, self.d, self.bs, self.kind = s.query, s.heads, s.kv, s.d, s.bs, kind
         self.starts, self.prefixes = list(s.starts), list(s.prefixes)
-        if hide:
-            for g, prefix in enumerate(self.prefixes):
-                for r in range(self.starts[g] + 1, self.starts[g + 1]):
-                    hidden = [-1, 2**31 - 1, self.n_blocks][r % 3]
-                    self.table[r, :max(prefix, 0) // s.bs] = hidden
+        self.max_seq_len = max(1, int(self.lens.max()))
+        requests, cols = len(self.lens), -(-self.max_seq_len // s.bs)
+        shared = np.zeros(requests, dtype=np.int64)          # pages wholly inside the prefix of another's
+        first = np.arange(requests)
+        for g, prefix in enumerate(self.prefixes):
+            for r in range(self.starts[g] + 1, self.starts[g + 1]):
+                shared[r], first[r] = max(prefix, 0) // s.bs, self.starts[g]
+        self.n_blocks = int((cols - shared).sum()) + 2
+        order = rng.permutation(self.n_blocks).astype(np.int32).tolist()
+        self.table = np.empty((requests, cols), dtype=np.int32)
+        for r in range(requests):
+            own = [order.pop() for _ in range(cols - shared[r])]
+            self.table[r, shared[r]:] = own
+            if shared[r]:
+                self.table[r, :shared[r]] = ([-1, 2**31 - 1, self.n_blocks][r % 3] if hide else
+                                             self.table[first[r], :shared[r]])
+        self.data = [rng.integers(0, 256, (self.n_blocks, s.bs, s.kv, s.d // 2), dtype=np.uint8) for _ in range(2)]
+        self.scale = [rng.integers(123, 129, (self.n_blocks, s.bs, s.kv, s.d // 32), dtype=np.uint8) for _ in range(2)]
+        self.q_t, self.q = typed(rng.standard_normal((requests * s.query, s.heads, s.d)) * spread, kind)
+        self.sm_scale = float(np.float32(1.0 / np.sqrt(s.d)))
+        rows = requests * s.query
+        self.rows = np.arange(rows)
+        if rows * s.heads * self.max_seq_len > 3e6:     # the first and last row, the last of the first group, some others
+            self.rows = np.unique(np.concatenate([[0, rows - 1, self.starts[1] * s.query - 1],
+                                                  rng.permutation(rows)[:SAMPLE]]))
 
     def groups(self):
         on = lambda a: torch.tensor(a, dtype=torch.int32, device=DEV)  # noqa: E731
@@ -37,15 +64,45 @@ class Shared(Case):
                     max_group=max((b - a for a, b in zip(self.starts, self.starts[1:])), default=0))
 
     def want(self, _=None):
-        rows = [plain.values(d, s) for d, s in zip(self.data, self.scale)]
-        return plain.attend_shared(self.q, *rows, self.table, self.lens, self.query, self.max_seq_len, self.sm_scale,
-                                   self.starts, self.prefixes)
+        """Of the rows of the sample, from the pages that their requests and groups name."""
+        requests = set((self.rows // self.query).tolist())
+        requests |= {self.starts[g] for g in range(len(self.prefixes)) for r in list(requests)
+                     if self.starts[g] <= r < self.starts[g + 1]}
+        table = np.full_like(self.table, -1)
+        for r in requests:
+            table[r] = self.table[r]
+        pages, place = np.unique(np.where((table >= 0) & (table < self.n_blocks), table, 0), return_inverse=True)
+        table = np.where((table >= 0) & (table < self.n_blocks), place.reshape(table.shape), -1)
+        rows = [plain.values(d[pages], s[pages]) for d, s in zip(self.data, self.scale)]
+        return plain.attend_shared(self.q, *rows, table, self.lens, self.query, self.max_seq_len, self.sm_scale,
+                                   self.starts, self.prefixes, self.rows)
+
+    def check(self, got, where=""):
+        torch.cuda.synchronize()
+        out, lse, b = self.want()
+        pick = self.rows
+        check([x[pick] for x in got], (out[pick], lse[pick], {k: v[pick] for k, v in b.items()}), self.kind, self.d, where)
 
     def run(self, where="", **kw):
         got = li.mx4_attend_shared(*self.args(), self.max_seq_len, self.sm_scale, **dict(self.groups(), **kw))
-        torch.cuda.synchronize()
-        check(got, self.want(), self.kind, self.d, where)
+        self.check(got, where)
         return got
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("names,d", [(names, d) for names in FORMS for d in FORMS[names]], ids=str)
+def test_every_form(names, d, kind):
+    """Each form of the two parts at each head dimension, against the plain form; then with NaN in the prefix and in own keys."""
+    s = of_form(names, d)
+    assert tuple(form_kind(f) for f in taken(s)) == names
+    case = Shared(21, s, kind)
+    case.run(f"{names} {d}")
+    first, last = case.starts[0], len(case.lens) - 1
+    for which, head, request, p, block in ((1, 0, first, s.prefixes[0] // 2, 0), (0, s.kv - 1, first, 1, d // 32 - 1),
+                                           (1, s.kv - 1, last, int(case.lens[last]) - 1, d // 32 - 1)):
+        case.scale[which][case.table[request, p // s.bs], p % s.bs, head, block] = 255
+    out, _ = case.run(f"{names} {d} NaN")
+    assert torch.isnan(out[:s.query]).any()
 
 
 SHAPES = [
@@ -125,6 +182,7 @@ def test_rows_that_see_less_than_the_prefix():
     want = Shared.want(case)
     case.prefixes = [2**31 - 1]          # counts as max_prefix_len
     got = li.mx4_attend_shared(*case.args(), case.max_seq_len, case.sm_scale, **dict(case.groups(), max_prefix_len=90))
+    torch.cuda.synchronize()
     check(got, want, "f16", 64, "a prefix past its limit")
 
 
@@ -196,17 +254,16 @@ def test_other_layouts(order):
         both = torch.stack((ks, vs), 2)
         ks, vs = both[:, :, 0], both[:, :, 1]
     got = li.mx4_attend_shared(q, kd, ks, vd, vs, *rest, case.max_seq_len, case.sm_scale, **case.groups())
-    check(got, case.want(), "f16", 128, order)
+    case.check(got, order)
 
 
 def test_given_outputs_and_no_lse():
     """Strided outputs, no lse, a workspace of the caller's; nothing else is written."""
-    s = Sizes([0, 4], [90], [3, 20, 1, 33], 2, 8, 2, 64, 16)
-    case = Shared(12, s, "bf16")
+    case = Shared(12, of_form(("two+", "one"), 64), "bf16")
     want = case.run()
-    room = torch.full((8, 9, 80), 5.0, dtype=torch.bfloat16, device=DEV)
-    sizes = (4, 2, case.max_seq_len, 1, 4, 90, 8, 2, 64)
-    need = li.mx4_attend_shared_workspace_bytes(*sizes)
+    room = torch.full((800, 5, 80), 5.0, dtype=torch.bfloat16, device=DEV)
+    need = li.mx4_attend_shared_workspace_bytes(200, 4, case.max_seq_len, 1, 200, 1500, 4, 4, 64)
+    assert need > 0
     workspace = torch.zeros(need + 256, dtype=torch.uint8, device=DEV)
     out, lse = li.mx4_attend_shared(*case.args(), case.max_seq_len, case.sm_scale, **case.groups(), out=room[:, 1:, 8:72],
                                     with_lse=False, workspace=workspace)
@@ -221,22 +278,22 @@ def test_agrees_with_attention_of_its_own():
     s = Sizes([0, 32], [1000], [17] * 32, 1, 64, 8, 128, 64)
     case = Shared(13, s, "f16", hide=False)
     full = 1000 // 64
-    case.table[1:, :full] = case.table[0, :full]
     for a in (*case.data, *case.scale):
         for r in range(1, 32):
             a[case.table[r, full], :1000 % 64] = a[case.table[0, full], :1000 % 64]
     out, lse = case.run()
-    alone = li.mx4_attend_window(*case.args(), case.max_seq_len, case.sm_scale)
-    check(alone, case.want(), "f16", 128, "alone")
+    case.check(li.mx4_attend_window(*case.args(), case.max_seq_len, case.sm_scale), "alone")
     for _ in range(3):
         again = li.mx4_attend_shared(*case.args(), case.max_seq_len, case.sm_scale, **case.groups())
         assert torch.equal(again[0], out) and torch.equal(again[1], lse)
 
 
 def test_streams_and_graphs():
-    """Two captured calls of their own workspaces replayed side by side, lengths changing between replays."""
-    s = Sizes([0, 5, 12], [200, 90], [9] * 12, 1, 16, 2, 128, 16)
-    cases = [Shared(14, s, "f16"), Shared(15, s, "bf16")]
+    """Captured calls of their own workspaces replayed side by side, lengths changing between replays."""
+    small, large = Sizes([0, 5, 12], [200, 90], [9] * 12, 1, 16, 2, 128, 16), of_form(("two+", "one"), 128)
+    cases = [Shared(14, small, "f16"), Shared(15, large, "bf16"), Shared(16, large, "f16")]
+    for case in cases:      # pages that leave the prefix become each request's own
+        case.table = np.where((case.table < 0) | (case.table >= case.n_blocks), 2, case.table).astype(np.int32)
     streams = [torch.cuda.Stream() for _ in cases]
     held = []
     for case, stream in zip(cases, streams):
@@ -252,16 +309,13 @@ def test_streams_and_graphs():
             case.prefixes = [p - 3 * step for p in case.prefixes]
             args[6].copy_(torch.from_numpy(case.lens))
             groups["prefix_lens"].copy_(torch.tensor(case.prefixes, dtype=torch.int32))
-            # pages that left the prefix are each request's own
-            case.table = np.where((case.table < 0) | (case.table >= case.n_blocks), 2, case.table).astype(np.int32)
-            args[5].copy_(torch.from_numpy(case.table))
         torch.cuda.synchronize()
         for (_, _, graph, _), stream in zip(held, streams):
             with torch.cuda.stream(stream):
                 graph.replay()
         torch.cuda.synchronize()
         for case, (_, _, _, out) in zip(cases, held):
-            check(out, case.want(), case.kind, case.d, f"replay {step}")
+            case.check(out, f"replay {step}")
 
 
 def test_refusals():

@@ -99,6 +99,7 @@ indexer_status indexer_norm_rope(const indexer_norm_rope_args *args) {
     a.head_dim = g.head_dim;
     a.n_freq = g.n_freq;
     a.eps = g.eps;
+    a.inv_dim = 1.0f / (float)g.head_dim;
     a.rotary_scale = g.rotary_scale;
     a.bf16 = g.type == INDEXER_ROPE_BF16;
     a.neighbours = g.interleaved != 0;

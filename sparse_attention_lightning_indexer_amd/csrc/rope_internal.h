@@ -21,7 +21,7 @@ struct Rope {
     uint64_t axes[4];  // two bits a frequency
     int32_t n_tokens, head_dim, n_freq;
     int32_t heads[2];
-    float eps, rotary_scale;
+    float eps, rotary_scale, inv_dim;
     bool bf16, neighbours;
     int32_t steps;  // of rows of its token that a wave takes
 };

@@ -5,13 +5,20 @@
 // memory-bound: 4 bytes a value.  `lanes` neighbouring lanes hold a row, each
 // VEC pairs as one wide load of first and one of second values (for pairs of
 // neighbours two consecutive loads), so a rotation never leaves its lane and
-// the norm is a sum over `lanes` lanes by lane moves.
+// the norm is a sum over `lanes` lanes by lane moves.  A wave takes a token (or
+// with few tokens some of its rows) and has kBatch steps of 64 / lanes rows on
+// the way; rows, weights, positions and frequencies are asked for together.
 //
 // The angles depend on the token and the pair alone: a wave computes its
-// token's sines and cosines once, one pair a lane, and its rows read them
-// from LDS.  angle = position * frequency is formed in f64 as turns and reduced
-// to half a turn there; position 131071 at frequency 1 in f32 would be off by
-// 2^-8 radians, and a table of sines would be read again for every token.
+// token's sines and cosines once, one or two pairs a lane, and its rows read
+// them from LDS.  angle = position * frequency is formed in f64 as turns and
+// reduced to half a turn there; position 131071 at frequency 1 in f32 would be
+// off by 2^-8 radians, and a table of sines would be read again for every token.
+//
+// Measured: 16384 tokens of 64 + 8 heads of 128 in bf16 104 us (5.8 TB/s; a copy of
+// 1 GiB reaches 5.1), 4001 tokens of 16 + 16 heads of 80 with three axes 12.6 us, 32
+// tokens of 64 + 8 heads 3.7 us.  With weights loaded value by value and the choice
+// between q's and k's arguments left to a load 162, 24 and 6 us.
 #include "device_common.h"
 #include "rope_internal.h"
 
@@ -49,6 +56,15 @@ __device__ __forceinline__ uint32_t narrow(float lo, float hi) {
     return (uint32_t)__builtin_bit_cast(uint16_t, a) | (uint32_t)__builtin_bit_cast(uint16_t, b) << 16;
 }
 
+// A kernel argument in scalar registers.  Of a choice between two arguments by
+// the lane the compiler would otherwise make a load from the arguments' memory
+// at an address of the lane's, and wait for it.
+__device__ __forceinline__ int64_t held(int64_t v) {
+    asm("" : "+s"(v));
+    return v;
+}
+__device__ __forceinline__ const void *held(const void *p) { return (const void *)held((int64_t)p); }
+
 // The sum over the LANES lanes of a row, in every one of them.
 template <int LANES>
 __device__ __forceinline__ float row_sum(float v) {
@@ -62,111 +78,134 @@ __device__ __forceinline__ float row_sum(float v) {
     return v;
 }
 
-template <bool BF16, int VEC, int LANES, bool NEIGHBOURS>
+template <bool BF16, int VEC, int LANES, bool NEIGHBOURS, bool STREAM>
 __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(Rope a) {
     typedef typename Words<VEC>::type words;
     constexpr int ROWS = 64 / LANES;  // rows of a step
-    __shared__ float turn[kWaves][2][128];
+    __shared__ __attribute__((aligned(16))) float turn[kWaves][2][128];
+    __shared__ __attribute__((aligned(16))) float weight[2][256];
     const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
-    const int64_t token = (int64_t)blockIdx.x * kWaves + wave;
-    if (token >= a.n_tokens) return;
+    const int64_t token = min((int64_t)blockIdx.x * kWaves + wave, (int64_t)a.n_tokens - 1);
     const int first = (int)blockIdx.y * a.steps;  // the wave's first step
     const int all = a.heads[0] + a.heads[1];
+    const int end = (int64_t)blockIdx.x * kWaves + wave < a.n_tokens ? min(first + a.steps, (all + ROWS - 1) / ROWS) : first;
 
     // the lane's pairs: i0 .. i0 + VEC, and where their values lie in a row
     const int i0 = (lane & (LANES - 1)) * VEC;
     const bool inside = i0 < a.head_dim / 2, turns = i0 < a.n_freq;
-    const int at0 = NEIGHBOURS ? 2 * i0 : (turns ? i0 : i0 + a.n_freq);
-    const int at1 = NEIGHBOURS ? 2 * i0 + VEC : (turns ? i0 + a.n_freq : i0 + a.head_dim / 2);
+    const int at0 = !inside ? 0 : NEIGHBOURS ? 2 * i0 : (turns ? i0 : i0 + a.n_freq);
+    const int at1 = !inside ? 0 : NEIGHBOURS ? 2 * i0 + VEC : (turns ? i0 + a.n_freq : i0 + a.head_dim / 2);
 
     struct Row {
         words x0, x1;
     };
     Row rows[kBatch];
     const int row = lane / LANES;
+    const int64_t q_sh = held(a.sh[0]), k_sh = held(a.sh[1]);
+    const uint16_t *q = (const uint16_t *)held(a.x[0]) + token * a.st[0];
+    const uint16_t *k = (const uint16_t *)held(a.x[1]) + token * a.st[1];
     auto load = [&](Row &r, int step) {
-        // past the last head: the last one again, not stored
-        const int h = min(step * ROWS + row, all - 1);
-        const int which = h >= a.heads[0];
-        const uint16_t *src = (const uint16_t *)a.x[which] + token * a.st[which] +
-                              (int64_t)(h - (which ? a.heads[0] : 0)) * a.sh[which];
-        r.x0 = *reinterpret_cast<const words *>(src + (inside ? at0 : 0));
-        r.x1 = *reinterpret_cast<const words *>(src + (inside ? at1 : 0));
+        const int h = min(step * ROWS + row, all - 1);  // past the last head: the last one again, not stored
+        const uint16_t *src = h < a.heads[0] ? q + h * q_sh : k + (h - a.heads[0]) * k_sh;
+        const words *s0 = reinterpret_cast<const words *>(src + at0), *s1 = reinterpret_cast<const words *>(src + at1);
+        r.x0 = STREAM ? __builtin_nontemporal_load(s0) : *s0;
+        r.x1 = STREAM ? __builtin_nontemporal_load(s1) : *s1;
     };
-    const int end = min(first + a.steps, (all + ROWS - 1) / ROWS);
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) load(rows[b], min(first + b, end - 1));
+    for (int b = 0; b < kBatch; ++b)
+        if (first + b < end) load(rows[b], first + b);
 
-    // sines and cosines of the token's pairs
-    for (int i = lane; i < a.n_freq; i += 64) {
-        const int axis = (int)(a.axes[i >> 5] >> (2 * (i & 31))) & 3;
-        const int64_t at = axis * a.pos_stride + token;
-        const double p = a.pos64 ? (double)((const int64_t *)a.positions)[at] : (double)((const int32_t *)a.positions)[at];
-        const double t = p * ((double)a.inv_freq[i] * 0.15915494309189533577);
+    // the weights, for all of the workgroup's waves
+    {
+        const int i = min((int)threadIdx.x, a.head_dim - 1);
+        uint32_t w[2] = {0u, 0u};
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+            if (a.weight[t]) {
+                if (a.weight_f32[t]) w[t] = ((const uint32_t *)a.weight[t])[i];
+                else w[t] = ((const uint16_t *)a.weight[t])[i];
+            }
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+            weight[t][threadIdx.x] = a.weight_f32[t] ? __builtin_bit_cast(float, w[t]) : widen<BF16>(w[t], 0);
+    }
+    // sines and cosines of the token's pairs, two at most a lane
+    double pos[2];
+    float freq[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int i = min(lane + u * 64, a.n_freq - 1);
+        pos[u] = 0.0;
+        freq[u] = 0.0f;
+        if (u * 64 < a.n_freq) {
+            const uint64_t w0 = i & 32 ? held((int64_t)a.axes[1]) : held((int64_t)a.axes[0]);
+            const uint64_t w1 = i & 32 ? held((int64_t)a.axes[3]) : held((int64_t)a.axes[2]);
+            const int axis = (int)((u ? w1 : w0) >> (2 * (i & 31))) & 3;
+            const int64_t at = axis * a.pos_stride + token;
+            if (a.pos64) pos[u] = (double)((const int64_t *)a.positions)[at];
+            else pos[u] = (double)((const int32_t *)a.positions)[at];
+            freq[u] = a.inv_freq[i];
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        if (u * 64 >= a.n_freq) break;
+        const double t = pos[u] * ((double)freq[u] * 0.15915494309189533577);
         float s, c;
         sincospif((float)(2.0 * (t - rint(t))), &s, &c);
-        turn[wave][0][i] = c * a.rotary_scale;
-        turn[wave][1][i] = s * a.rotary_scale;
+        turn[wave][0][lane + u * 64] = c * a.rotary_scale;
+        turn[wave][1][lane + u * 64] = s * a.rotary_scale;
     }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    lds_barrier();
     float c[VEC], s[VEC];
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
-        c[j] = turn[wave][0][turns ? i0 + j : 0];
-        s[j] = turn[wave][1][turns ? i0 + j : 0];
+        c[j] = turn[wave][0][turns ? i0 + j : j];
+        s[j] = turn[wave][1][turns ? i0 + j : j];
     }
-    // the weights of the lane's values, of q and k
-    float w[2][2 * VEC];
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            w[t][j] = w[t][VEC + j] = 1.0f;
-            if (!a.weight[t] || !inside) continue;
-            const int p = at0 + j, q = at1 + j;
-            if (a.weight_f32[t]) {
-                w[t][j] = ((const float *)a.weight[t])[p];
-                w[t][VEC + j] = ((const float *)a.weight[t])[q];
-            } else {
-                w[t][j] = widen<BF16>(((const uint16_t *)a.weight[t])[p], 0);
-                w[t][VEC + j] = widen<BF16>(((const uint16_t *)a.weight[t])[q], 0);
-            }
-        }
 
+    const int64_t q_osh = held(a.ysh[0]), k_osh = held(a.ysh[1]);
+    uint16_t *q_out = (uint16_t *)held(a.y[0]) + token * a.yst[0], *k_out = (uint16_t *)held(a.y[1]) + token * a.yst[1];
+    const bool q_normed = a.weight[0], k_normed = a.weight[1];
     for (int step = first; step < end; step += kBatch) {
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
             if (step + b >= end) break;
             const int h = (step + b) * ROWS + row;
-            const int which = h >= a.heads[0];
+            const bool is_q = h < a.heads[0];
             float x[2 * VEC];
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
                 x[j] = widen<BF16>(rows[b].x0[j / 2], j & 1);
                 x[VEC + j] = widen<BF16>(rows[b].x1[j / 2], j & 1);
             }
-            load(rows[b], min(step + b + kBatch, end - 1));
-            // the norm's sum; bf16 squares may pass f32's range, and are then summed of smaller values
-            float sum = 0.0f;
+            if (step + b + kBatch < end) load(rows[b], step + b + kBatch);
+            if (is_q ? q_normed : k_normed) {
+                float sum = 0.0f;
 #pragma unroll
-            for (int j = 0; j < 2 * VEC; ++j) sum = __builtin_fmaf(x[j], x[j], sum);
-            sum = row_sum<LANES>(inside ? sum : 0.0f);
-            float r = 1.0f / sqrtf(sum / (float)a.head_dim + a.eps);
-            if (BF16 && __ballot(sum == __builtin_huge_valf())) {
-                float small = 0.0f;
+                for (int j = 0; j < 2 * VEC; ++j) sum = __builtin_fmaf(x[j], x[j], sum);
+                sum = row_sum<LANES>(inside ? sum : 0.0f);
+                const float mean = __builtin_fmaf(sum, a.inv_dim, a.eps);
+                float r = __builtin_amdgcn_rsqf(mean);
+                // squares of bf16 values pass f32's range on both sides: such rows are summed again, scaled
+                if (BF16 && __ballot(!(mean >= 0x1p-100f && mean < __builtin_huge_valf()))) {
+                    const float by = mean < 0x1p-100f ? 0x1p70f : 0x1p-70f;
+                    float scaled = 0.0f;
 #pragma unroll
-                for (int j = 0; j < 2 * VEC; ++j) {
-                    const float v = x[j] * 0x1p-70f;
-                    small = __builtin_fmaf(v, v, small);
+                    for (int j = 0; j < 2 * VEC; ++j) {
+                        const float v = x[j] * by;
+                        scaled = __builtin_fmaf(v, v, scaled);
+                    }
+                    scaled = row_sum<LANES>(inside ? scaled : 0.0f);
+                    const float other = by * __builtin_amdgcn_rsqf(__builtin_fmaf(scaled, a.inv_dim, a.eps * by * by));
+                    if (!(mean >= 0x1p-100f && mean < __builtin_huge_valf())) r = other;
                 }
-                small = row_sum<LANES>(inside ? small : 0.0f);
-                if (sum == __builtin_huge_valf()) r = 0x1p-70f / sqrtf(small / (float)a.head_dim);
-            }
-            if (a.weight[which]) {
+                const float *w = weight[is_q ? 0 : 1];
 #pragma unroll
-                for (int j = 0; j < 2 * VEC; ++j) x[j] = x[j] * r * (which ? w[1][j] : w[0][j]);
+                for (int j = 0; j < VEC; ++j) {
+                    x[j] *= r * w[at0 + j];
+                    x[VEC + j] *= r * w[at1 + j];
+                }
             }
             if (turns) {
 #pragma unroll
@@ -184,10 +223,15 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(Rope a) {
                 y0[j] = narrow<BF16>(x[2 * j], x[2 * j + 1]);
                 y1[j] = narrow<BF16>(x[VEC + 2 * j], x[VEC + 2 * j + 1]);
             }
-            uint16_t *dst = (uint16_t *)a.y[which] + token * a.yst[which] +
-                            (int64_t)(h - (which ? a.heads[0] : 0)) * a.ysh[which];
-            *reinterpret_cast<words *>(dst + at0) = y0;
-            *reinterpret_cast<words *>(dst + at1) = y1;
+            uint16_t *dst = is_q ? q_out + h * q_osh : k_out + (h - a.heads[0]) * k_osh;
+            words *d0 = reinterpret_cast<words *>(dst + at0), *d1 = reinterpret_cast<words *>(dst + at1);
+            if (STREAM) {
+                __builtin_nontemporal_store(y0, d0);
+                __builtin_nontemporal_store(y1, d1);
+            } else {
+                *d0 = y0;
+                *d1 = y1;
+            }
         }
     }
 }
@@ -195,10 +239,16 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(Rope a) {
 template <bool BF16, int VEC, int LANES>
 hipError_t launch_lanes(const Rope &a, const RopePlan &p, hipStream_t stream) {
     const dim3 grid((unsigned)((a.n_tokens + (int64_t)kWaves - 1) / kWaves), (unsigned)p.parts), block(kRopeThreads);
+    const bool stream_rows = (int64_t)a.n_tokens * (a.heads[0] + a.heads[1]) * a.head_dim * 2 > (int64_t)32 << 20;
     if (a.neighbours)
-        hipLaunchKernelGGL((norm_rope_kernel<BF16, VEC, LANES, true>), grid, block, 0, stream, a);
+        if (stream_rows)
+            hipLaunchKernelGGL((norm_rope_kernel<BF16, VEC, LANES, true, true>), grid, block, 0, stream, a);
+        else
+            hipLaunchKernelGGL((norm_rope_kernel<BF16, VEC, LANES, true, false>), grid, block, 0, stream, a);
+    else if (stream_rows)
+        hipLaunchKernelGGL((norm_rope_kernel<BF16, VEC, LANES, false, true>), grid, block, 0, stream, a);
     else
-        hipLaunchKernelGGL((norm_rope_kernel<BF16, VEC, LANES, false>), grid, block, 0, stream, a);
+        hipLaunchKernelGGL((norm_rope_kernel<BF16, VEC, LANES, false, false>), grid, block, 0, stream, a);
     return hipGetLastError();
 }
 

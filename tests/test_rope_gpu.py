@@ -159,6 +159,19 @@ def test_extreme_rows(kind):
             assert got[4, 0][turned_with_inf].isnan().all()
 
 
+@pytest.mark.parametrize("eps", [0.0, 1e-30, 1e-6])
+def test_rows_whose_squares_leave_the_range(eps):
+    """bf16 rows of sizes from 2^-120 to 2^120 side by side: their squares are past f32's range on both sides."""
+    n, d, m = 25, 128, 64
+    rng = np.random.default_rng(21)
+    x = rng.standard_normal((n, 3, d)) * np.exp2(np.linspace(-120, 120, 3 * n).reshape(3, n).T[..., None])
+    q = dev(x, torch.bfloat16)
+    positions, inv = rng.integers(0, 9000, (1, n)), frequencies(m)
+    w = (1 + 0.2 * rng.standard_normal(d)).astype(np.float32)
+    got, _ = li.norm_rope(q, None, dev(positions[0]), dev(inv), dev(w), eps=eps)
+    check(got, q, w.astype(np.float64), positions, inv, [0] * m, float(np.float32(eps)), False, 1.0, "bf16")
+
+
 def test_a_weight_norms_and_none_does_not():
     """No weight, no frequency: the rows pass bit for bit; weights of one and eps 0 make unit mean squares."""
     x = torch.randn((5, 3, 40), device=DEV).half()

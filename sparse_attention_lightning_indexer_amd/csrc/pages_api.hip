@@ -113,7 +113,7 @@ indexer_status indexer_pages_copy(const indexer_pages_copy_args *args) {
     PAGES_TRY(check_list("from", g.from, 4));
     PAGES_TRY(check_list("to", g.to, 4));
     for (int32_t first = 0; first < g.n_arrays;) {
-        lidx::PageCopy a{arrays_from(g.arrays, g.n_arrays, first), g.from, g.to, nullptr, g.n, g.n_pages};
+        lidx::PageCopy a{arrays_from(g.arrays, g.n_arrays, first), g.from, g.to, g.n, g.n_pages};
         PAGES_TRY(done(lidx::launch_pages_copy(a, (hipStream_t)g.stream), "page copy launch"));
         first += a.arrays.n;
     }
@@ -138,13 +138,15 @@ indexer_status indexer_pages_fork(const indexer_pages_fork_args *args) {
     a.children = g.children;
     a.fresh = g.fresh;
     a.n = g.n;
-    PAGES_TRY(done(lidx::launch_pages_fork(a, (hipStream_t)g.stream), "page fork launch"));
-    if (g.n_pages == 0 || g.n_cols == 0) return INDEXER_OK;
-    for (int32_t first = 0; first < g.n_arrays;) {
-        const lidx::PageArrays arrays = arrays_from(g.arrays, g.n_arrays, first);
-        PAGES_TRY(done(lidx::launch_pages_fork_copy(a, arrays, (hipStream_t)g.stream), "page fork copy launch"));
+    PAGES_TRY(done(lidx::launch_pages_fork_plan(a, (hipStream_t)g.stream), "page fork launch"));
+    if (g.n_cols == 0) return INDEXER_OK;
+    int32_t first = 0;
+    do {  // the rows, and copies of the first list of arrays, if there is one
+        lidx::PageArrays arrays = arrays_from(g.arrays, g.n_arrays, first);
+        if (g.n_pages == 0) arrays.units = 0;
+        PAGES_TRY(done(lidx::launch_pages_fork(a, arrays, first == 0, (hipStream_t)g.stream), "page fork launch"));
         first += arrays.n;
-    }
+    } while (first < g.n_arrays);
     return INDEXER_OK;
 }
 
@@ -206,13 +208,14 @@ indexer_status indexer_pages_compact(const indexer_pages_compact_args *args) {
     a.moves = (int32_t *)g.workspace;
     a.from = a.moves + 1;
     a.to = a.from + g.n_pages / 2;
-    PAGES_TRY(done(lidx::launch_pages_compact(a, (hipStream_t)g.stream), "page compaction launch"));
-    if (g.n_pages < 2) return INDEXER_OK;
-    for (int32_t first = 0; first < g.n_arrays;) {
-        lidx::PageCopy c{arrays_from(g.arrays, g.n_arrays, first), a.from, a.to, a.moves, g.n_pages / 2, g.n_pages};
-        PAGES_TRY(done(lidx::launch_pages_copy(c, (hipStream_t)g.stream), "page compaction copy launch"));
-        first += c.arrays.n;
-    }
+    PAGES_TRY(done(lidx::launch_pages_compact_plan(a, (hipStream_t)g.stream), "page compaction launch"));
+    int32_t first = 0;
+    do {
+        const lidx::PageArrays arrays = arrays_from(g.arrays, g.n_arrays, first);
+        PAGES_TRY(done(lidx::launch_pages_move(a, arrays, first == 0 && g.n_cols > 0, (hipStream_t)g.stream),
+                       "page compaction launch"));
+        first += arrays.n;
+    } while (first < g.n_arrays);
     return INDEXER_OK;
 }
 

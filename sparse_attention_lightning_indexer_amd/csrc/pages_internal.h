@@ -28,10 +28,10 @@ struct PageArrays {
     FastDiv div_units;
 };
 
-// Pairs of pages to copy: from[i] to to[i]; their number is on the host, or (count) on the device.
+// Pairs of pages to copy: from[i] to to[i].
 struct PageCopy {
     PageArrays arrays;
-    const int32_t *from, *to, *count;
+    const int32_t *from, *to;
     int32_t n, n_pages;
 };
 
@@ -70,12 +70,13 @@ struct PageCompact {
 };
 
 hipError_t launch_pages_copy(const PageCopy &a, hipStream_t stream);
-// The tables, then the copies of each list of arrays.
-hipError_t launch_pages_fork(const PageFork &a, hipStream_t stream);
-hipError_t launch_pages_fork_copy(const PageFork &a, const PageArrays &arrays, hipStream_t stream);
+// Which pages go to whom; then (a list of arrays at a time) the copies and, with the first, the tables' rows.
+hipError_t launch_pages_fork_plan(const PageFork &a, hipStream_t stream);
+hipError_t launch_pages_fork(const PageFork &a, const PageArrays &arrays, bool rows, hipStream_t stream);
 hipError_t launch_pages_grow(const PageGrow &a, hipStream_t stream);
 hipError_t launch_pages_free(const PageFree &a, hipStream_t stream);
-hipError_t launch_pages_compact(const PageCompact &a, hipStream_t stream);
+hipError_t launch_pages_compact_plan(const PageCompact &a, hipStream_t stream);
+hipError_t launch_pages_move(const PageCompact &a, const PageArrays &arrays, bool rows, hipStream_t stream);
 uint32_t page_units(int64_t bytes, int width);
 
 }  // namespace lidx

@@ -2,13 +2,16 @@
 //
 // Copies are memory-bound, two bytes moved for each copied.  A wave takes a
 // unit of a page of one cache, kLoads accesses of 16 bytes a lane, all asked
-// for before the first is stored.
+// for before the first is stored.  512 pages of the 20 caches of four layers, 176 MB:
+// 53 us back to back (6.6 TB/s there and back; a copy of 1 GiB reaches 5.1).
 //
 // Which free page goes to whom depends on all entries of a list and on all
 // pages before it, so one workgroup decides: it scans the list for what each
 // entry needs, then the counts for as many free pages as that, lowest first,
-// and stops there.  The result is the same in any run; only counts change by
-// atomics, whose order does not matter.
+// and stops there (3 to 4 us).  The result is the same in any run; only counts
+// change by atomics, whose order does not matter.  What follows the decision,
+// tables and copies, is one launch, by workgroups of either kind: 64 requests that
+// share four prompts of about 500 pages, 44 MB moved, 10 us.
 #include "device_common.h"
 #include "mx4_internal.h"
 #include "pages_internal.h"
@@ -24,19 +27,33 @@ constexpr int kPlanThreads = 1024, kPlanWaves = kPlanThreads / 64;
 constexpr int kCounts = 16;  // counts of pages a thread looks at at a time
 constexpr int kGroup = 8;    // children whose rows a workgroup writes
 
-template <typename W>
+template <typename W, bool STREAM>
 __device__ __forceinline__ void copy_unit(const uint8_t *src, uint8_t *dst, int64_t left, int lane) {
     W v[kLoads];
     const int64_t n = left / (int64_t)sizeof(W);
+    const W *s = reinterpret_cast<const W *>(src) + lane;
+    W *d = reinterpret_cast<W *>(dst) + lane;
+    auto put = [&](int i) {
+        if (STREAM) __builtin_nontemporal_store(v[i], d + i * 64);
+        else d[i * 64] = v[i];
+    };
+    if (n >= 64 * kLoads) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) v[i] = s[i * 64];
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) put(i);
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < kLoads; ++i)
-        if (i * 64 + lane < n) v[i] = reinterpret_cast<const W *>(src)[i * 64 + lane];
+        if (i * 64 + lane < n) v[i] = s[i * 64];
 #pragma unroll
     for (int i = 0; i < kLoads; ++i)
-        if (i * 64 + lane < n) reinterpret_cast<W *>(dst)[i * 64 + lane] = v[i];
+        if (i * 64 + lane < n) put(i);
 }
 
 // One unit of a page, by a wave.
+template <bool STREAM>
 __device__ __forceinline__ void copy_part(const PageArrays &arrays, uint32_t unit, int from, int to, int lane) {
     int lo = 0, hi = arrays.n - 1;
     while (lo < hi) {
@@ -48,9 +65,9 @@ __device__ __forceinline__ void copy_part(const PageArrays &arrays, uint32_t uni
     const int64_t at = (int64_t)(unit - a.first_unit) * (64 * kLoads) * a.width;
     const uint8_t *src = a.base + (int64_t)from * a.stride + at;
     uint8_t *dst = a.base + (int64_t)to * a.stride + at;
-    if (a.width == 16) copy_unit<u32x4>(src, dst, a.bytes - at, lane);
-    else if (a.width == 4) copy_unit<uint32_t>(src, dst, a.bytes - at, lane);
-    else copy_unit<uint8_t>(src, dst, a.bytes - at, lane);
+    if (a.width == 16) copy_unit<u32x4, STREAM>(src, dst, a.bytes - at, lane);
+    else if (a.width == 4) copy_unit<uint32_t, false>(src, dst, a.bytes - at, lane);
+    else copy_unit<uint8_t, false>(src, dst, a.bytes - at, lane);
 }
 
 // The pair that an item, a unit of a pair's page, belongs to.
@@ -58,17 +75,24 @@ __device__ __forceinline__ int pair_of(int64_t item, const PageArrays &arrays) {
     return (int)(item <= INT32_MAX ? quotient((uint32_t)item, arrays.div_units) : item / arrays.units);
 }
 
-__global__ void __launch_bounds__(kThreads) pages_copy_kernel(PageCopy c) {
+// The pairs of a list, shared out to the waves of `groups` workgroups, of which this is `group`.
+template <bool STREAM>
+__device__ __forceinline__ void copy_pairs(const PageArrays &arrays, const int32_t *list_from, const int32_t *list_to, int n,
+                                           int n_pages, unsigned group, unsigned groups) {
     const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
-    const int n = c.count ? min(*c.count, c.n) : c.n;
-    const int64_t items = (int64_t)n * c.arrays.units;
-    for (int64_t item = (int64_t)blockIdx.x * kWaves + wave; item < items; item += (int64_t)gridDim.x * kWaves) {
-        const int i = pair_of(item, c.arrays);
-        const uint32_t unit = (uint32_t)(item - (int64_t)i * c.arrays.units);
-        const int from = uni(c.from[i]), to = uni(c.to[i]);
-        if ((uint32_t)from >= (uint32_t)c.n_pages || (uint32_t)to >= (uint32_t)c.n_pages || from == to) continue;
-        copy_part(c.arrays, unit, from, to, lane);
+    const int64_t items = (int64_t)n * arrays.units;
+    for (int64_t item = (int64_t)group * kWaves + wave; item < items; item += (int64_t)groups * kWaves) {
+        const int i = pair_of(item, arrays);
+        const uint32_t unit = (uint32_t)(item - (int64_t)i * arrays.units);
+        const int from = uni(list_from[i]), to = uni(list_to[i]);
+        if ((uint32_t)from >= (uint32_t)n_pages || (uint32_t)to >= (uint32_t)n_pages || from == to) continue;
+        copy_part<STREAM>(arrays, unit, from, to, lane);
     }
+}
+
+template <bool STREAM>
+__global__ void __launch_bounds__(kThreads) pages_copy_kernel(PageCopy c) {
+    copy_pairs<STREAM>(c.arrays, c.from, c.to, c.n, c.n_pages, blockIdx.x, gridDim.x);
 }
 
 // The sum of the values of the threads before, and of all of them.  `scratch`
@@ -180,51 +204,66 @@ __global__ void __launch_bounds__(kPlanThreads) pages_fork_plan_kernel(PageFork 
 
 // The rows of kGroup children, 256 columns of them: a thread a column, so the
 // children of one parent in a row add to a page's count once.
-__global__ void __launch_bounds__(kThreads) pages_fork_rows_kernel(PageFork a) {
+__device__ __forceinline__ void fork_rows(const PageFork &a, unsigned group) {
+    __shared__ int fresh_of[kGroup], child_of[kGroup], parent_of[kGroup], full_of[kGroup];
     const PageTable &t = a.t;
-    const int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    const unsigned strips = ((unsigned)t.n_cols + kThreads - 1) / kThreads;
+    const int i0 = (int)(group / strips) * kGroup;
+    const int64_t c = (int64_t)(group % strips) * kThreads + threadIdx.x;
+    if (threadIdx.x < kGroup) {
+        const int i = i0 + (int)threadIdx.x;
+        const int fresh = i < a.n ? a.fresh[i] : -3, child = i < a.n ? a.children[i] : 0, parent = i < a.n ? a.parents[i] : 0;
+        const bool counts = fresh != -3;
+        fresh_of[threadIdx.x] = fresh;
+        child_of[threadIdx.x] = counts ? child : 0;
+        parent_of[threadIdx.x] = counts ? parent : 0;
+        full_of[threadIdx.x] = counts ? t.seq_lens[child] / t.block_size : 0;  // 0 where it was left empty
+    }
+    __syncthreads();
     if (c >= t.n_cols) return;
-    const int i0 = (int)blockIdx.y * kGroup, i1 = min(i0 + kGroup, a.n);
+    int page[kGroup];
+#pragma unroll
+    for (int k = 0; k < kGroup; ++k) page[k] = c < full_of[k] ? t.table[(int64_t)parent_of[k] * t.stride + c] : -1;
     int held = -1, times = 0;
-    for (int i = i0; i < i1; ++i) {
-        const int fresh = a.fresh[i];
-        if (fresh == -3) continue;
-        const int child = a.children[i];
-        int page = -1;
-        if (fresh != -2) {
-            const int full = t.seq_lens[child] / t.block_size;
-            if (c < full) {
-                page = t.table[(int64_t)a.parents[i] * t.stride + c];
-                if ((uint32_t)page >= (uint32_t)t.n_pages) page = -1;
-                if (page != held) {
-                    if (held >= 0) atomicAdd(&t.refs[held], times);
-                    held = page;
-                    times = 0;
-                }
-                ++times;
-            } else if (c == full) {
-                page = fresh;  // or -1
+#pragma unroll
+    for (int k = 0; k < kGroup; ++k) {
+        if (fresh_of[k] == -3) continue;
+        int mine = (uint32_t)page[k] < (uint32_t)t.n_pages ? page[k] : -1;
+        if (c < full_of[k]) {
+            if (mine != held) {
+                if (held >= 0) atomicAdd(&t.refs[held], times);
+                held = mine;
+                times = 0;
             }
+            ++times;
+        } else if (c == full_of[k]) {
+            mine = fresh_of[k] >= 0 ? fresh_of[k] : -1;
         }
-        t.table[(int64_t)child * t.stride + c] = page;
+        t.table[(int64_t)child_of[k] * t.stride + c] = mine;
     }
     if (held >= 0) atomicAdd(&t.refs[held], times);
 }
 
-__global__ void __launch_bounds__(kThreads) pages_fork_copy_kernel(PageFork a, PageArrays arrays) {
+// The copies of the parents' last pages, by the workgroups from first_group on.
+__device__ __forceinline__ void fork_copies(const PageFork &a, const PageArrays &arrays, unsigned group, unsigned groups) {
     const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
     const PageTable &t = a.t;
     const int64_t items = (int64_t)a.n * arrays.units;
-    for (int64_t item = (int64_t)blockIdx.x * kWaves + wave; item < items; item += (int64_t)gridDim.x * kWaves) {
+    for (int64_t item = (int64_t)group * kWaves + wave; item < items; item += (int64_t)groups * kWaves) {
         const int i = pair_of(item, arrays);
         const uint32_t unit = (uint32_t)(item - (int64_t)i * arrays.units);
-        const int to = uni(a.fresh[i]);
+        const int to = uni(a.fresh[i]), parent = uni(a.parents[i]);
         if (to < 0) continue;
-        const int full = t.seq_lens[a.children[i]] / t.block_size;
-        const int from = uni(t.table[(int64_t)a.parents[i] * t.stride + full]);
-        if ((uint32_t)from >= (uint32_t)t.n_pages) continue;
-        copy_part(arrays, unit, from, to, lane);
+        const int full = length_of(t, parent) / t.block_size;
+        const int from = uni(t.table[(int64_t)parent * t.stride + full]);
+        if ((uint32_t)from < (uint32_t)t.n_pages) copy_part<false>(arrays, unit, from, to, lane);
     }
+}
+
+// After the plan: the rows by the first row_groups workgroups, the copies by the others.
+__global__ void __launch_bounds__(kThreads) pages_fork_kernel(PageFork a, PageArrays arrays, unsigned row_groups) {
+    if (blockIdx.x < row_groups) fork_rows(a, blockIdx.x);
+    else fork_copies(a, arrays, blockIdx.x - row_groups, gridDim.x - row_groups);
 }
 
 // New tokens of entry i.
@@ -311,18 +350,21 @@ __global__ void __launch_bounds__(kThreads) pages_slots_kernel(PageGrow a) {
     }
 }
 
-// A row of the list a workgroup of blockIdx.y, 256 columns of it.  An entry is taken by
-// exchanging it with -1, so a row named twice gives its pages back once.
+// A row of the list a workgroup of blockIdx.y, 256 columns of it.  A row named
+// before in the list is left to the workgroups of its first mention.
 __global__ void __launch_bounds__(kThreads) pages_free_kernel(PageFree a) {
     const PageTable &t = a.t;
     const int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    const int r = a.rows[blockIdx.y];
+    const int y = (int)blockIdx.y, r = a.rows[y];
     if ((uint32_t)r >= (uint32_t)t.n_rows) return;
+    int32_t *entry = t.table + (int64_t)r * t.stride + min(c, (int64_t)t.n_cols - 1);
+    const int page = c < t.n_cols ? *entry : -1;
+    bool again = false;
+    for (int i = (int)(threadIdx.x & 63); i < y; i += 64) again |= a.rows[i] == r;
+    if (__ballot(again)) return;
     if (c == 0) t.seq_lens[r] = 0;
-    if (c >= t.n_cols) return;
-    int32_t *entry = t.table + (int64_t)r * t.stride + c;
-    if (*entry == -1) return;
-    const int page = atomicExch(entry, -1);
+    if (page == -1) return;
+    *entry = -1;
     if ((uint32_t)page < (uint32_t)t.n_pages) atomicSub(&t.refs[page], 1);
 }
 
@@ -331,22 +373,29 @@ __global__ void __launch_bounds__(kPlanThreads) pages_compact_plan_kernel(PageCo
     const PageTable &t = a.t;
     constexpr int STEP = kPlanThreads * kCounts;
     int live = 0, below = 0, total;  // pages in use; those of them below `live`, which stay
-    for (int64_t base = 0; base < t.n_pages; base += STEP) {
+    const uint32_t mine = held_bits(t, threadIdx.x * kCounts);
+    const int mine_before = plan_scan(__popc(mine), scratch, total);
+    live = total;
+    for (int64_t base = STEP; base < t.n_pages; base += STEP) {
         plan_scan(__popc(held_bits(t, base + threadIdx.x * kCounts)), scratch, total);
         live += total;
     }
     for (int64_t base = 0; base < live; base += STEP) {
         const int64_t first = base + threadIdx.x * kCounts;
-        plan_scan(first < live ? __popc(held_bits(t, first) & bits_below(first, live)) : 0, scratch, total);
+        const uint32_t bits = base ? (first < live ? held_bits(t, first) : 0u) : mine;
+        plan_scan(__popc(bits & bits_below(first, live)), scratch, total);
         below += total;
     }
     // the free pages below `live` and the pages in use from there on, each in order: live - below of either
     int seen = 0;
     for (int64_t base = 0; base < t.n_pages; base += STEP) {
         const int64_t first = base + threadIdx.x * kCounts;
-        const uint32_t bits = held_bits(t, first);
-        int before = seen + plan_scan(__popc(bits), scratch, total);  // pages in use before this one
-        seen += total;
+        const uint32_t bits = base ? held_bits(t, first) : mine;
+        int before = mine_before;  // pages in use before this one
+        if (t.n_pages > STEP) {
+            before = seen + plan_scan(__popc(bits), scratch, total);
+            seen += total;
+        }
         for (int i = 0; i < kCounts && first + i < t.n_pages; ++i) {
             const int p = (int)(first + i);
             const bool used = bits >> i & 1;
@@ -369,24 +418,37 @@ __global__ void __launch_bounds__(kPlanThreads) pages_compact_plan_kernel(PageCo
     }
 }
 
-__global__ void __launch_bounds__(kThreads) pages_rename_kernel(PageCompact a) {
+// After the plan: table entries renamed by the first row_groups workgroups, pages copied by the others.
+template <bool STREAM>
+__global__ void __launch_bounds__(kThreads) pages_move_kernel(PageCompact a, PageArrays arrays, unsigned row_groups) {
     const PageTable &t = a.t;
-    const int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (c >= t.n_cols) return;
-    for (int r = (int)blockIdx.y; r < t.n_rows; r += (int)gridDim.y) {
-        int32_t *entry = t.table + (int64_t)r * t.stride + c;
-        const int page = *entry;
-        if (page != -1) *entry = (uint32_t)page < (uint32_t)t.n_pages ? a.place[page] : -1;
+    if (blockIdx.x >= row_groups) {
+        copy_pairs<STREAM>(arrays, a.from, a.to, min(*a.moves, t.n_pages / 2), t.n_pages, blockIdx.x - row_groups,
+                           gridDim.x - row_groups);
+        return;
     }
+    const unsigned strips = ((unsigned)t.n_cols + kThreads - 1) / kThreads;
+    const int64_t c = (int64_t)(blockIdx.x % strips) * kThreads + threadIdx.x;
+    if (c >= t.n_cols) return;
+    int32_t *entry = t.table + (int64_t)(blockIdx.x / strips) * t.stride + c;
+    const int page = *entry;
+    if (page != -1) *entry = (uint32_t)page < (uint32_t)t.n_pages ? a.place[page] : -1;
 }
 
-// Workgroups of a copy: a wave a unit, up to 16 workgroups a compute unit, which then take several
+// Workgroups of a copy: a wave a unit, up to 32 workgroups a compute unit, whose
+// waves then take several (8, 16 and 32 a compute unit: 512 pages of 344 KB in 77,
+// 55 and 53 us).
 unsigned copy_groups(int64_t items) {
-    const int64_t groups = (items + kWaves - 1) / kWaves, most = 16 * 256;
+    const int64_t groups = (items + kWaves - 1) / kWaves, most = 32 * 256;
     return (unsigned)(groups < most ? groups : most);
 }
 
-dim3 columns(int n_cols, int rows) { return dim3(n_cols ? (unsigned)((n_cols + kThreads - 1) / kThreads) : 1u, (unsigned)rows); }
+unsigned strips_of(int n_cols) { return ((unsigned)n_cols + kThreads - 1) / kThreads; }
+
+// More bytes than the eight L2s hold on either side of the copy: what is written
+// passes through once.  512 pages of 344 KB, streaming accesses for nothing, what is
+// written, what is read and both: 70, 55, 60 and 70 us.
+bool streams(int64_t items) { return items * 64 * kLoads * 16 > (int64_t)32 << 20; }
 
 }  // namespace
 
@@ -396,21 +458,23 @@ uint32_t page_units(int64_t bytes, int width) {
 }
 
 hipError_t launch_pages_copy(const PageCopy &a, hipStream_t stream) {
-    hipLaunchKernelGGL(pages_copy_kernel, dim3(copy_groups((int64_t)a.n * a.arrays.units)), dim3(kThreads), 0, stream, a);
+    const int64_t items = (int64_t)a.n * a.arrays.units;
+    if (streams(items))
+        hipLaunchKernelGGL((pages_copy_kernel<true>), dim3(copy_groups(items)), dim3(kThreads), 0, stream, a);
+    else
+        hipLaunchKernelGGL((pages_copy_kernel<false>), dim3(copy_groups(items)), dim3(kThreads), 0, stream, a);
     return hipGetLastError();
 }
 
-hipError_t launch_pages_fork(const PageFork &a, hipStream_t stream) {
+hipError_t launch_pages_fork_plan(const PageFork &a, hipStream_t stream) {
     hipLaunchKernelGGL(pages_fork_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a);
-    if (a.t.n_cols > 0)
-        hipLaunchKernelGGL(pages_fork_rows_kernel, columns(a.t.n_cols, (a.n + kGroup - 1) / kGroup), dim3(kThreads), 0, stream,
-                           a);
     return hipGetLastError();
 }
 
-hipError_t launch_pages_fork_copy(const PageFork &a, const PageArrays &arrays, hipStream_t stream) {
-    hipLaunchKernelGGL(pages_fork_copy_kernel, dim3(copy_groups((int64_t)a.n * arrays.units)), dim3(kThreads), 0, stream, a,
-                       arrays);
+hipError_t launch_pages_fork(const PageFork &a, const PageArrays &arrays, bool rows, hipStream_t stream) {
+    const unsigned row_groups = rows ? strips_of(a.t.n_cols) * (((unsigned)a.n + kGroup - 1) / kGroup) : 0u;
+    const unsigned groups = row_groups + (arrays.units ? copy_groups((int64_t)a.n * arrays.units) : 0u);
+    if (groups) hipLaunchKernelGGL(pages_fork_kernel, dim3(groups), dim3(kThreads), 0, stream, a, arrays, row_groups);
     return hipGetLastError();
 }
 
@@ -427,14 +491,25 @@ hipError_t launch_pages_grow(const PageGrow &grow, hipStream_t stream) {
 }
 
 hipError_t launch_pages_free(const PageFree &a, hipStream_t stream) {
-    hipLaunchKernelGGL(pages_free_kernel, columns(a.t.n_cols, a.n), dim3(kThreads), 0, stream, a);
+    const unsigned strips = a.t.n_cols ? strips_of(a.t.n_cols) : 1u;
+    hipLaunchKernelGGL(pages_free_kernel, dim3(strips, (unsigned)a.n), dim3(kThreads), 0, stream, a);
     return hipGetLastError();
 }
 
-hipError_t launch_pages_compact(const PageCompact &a, hipStream_t stream) {
+hipError_t launch_pages_compact_plan(const PageCompact &a, hipStream_t stream) {
     hipLaunchKernelGGL(pages_compact_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a);
-    if (a.t.n_rows > 0 && a.t.n_cols > 0)
-        hipLaunchKernelGGL(pages_rename_kernel, columns(a.t.n_cols, a.t.n_rows), dim3(kThreads), 0, stream, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_pages_move(const PageCompact &a, const PageArrays &arrays, bool rows, hipStream_t stream) {
+    const unsigned row_groups = rows ? strips_of(a.t.n_cols) * (unsigned)a.t.n_rows : 0u;
+    const int64_t items = (int64_t)(a.t.n_pages / 2) * arrays.units;
+    const unsigned groups = row_groups + (items ? copy_groups(items) : 0u);
+    if (!groups) return hipSuccess;
+    if (streams(items))
+        hipLaunchKernelGGL((pages_move_kernel<true>), dim3(groups), dim3(kThreads), 0, stream, a, arrays, row_groups);
+    else
+        hipLaunchKernelGGL((pages_move_kernel<false>), dim3(groups), dim3(kThreads), 0, stream, a, arrays, row_groups);
     return hipGetLastError();
 }
 

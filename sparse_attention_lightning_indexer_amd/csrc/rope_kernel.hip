@@ -15,7 +15,7 @@
 // reduced to half a turn there; position 131071 at frequency 1 in f32 would be
 // off by 2^-8 radians, and a table of sines would be read again for every token.
 //
-// Measured: 16384 tokens of 64 + 8 heads of 128 in bf16 104 us (5.8 TB/s; a copy of
+// Measured: 16384 tokens of 64 + 8 heads of 128 in bf16 102 us (5.9 TB/s; a copy of
 // 1 GiB reaches 5.1), 4001 tokens of 16 + 16 heads of 80 with three axes 12.6 us, 32
 // tokens of 64 + 8 heads 3.7 us.  With weights loaded value by value and the choice
 // between q's and k's arguments left to a load 162, 24 and 6 us.
@@ -108,8 +108,8 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(Rope a) {
         const int h = min(step * ROWS + row, all - 1);  // past the last head: the last one again, not stored
         const uint16_t *src = h < a.heads[0] ? q + h * q_sh : k + (h - a.heads[0]) * k_sh;
         const words *s0 = reinterpret_cast<const words *>(src + at0), *s1 = reinterpret_cast<const words *>(src + at1);
-        r.x0 = STREAM ? __builtin_nontemporal_load(s0) : *s0;
-        r.x1 = STREAM ? __builtin_nontemporal_load(s1) : *s1;
+        r.x0 = *s0;
+        r.x1 = *s1;
     };
 #pragma unroll
     for (int b = 0; b < kBatch; ++b)
@@ -239,6 +239,7 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(Rope a) {
 template <bool BF16, int VEC, int LANES>
 hipError_t launch_lanes(const Rope &a, const RopePlan &p, hipStream_t stream) {
     const dim3 grid((unsigned)((a.n_tokens + (int64_t)kWaves - 1) / kWaves), (unsigned)p.parts), block(kRopeThreads);
+    // more than the eight L2s hold: what is written passes through once (104 us with streaming loads too, 102 without)
     const bool stream_rows = (int64_t)a.n_tokens * (a.heads[0] + a.heads[1]) * a.head_dim * 2 > (int64_t)32 << 20;
     if (a.neighbours)
         if (stream_rows)

@@ -89,12 +89,13 @@ def _set(pages):
 
 def _ints(t, name, dev, n=None):
     """Checks a contiguous i32 vector; its length."""
-    _mx4._need(t, name, _torch.int32, dev, 1)
+    if not (isinstance(t, _torch.Tensor) and t.dtype is _torch.int32 and t.get_device() == dev and t.dim() == 1
+            and t.is_contiguous()):
+        _mx4._need(t, name, _torch.int32, dev, 1)
+        raise ValueError(f"{name} must be contiguous")
     size = t.shape[0]
     if n is not None and size != n:
         raise ValueError(f"{name} must have {n} entries, got {size}")
-    if size > 1 and t.stride(0) != 1:
-        raise ValueError(f"{name} must be contiguous")
     return size
 
 

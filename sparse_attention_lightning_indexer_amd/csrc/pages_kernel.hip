@@ -254,7 +254,7 @@ __device__ __forceinline__ void fork_copies(const PageFork &a, const PageArrays 
         const uint32_t unit = (uint32_t)(item - (int64_t)i * arrays.units);
         const int to = uni(a.fresh[i]), parent = uni(a.parents[i]);
         if (to < 0) continue;
-        const int full = length_of(t, parent) / t.block_size;
+        const int full = min(length_of(t, parent) / t.block_size, t.n_cols - 1);  // (its column exists, whatever the row)
         const int from = uni(t.table[(int64_t)parent * t.stride + full]);
         if ((uint32_t)from < (uint32_t)t.n_pages) copy_part<false>(arrays, unit, from, to, lane);
     }

@@ -53,7 +53,7 @@ class Shared(Case):
         self.sm_scale = float(np.float32(1.0 / np.sqrt(s.d)))
         rows = requests * s.query
         self.rows = np.arange(rows)
-        if rows * s.heads * self.max_seq_len > 3e6:     # the first and last row, the last of the first group, some others
+        if rows > 30 and rows * s.heads * self.max_seq_len > 3e5:     # the first and last row, the last of the first group, some others
             self.rows = np.unique(np.concatenate([[0, rows - 1, self.starts[1] * s.query - 1],
                                                   rng.permutation(rows)[:SAMPLE]]))
 

@@ -101,11 +101,14 @@ def _ints(t, name, dev, n=None):
 
 def _table(block_table, dev):
     """(rows, columns, row stride) of a block table."""
-    _mx4._need(block_table, "block_table", _torch.int32, dev, 2)
+    if not (isinstance(block_table, _torch.Tensor) and block_table.dtype is _torch.int32
+            and block_table.get_device() == dev and block_table.dim() == 2):
+        _mx4._need(block_table, "block_table", _torch.int32, dev, 2)
     rows, cols = block_table.shape
-    if cols > 1 and block_table.stride(1) != 1:
+    stride, one = block_table.stride()
+    if cols > 1 and one != 1:
         raise ValueError("block_table rows must be contiguous")
-    return rows, cols, block_table.stride(0) if rows > 1 else cols
+    return rows, cols, stride if rows > 1 else cols
 
 
 def _refs(refs):

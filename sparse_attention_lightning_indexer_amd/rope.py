@@ -49,12 +49,21 @@ def _weight(w, name, of, d, dev):
         return 0, 0
     if not isinstance(w, _torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if w.dtype not in (_torch.float32, of.dtype):
-        raise TypeError(f"{name} must be torch.float32 or {of.dtype}, got {w.dtype}")
-    _mx4._need(w, name, w.dtype, dev, 1)
+    dtype = w.dtype
+    if dtype is not _torch.float32 and dtype is not of:
+        raise TypeError(f"{name} must be torch.float32 or {of}, got {dtype}")
+    if w.get_device() != dev or w.dim() != 1:
+        _mx4._need(w, name, dtype, dev, 1)
     if w.shape[0] != d or not w.is_contiguous():
         raise ValueError(f"{name} must hold one value per dimension ({d}), contiguous, got {list(w.shape)}")
-    return w.data_ptr(), int(w.dtype is not _torch.float32)
+    return w.data_ptr(), int(dtype is of)
+
+
+def _out(given, like, name, dtype, dev, shape):
+    """The output, a new one unless given, and its strides."""
+    if given is None:
+        return like.new_empty(shape), shape[1] * shape[2], shape[2]
+    return (given, *_mx4._rows(given, name, dtype, dev, shape))
 
 
 def norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -78,36 +87,29 @@ def norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: floa
     kind = _mx4._types.get(dtype)
     if kind is None:
         raise TypeError(f"q must be torch.float16 or torch.bfloat16, got {dtype}")
-    q_strides = _mx4._rows(q, "q", dtype, dev)
-    n, heads, d = shape = tuple(q.shape)
-    if q_out is None:
-        q_out = q.new_empty(shape)
-        q_out_strides = (heads * d, d)
-    else:
-        q_out_strides = _mx4._rows(q_out, "q_out", dtype, dev, shape)
-    k_ptr = k_out_ptr = k_heads = 0
-    k_strides = k_out_strides = (0, 0)
+    q_st, q_sh = _mx4._rows(q, "q", dtype, dev)
+    n, heads, d = shape = q.shape
+    q_out, q_ost, q_osh = _out(q_out, q, "q_out", dtype, dev, shape)
+    k_ptr = k_out_ptr = k_heads = k_st = k_sh = k_ost = k_osh = 0
     if k is not None:
-        k_strides = _mx4._rows(k, "k", dtype, dev)
-        k_heads = k.shape[1]
-        if k.shape[0] != n or k.shape[2] != d:
-            raise ValueError(f"k must be [{n}, k_heads, {d}] as q, got {list(k.shape)}")
-        k_shape = (n, k_heads, d)
-        if k_out is None:
-            k_out = k.new_empty(k_shape)
-            k_out_strides = (k_heads * d, d)
-        else:
-            k_out_strides = _mx4._rows(k_out, "k_out", dtype, dev, k_shape)
+        k_st, k_sh = _mx4._rows(k, "k", dtype, dev)
+        k_n, k_heads, k_d = k_shape = k.shape
+        if k_n != n or k_d != d:
+            raise ValueError(f"k must be [{n}, k_heads, {d}] as q, got {list(k_shape)}")
+        k_out, k_ost, k_osh = _out(k_out, k, "k_out", dtype, dev, k_shape)
         k_ptr, k_out_ptr = k.data_ptr(), k_out.data_ptr()
     elif k_out is not None or k_weight is not None:
         raise ValueError("k_out and k_weight need k")
-    _mx4._need(inv_freq, "inv_freq", torch.float32, dev, 1)
-    freqs = inv_freq.shape[0]
-    if freqs > 1 and inv_freq.stride(0) != 1:
+    if not (isinstance(inv_freq, torch.Tensor) and inv_freq.dtype is torch.float32 and inv_freq.get_device() == dev
+            and inv_freq.dim() == 1 and inv_freq.is_contiguous()):
+        _mx4._need(inv_freq, "inv_freq", torch.float32, dev, 1)
         raise ValueError("inv_freq must be contiguous")
-    if not isinstance(positions, torch.Tensor) or positions.dtype not in (torch.int32, torch.int64):
+    freqs = inv_freq.shape[0]
+    wide = isinstance(positions, torch.Tensor) and positions.dtype is torch.int64
+    if not wide and not (isinstance(positions, torch.Tensor) and positions.dtype is torch.int32):
         raise TypeError("positions must be a torch.int32 or torch.int64 tensor")
-    _mx4._need(positions, "positions", positions.dtype, dev, 1 if axes is None else 2)
+    if positions.get_device() != dev or positions.dim() != (1 if axes is None else 2):
+        _mx4._need(positions, "positions", positions.dtype, dev, 1 if axes is None else 2)
     if axes is None:
         n_axes, pos_stride, words = 1, 0, (0, 0, 0, 0)
     else:
@@ -120,13 +122,12 @@ def norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: floa
         raise ValueError(f"positions must have one entry per token ({n}), got {positions.shape[-1]}")
     if n > 1 and positions.stride(-1) != 1:
         raise ValueError("positions must be contiguous along the tokens")
-    q_w, q_kind = _weight(q_weight, "q_weight", q, d, dev)
-    k_w, k_kind = _weight(k_weight, "k_weight", q, d, dev)
+    q_w, q_kind = _weight(q_weight, "q_weight", dtype, d, dev)
+    k_w, k_kind = _weight(k_weight, "k_weight", dtype, d, dev)
     if n == 0:  # nothing to do (and empty tensors have no address)
         return q_out, k_out
     _mx4._call(dev, lib.indexer_norm_rope, _mx4._pack(
-        NORM_ROPE, q.data_ptr(), *q_strides, k_ptr, *k_strides, q_out.data_ptr(), *q_out_strides, k_out_ptr,
-        *k_out_strides, q_w, k_w, positions.data_ptr(), pos_stride, inv_freq.data_ptr(), *words, _mx4._stream(dev),
-        kind, n, heads, k_heads, d, freqs, n_axes, int(bool(interleaved)), int(positions.dtype is torch.int64), q_kind,
-        k_kind, eps, rotary_scale))
+        NORM_ROPE, q.data_ptr(), q_st, q_sh, k_ptr, k_st, k_sh, q_out.data_ptr(), q_ost, q_osh, k_out_ptr, k_ost, k_osh,
+        q_w, k_w, positions.data_ptr(), pos_stride, inv_freq.data_ptr(), *words, _mx4._stream(dev), kind, n, heads,
+        k_heads, d, freqs, n_axes, int(bool(interleaved)), int(wide), q_kind, k_kind, eps, rotary_scale))
     return q_out, k_out

@@ -187,24 +187,24 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(Rope a) {
                 sum = row_sum<LANES>(inside ? sum : 0.0f);
                 const float mean = __builtin_fmaf(sum, a.inv_dim, a.eps);
                 float r = __builtin_amdgcn_rsqf(mean);
-                // squares of bf16 values pass f32's range on both sides: such rows are summed again, scaled
-                if (BF16 && __ballot(!(mean >= 0x1p-100f && mean < __builtin_huge_valf()))) {
-                    const float by = mean < 0x1p-100f ? 0x1p70f : 0x1p-70f;
-                    float scaled = 0.0f;
+                // squares of bf16 values pass f32's range on both sides: such rows are scaled and summed again
+                const bool range = mean >= 0x1p-100f && mean < __builtin_huge_valf();
+                if (BF16 && __ballot(!range)) {
+                    const float by = range ? 1.0f : (mean < 0x1p-100f ? 0x1p100f : 0x1p-70f);
+                    sum = 0.0f;
 #pragma unroll
                     for (int j = 0; j < 2 * VEC; ++j) {
-                        const float v = x[j] * by;
-                        scaled = __builtin_fmaf(v, v, scaled);
+                        x[j] *= by;
+                        sum = __builtin_fmaf(x[j], x[j], sum);
                     }
-                    scaled = row_sum<LANES>(inside ? scaled : 0.0f);
-                    const float other = by * __builtin_amdgcn_rsqf(__builtin_fmaf(scaled, a.inv_dim, a.eps * by * by));
-                    if (!(mean >= 0x1p-100f && mean < __builtin_huge_valf())) r = other;
+                    sum = row_sum<LANES>(inside ? sum : 0.0f);
+                    r = __builtin_amdgcn_rsqf(__builtin_fmaf(sum, a.inv_dim, a.eps * by * by));
                 }
                 const float *w = weight[is_q ? 0 : 1];
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) {
-                    x[j] *= r * w[at0 + j];
-                    x[VEC + j] *= r * w[at1 + j];
+                    x[j] = x[j] * r * w[at0 + j];  // (r times a weight may leave the range)
+                    x[VEC + j] = x[VEC + j] * r * w[at1 + j];
                 }
             }
             if (turns) {

@@ -172,6 +172,18 @@ def test_rows_whose_squares_leave_the_range(eps):
     check(got, q, w.astype(np.float64), positions, inv, [0] * m, float(np.float32(eps)), False, 1.0, "bf16")
 
 
+@pytest.mark.parametrize("size,scale", [(-131, 0), (-128, -20), (-48, 100), (-60, 120), (100, -90), (40, 80)])
+def test_rows_and_weights_far_apart(size, scale):
+    """bf16 rows down to subnormal values, with weights whose product with 1 / sqrt(mean) leaves f32's range."""
+    n, d, m = 20, 64, 32
+    rng = np.random.default_rng(22)
+    q = dev(rng.standard_normal((n, 2, d)) * 2.0**size, torch.bfloat16)
+    positions, inv = rng.integers(0, 9000, (1, n)), frequencies(m)
+    w = ((1 + 0.2 * rng.standard_normal(d)) * 2.0**scale).astype(np.float32)
+    got, _ = li.norm_rope(q, None, dev(positions[0]), dev(inv), dev(w), eps=0.0)
+    check(got, q, w.astype(np.float64), positions, inv, [0] * m, 0.0, False, 1.0, "bf16")
+
+
 def test_a_weight_norms_and_none_does_not():
     """No weight, no frequency: the rows pass bit for bit; weights of one and eps 0 make unit mean squares."""
     x = torch.randn((5, 3, 40), device=DEV).half()

@@ -447,7 +447,7 @@ Mx4SharedPlan plan_mx4_shared(int n_requests, int q_len, int max_seq_len, int n_
         }
         p.prefix = plan_prefix(n_groups, max_group * q_len, rows, prefix_keys, n_heads, n_kv, head_dim,
                                kMx4MaxSplits - p.own.n_splits);
-        const int64_t group_rows = n_m * ((n_requests + n_groups - 1) / n_groups);
+        const int64_t group_rows = n_m * (((int64_t)n_requests + n_groups - 1) / n_groups);
         const bool joined = !p.own.prompt && p.own.n_splits == 1;
         const double apart =
             estimate(p.prefix, n_groups, rows, group_rows, prefix_keys, n_heads, n_kv, head_dim, false) +

@@ -24,7 +24,9 @@
  *
  * A list of table rows may name a row that is not there (negative, or past
  * n_rows; padding of a batch), which is skipped, and name one twice: the
- * second and later ones are skipped.
+ * second and later ones are skipped.  Tables and lists have at most 8192 rows;
+ * those of a call times its columns (rounded up to 256) fill a launch of fewer
+ * than 2^32 threads, else it is INDEXER_EINVAL.
  */
 #ifndef LIGHTNING_INDEXER_PAGES_H
 #define LIGHTNING_INDEXER_PAGES_H
@@ -99,8 +101,9 @@ indexer_status indexer_pages_fork(const indexer_pages_fork_args *args);
  * as 0..tokens): its row the free pages that ceil((len + new) / block_size)
  * asks for, its seq_len len + new.  It must be the only holder of a partly
  * filled last page, as indexer_pages_fork leaves it.  A request whose row has
- * no column left is left as it is; so is one that needs pages where the pages
- * needed by the list up to it are more than were free.
+ * no column left is left as it is; so is one whose partly filled last page is
+ * not of the pool, and one that needs pages where the pages needed by the list
+ * up to it are more than were free.
  *
  *   slots  i64 [n][tokens], out: where the new tokens go in the caches, page *
  *          block_size + offset, as indexer_mx4_cache_write takes them; -1 for

@@ -82,6 +82,8 @@ def grow(refs, table, lens, rows, tokens, bs, new_tokens=None):
         held, want = -(-length // bs), -(-(length + new) // bs)
         if want > cols:
             continue
+        if new and length % bs and not 0 <= table[r][length // bs] < len(refs):
+            continue
         asked += want - held
         if want > held and asked > len(free):
             continue
@@ -91,7 +93,7 @@ def grow(refs, table, lens, rows, tokens, bs, new_tokens=None):
             refs[page] = 1
         for k in range(new):
             page = table[r][(length + k) // bs]
-            mine[k] = page * bs + (length + k) % bs if 0 <= page < len(refs) else -1
+            mine[k] = page * bs + (length + k) % bs
         lens[r] = length + new
     return slots
 

@@ -93,6 +93,12 @@ indexer_status check_rows(int32_t n, int32_t n_rows) {
     return INDEXER_OK;
 }
 
+indexer_status check_launch(int32_t n_cols, int32_t n) {
+    if (!lidx::page_rows_fit(n_cols, n))
+        PAGES_FAIL(INDEXER_EINVAL, "problem too large for one launch: %d rows of %d columns", n, n_cols);
+    return INDEXER_OK;
+}
+
 indexer_status check_block(int32_t block_size, int32_t n_cols) {
     if (block_size < 1) PAGES_FAIL(INDEXER_EINVAL, "block_size=%d must be >= 1", block_size);
     if ((int64_t)n_cols * block_size > kMaxTokens)
@@ -131,6 +137,7 @@ indexer_status indexer_pages_fork(const indexer_pages_fork_args *args) {
     PAGES_TRY(check_table(g.refs, g.block_table, g.table_stride, g.seq_lens, g.n_pages, g.n_rows, g.n_cols, g.block_size, &a.t));
     if (g.n == 0) return done(hipSuccess, "");
     if (g.n_rows > 0) PAGES_TRY(check_list("seq_lens", g.seq_lens, 4));
+    PAGES_TRY(check_launch(g.n_cols, g.n));
     PAGES_TRY(check_list("parents", g.parents, 4));
     PAGES_TRY(check_list("children", g.children, 4));
     PAGES_TRY(check_list("fresh", g.fresh, 4));
@@ -182,6 +189,7 @@ indexer_status indexer_pages_free(const indexer_pages_free_args *args) {
     lidx::PageFree a{};
     PAGES_TRY(check_table(g.refs, g.block_table, g.table_stride, g.seq_lens, g.n_pages, g.n_rows, g.n_cols, 0, &a.t));
     if (g.n == 0 || g.n_rows == 0) return done(hipSuccess, "");
+    PAGES_TRY(check_launch(g.n_cols, g.n));
     PAGES_TRY(check_list("seq_lens", g.seq_lens, 4));
     PAGES_TRY(check_list("rows", g.rows, 4));
     a.rows = g.rows;
@@ -197,6 +205,7 @@ indexer_status indexer_pages_compact(const indexer_pages_compact_args *args) {
     PAGES_TRY(check_rows(0, g.n_rows));
     lidx::PageCompact a{};
     PAGES_TRY(check_table(g.refs, g.block_table, g.table_stride, nullptr, g.n_pages, g.n_rows, g.n_cols, 0, &a.t));
+    PAGES_TRY(check_launch(g.n_cols, g.n_rows));
     PAGES_TRY(check_list("live", g.live, 4));
     if (g.n_pages > 0) PAGES_TRY(check_list("place", g.place, 4));
     const size_t need = indexer_pages_compact_workspace_bytes(g.n_pages);

@@ -77,6 +77,8 @@ hipError_t launch_pages_grow(const PageGrow &a, hipStream_t stream);
 hipError_t launch_pages_free(const PageFree &a, hipStream_t stream);
 hipError_t launch_pages_compact_plan(const PageCompact &a, hipStream_t stream);
 hipError_t launch_pages_move(const PageCompact &a, const PageArrays &arrays, bool rows, hipStream_t stream);
+// A launch holds the rows of n entries, 256 columns a workgroup, and the copies.
+bool page_rows_fit(int n_cols, int64_t n);
 uint32_t page_units(int64_t bytes, int width);
 
 }  // namespace lidx

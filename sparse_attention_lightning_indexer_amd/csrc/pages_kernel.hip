@@ -26,6 +26,7 @@ constexpr int kLoads = 4;
 constexpr int kPlanThreads = 1024, kPlanWaves = kPlanThreads / 64;
 constexpr int kCounts = 16;  // counts of pages a thread looks at at a time
 constexpr int kGroup = 8;    // children whose rows a workgroup writes
+constexpr int kOwnPages = 2; // new pages of a row that its thread writes itself
 
 template <typename W, bool STREAM>
 __device__ __forceinline__ void copy_unit(const uint8_t *src, uint8_t *dst, int64_t left, int lane) {
@@ -282,13 +283,13 @@ __device__ __forceinline__ int64_t slot_of(const PageGrow &a, int i, int k) {
     if (k >= mine) return -1;
     const uint32_t p = (uint32_t)(t.seq_lens[r] - mine + k), c = p / (uint32_t)t.block_size;
     const int page = t.table[(int64_t)r * t.stride + c];
-    if ((uint32_t)page >= (uint32_t)t.n_pages) return -1;
     return (int64_t)page * t.block_size + (p - c * (uint32_t)t.block_size);
 }
 
 __global__ void __launch_bounds__(kPlanThreads) pages_grow_kernel(PageGrow a) {
-    __shared__ int first[kPageRows], upto_of[kPageRows], scratch[kPlanWaves];
+    __shared__ int first[kPageRows], upto_of[kPageRows], scratch[kPlanWaves], long_rows;
     const PageTable &t = a.t;
+    if (threadIdx.x == 0) long_rows = 0;
     mark_first(first, a.rows, a.n, t.n_rows);
     // entry i needs pages upto_of[i - 1] .. upto_of[i] of the free ones; bit 31: it is left or skipped
     int wanted = 0;
@@ -299,9 +300,11 @@ __global__ void __launch_bounds__(kPlanThreads) pages_grow_kernel(PageGrow a) {
         if (i < a.n) {
             const int r = a.rows[i];
             if ((uint32_t)r < (uint32_t)t.n_rows && first[r] == i) {
-                const int len = length_of(t, r);
-                const int64_t want = pages_for((int64_t)len + new_of(a, i), t.block_size);
+                const int len = length_of(t, r), more = new_of(a, i);
+                const int64_t want = pages_for((int64_t)len + more, t.block_size);
                 counts = want <= t.n_cols;
+                if (counts && more && len % t.block_size)  // the page that is not full yet
+                    counts = (uint32_t)t.table[(int64_t)r * t.stride + len / t.block_size] < (uint32_t)t.n_pages;
                 if (counts) need = (int)(want - pages_for(len, t.block_size));
             }
         }
@@ -320,16 +323,34 @@ __global__ void __launch_bounds__(kPlanThreads) pages_grow_kernel(PageGrow a) {
         bool grows = word >= 0 && (need == 0 || upto <= have);
         if (grows) {
             const int r = a.rows[i], len = length_of(t, r), held = (int)pages_for(len, t.block_size);
-            for (int k = 0; k < need; ++k) {
+            for (int k = 0; k < min(need, kOwnPages); ++k) {
                 const int page = (int)a.slots[upto - need + k];
                 t.table[(int64_t)r * t.stride + held + k] = page;
                 t.refs[page] = 1;
             }
+            if (need > kOwnPages) long_rows = 1;
             t.seq_lens[r] = len + new_of(a, i);
         }
         first[i] = grows;  // rows are known; i < kPageRows
     }
     __syncthreads();
+    if (long_rows) {  // the other pages of long rows, a thread each
+        for (int rank = threadIdx.x; rank < have; rank += kPlanThreads) {
+            int lo = 0, hi = a.n - 1;  // whose it is: the first that asks for more up to there
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if ((upto_of[mid] & 0x7fffffff) > rank) hi = mid;
+                else lo = mid + 1;
+            }
+            const int k = rank - (lo ? upto_of[lo - 1] & 0x7fffffff : 0);
+            if (!first[lo] || k < kOwnPages) continue;
+            const int r = a.rows[lo], held = (int)pages_for(t.seq_lens[r] - new_of(a, lo), t.block_size);
+            const int page = (int)a.slots[rank];
+            t.table[(int64_t)r * t.stride + held + k] = page;
+            t.refs[page] = 1;
+        }
+        __syncthreads();
+    }
     // the first slot of every entry, and in a short list the others
     for (int i = threadIdx.x; i < a.n; i += kPlanThreads)
         a.slots[(int64_t)i * a.tokens] = first[i] ? slot_of(a, i, 0) : -1;
@@ -435,6 +456,8 @@ __global__ void __launch_bounds__(kThreads) pages_move_kernel(PageCompact a, Pag
     if (page != -1) *entry = (uint32_t)page < (uint32_t)t.n_pages ? a.place[page] : -1;
 }
 
+unsigned strips_of(int n_cols) { return ((unsigned)n_cols + kThreads - 1) / kThreads; }
+
 // Workgroups of a copy: a wave a unit, up to 32 workgroups a compute unit, whose
 // waves then take several (8, 16 and 32 a compute unit: 512 pages of 344 KB in 77,
 // 55 and 53 us).
@@ -443,7 +466,6 @@ unsigned copy_groups(int64_t items) {
     return (unsigned)(groups < most ? groups : most);
 }
 
-unsigned strips_of(int n_cols) { return ((unsigned)n_cols + kThreads - 1) / kThreads; }
 
 // More bytes than the eight L2s hold on either side of the copy: what is written
 // passes through once.  512 pages of 344 KB, streaming accesses for nothing, what is
@@ -451,6 +473,10 @@ unsigned strips_of(int n_cols) { return ((unsigned)n_cols + kThreads - 1) / kThr
 bool streams(int64_t items) { return items * 64 * kLoads * 16 > (int64_t)32 << 20; }
 
 }  // namespace
+
+bool page_rows_fit(int n_cols, int64_t n) {
+    return ((int64_t)strips_of(n_cols) * n + 32 * 256) * kThreads <= (int64_t)UINT32_MAX;
+}
 
 uint32_t page_units(int64_t bytes, int width) {
     const int64_t unit = (int64_t)64 * kLoads * width;
@@ -481,7 +507,9 @@ hipError_t launch_pages_fork(const PageFork &a, const PageArrays &arrays, bool r
 hipError_t launch_pages_grow(const PageGrow &grow, hipStream_t stream) {
     PageGrow a = grow;
     const int64_t all = (int64_t)a.n * a.tokens;
-    a.all = all <= 16 * kPlanThreads;
+    // few slots are written by the workgroup that decides: 4096 of one request in 7.8 us,
+    // 8192 in 10.3 where two launches take 7.5, and 16384 in 15.5 where they take 7.7
+    a.all = all <= 4 * kPlanThreads;
     hipLaunchKernelGGL(pages_grow_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a);
     if (!a.all) {
         const int64_t groups = (all + kThreads - 1) / kThreads;

@@ -167,7 +167,8 @@ def pages_grow(refs, block_table, seq_lens, rows, tokens: int, block_size: int, 
     most `tokens`) of them: free pages, lowest first, in the order of the list,
     and their lengths.  -> slots i64 [n, tokens], -1 past a request's new
     tokens and for requests that could not grow (no free page or no column
-    left; they stay as they were) or were skipped."""
+    left, or a last page that is not of the pool; they stay as they were) or
+    were skipped."""
     lib = _library()
     dev, n_pages = _refs(refs)
     n_rows, cols, stride = _table(block_table, dev)

@@ -77,6 +77,7 @@ TABLE = [
     (dict(stride=39), li.EINVAL, b"table_stride"),
     (dict(rows=8193), li.ENOTSUP, b"n_rows=8193"),
 ]
+WIDE = dict(cols=2**29, stride=2**29, bs=1)
 LIST = [(dict(n=-1), li.EINVAL, b"n=-1")]
 ROWS = LIST + [(dict(n=8193), li.ENOTSUP, b"n=8193"), (dict(lens=0), li.EINVAL, b"seq_lens is NULL"),
                (dict(lens=A + 2), li.EINVAL, b"seq_lens must be")]
@@ -85,16 +86,17 @@ REFUSALS = {
     "copy": POOL + ARRAYS + LIST + [({"from": 0}, li.EINVAL, b"from is NULL"), (dict(to=B + 2), li.EINVAL, b"to must be")],
     "fork": POOL + ARRAYS + TABLE + ROWS + BLOCK + [
         (dict(parents=0), li.EINVAL, b"parents"), (dict(children=A + 1), li.EINVAL, b"children"),
-        (dict(fresh=0), li.EINVAL, b"fresh")],
+        (dict(fresh=0), li.EINVAL, b"fresh"), (dict(WIDE, n=9), li.EINVAL, b"9 rows of 536870912 columns")],
     "grow": POOL + TABLE + ROWS + BLOCK + [
         (dict(tokens=-1), li.EINVAL, b"tokens=-1"), (dict(tokens=2**30), li.ENOTSUP, b"n*tokens"),
         (dict(list=0), li.EINVAL, b"rows is NULL"), (dict(slots=A + 4), li.EINVAL, b"slots must be 8-byte"),
         (dict(new=A + 2), li.EINVAL, b"new_tokens")],
-    "free": POOL + TABLE + ROWS + [(dict(list=A + 2), li.EINVAL, b"rows must be")],
+    "free": POOL + TABLE + ROWS + [
+        (dict(WIDE, n=8), li.EINVAL, b"too large for one launch"), (dict(list=A + 2), li.EINVAL, b"rows must be")],
     "compact": POOL + ARRAYS + TABLE + [
         (dict(place=0), li.EINVAL, b"place"), (dict(live=0), li.EINVAL, b"live"),
-        (dict(ws=0), li.EWORKSPACE, b"workspace"), (dict(ws=A + 2), li.EWORKSPACE, b"workspace"),
-        (dict(ws_bytes=403), li.EWORKSPACE, b"needs 404 bytes")],
+        (dict(WIDE, rows=8), li.EINVAL, b"8 rows of 536870912 columns"), (dict(ws=0), li.EWORKSPACE, b"workspace"),
+        (dict(ws=A + 2), li.EWORKSPACE, b"workspace"), (dict(ws_bytes=403), li.EWORKSPACE, b"needs 404 bytes")],
 }
 
 

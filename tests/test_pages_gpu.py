@@ -134,6 +134,33 @@ def test_long_slots():
     p.same()
 
 
+def test_prompts_of_many_pages():
+    """Requests that ask for hundreds of pages beside some that ask for one, two, three or none, or find too few."""
+    p = Pool(2000, 40, 700, 4, seed=12)
+    p.grow([7, 3, 39, 20, 21, 0], 2700, [1, 2699, 8, 9, 0, 2700])
+    p.same()
+    order = p.rng.permutation(40).tolist()
+    p.grow(order + [-1, 40], 1500, [int(v) for v in p.rng.choice([0, 1, 3, 4, 5, 8, 9, 13, 200, 1500], 42)])
+    p.same()
+    p.free(order[:30])
+    p.grow(order, 901)
+    p.same()
+
+
+@pytest.mark.parametrize("tokens", [5, 4000])
+def test_a_row_without_its_last_page_does_not_grow(tokens):
+    """The partly filled last page is none of the pool's: left as it is; a missing full page before it does not matter."""
+    p = Pool(4000, 6, 1100, 8, seed=13)
+    p.grow(list(range(6)), 21)
+    for row, column, page in ((0, 2, -1), (1, 2, 4000), (2, 2, 2**31 - 1), (3, 1, -7)):
+        p.refs[p.table[row][column]] -= 1
+        p.table[row][column] = page
+    p.put()
+    p.grow([0, 1, 2, 3, 4], tokens, [tokens, 0, 4, tokens, tokens])
+    p.same()
+    assert p.lens[:5] == [21, 21, 21, 21 + tokens, 21 + tokens]
+
+
 @pytest.mark.parametrize("n_pages", [40000, 16384, 16385])
 def test_large_pools(n_pages):
     """More pages than the decision looks at in one step: free ones only far behind, and compaction of all."""

@@ -228,6 +228,11 @@ indexer_status indexer_mx4_attend_window(const indexer_mx4_attend_args *args);
  *   max_group     the most requests of a group, in 0..n_requests.  Rows of a
  *                 group's requests past it have undefined results
  *
+ * How a call's work is laid out follows from its sizes: requests' own keys are
+ * taken to be max_seq_len - max_prefix_len at most.  A request of far more (of
+ * a far shorter prefix, or of none) is as right, but slower than in a call of
+ * its own kind.
+ *
  * Limits and errors are those of the other attention calls, and
  * n_groups * max_group * query_len * n_heads at most 2^31 - 1024.
  */

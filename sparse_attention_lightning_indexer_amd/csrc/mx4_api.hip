@@ -243,11 +243,10 @@ static Mx4Plan sized(Mx4Plan p, int64_t rows, int n_heads, int n_kv, int head_di
 // compute unit and 10 us, the keys shared out where that fills the last round
 // better, at the price of a second launch and of the shares' traffic; against
 // 0.79 us a SIMD for 32 keys and 32 rows of a wave, and 7 us a round.  Measured,
-// together and apart, 8 query heads a K/V head: 1024 tokens over 16384 keys 510
-// and 783 us, 512 tokens 304 and 401, 1000 under a window of 4096 156 and 223,
-// 1100 under one of 512 77 and 108, 128 under one of 1024 37 and 18, 256 over
-// 2048 52 and 39, 16 tokens of 32 requests over 4096 115 and 128, 4 tokens of
-// them 106 and 41.
+// together and apart, 8 query heads a K/V head: 1024 tokens over 16384 keys 557
+// and 841 us, 512 tokens 297 and 403, 1000 under a window of 4096 154 and 217,
+// 1100 under one of 512 75 and 109, 128 under one of 1024 37 and 18, 256 over
+// 2048 52 and 39, 16 tokens of 32 requests over 4096 121 and 138.
 //
 // Where a row's pairs of heads make a multiple of four and the rows fill the
 // chip, the four waves of a workgroup take the same keys of four pairs, instead

@@ -48,8 +48,8 @@
 //    indices one more.
 //
 // Measured, 64 query heads on 8 K/V heads of 128: one row over 131072 keys 31 us
-// (bf16, 4.6 TB/s: memory); 128 rows x 2048 keys of 32 requests 64 us (bf16, 4.5
-// TB/s in gathered rows); 32 rows under a window of 1024 13.3 us and 32 rows x 512
+// (bf16, 4.6 TB/s: memory); 128 rows x 2048 keys of 32 requests 62 us (bf16, 4.7
+// TB/s in gathered rows); 32 rows under a window of 1024 12.5 us and 32 rows x 512
 // keys 9.5 us (f16: the latency of dependent loads and few tiles a wave).  What is
 // loaded ahead is used as loaded, in a later tile (scale bytes as bytes), and q is
 // known to have arrived before the loop: a value widened at once, or first used

@@ -384,7 +384,9 @@ def mx4_attend_shared(q, k_data, k_scale, v_data, v_scale, block_table, seq_lens
     first prefix_lens[g] (i32 [n_groups], at most max_prefix_len) positions,
     whose pages the group's first request's row of block_table names; later
     positions are read through each request's own row, as pages_fork makes
-    them.  Other arguments and results as in mx4_attend_window without a
+    them.  The work is laid out for max_seq_len - max_prefix_len own keys:
+    requests of far more (of shorter prefixes, or of none) do better in a call
+    of their own.  Other arguments and results as in mx4_attend_window without a
     window."""
     lib = _library()
     if not isinstance(q, _torch.Tensor):

@@ -288,6 +288,43 @@ def test_agrees_with_attention_of_its_own():
         assert torch.equal(again[0], out) and torch.equal(again[1], lse)
 
 
+@pytest.mark.parametrize("requests,query,prefix,kind", [(40, 1, 2000, "f16"), (3, 70, 500, "bf16"), (5, 2, 60, "f16"),
+                                                        (9, 1, 3000, "bf16")])
+def test_rows_of_infinities_and_nan_stay_alone(requests, query, prefix, kind):
+    """Query rows that hold a NaN, an infinity or the type's largest values: NaN and finite results where attention
+    without shared prefixes has them, all other rows as without such rows, within the bounds of the plain form (rows of
+    a wave take a new reference for their weights together, so their roundings may differ)."""
+    s = Sizes([0, requests], [prefix], [query + i % 5 for i in range(requests)], query, 16, 2, 128, 32)
+    case = Shared(31, s, kind, hide=False)
+    full = prefix // 32
+    for a in (*case.data, *case.scale):
+        for r in range(1, requests):
+            a[case.table[r, full], :prefix % 32] = a[case.table[0, full], :prefix % 32]
+    rest, rest_lse = case.run("plain rows")
+    rows = requests * query
+    odd = {0: (3, float("nan")), 1: (17, float("inf")), 2: (0, float("-inf")), rows - 2: (9, 0.0), rows - 1: (5, None)}
+    for row, (head, value) in odd.items():
+        if value is None:
+            case.q_t[row, head] = torch.finfo(case.q_t.dtype).max
+        else:
+            case.q_t[row, head % 16, 7] = value
+    out, lse = li.mx4_attend_shared(*case.args(), case.max_seq_len, case.sm_scale, **case.groups())
+    alone, alone_lse = li.mx4_attend_window(*case.args(), case.max_seq_len, case.sm_scale)
+    assert torch.equal(out.isnan(), alone.isnan()) and torch.equal(lse.isnan(), alone_lse.isnan())
+    assert out[0, 3].isnan().all()
+    for row, (head, _) in odd.items():
+        out[row, head % 16], lse[row, head % 16] = rest[row, head % 16], rest_lse[row, head % 16]
+    assert out.isfinite().all() and lse.isfinite().all()
+    case.check((out, lse), "beside odd rows")
+
+
+def test_requests_that_share_little_beside_long_prefixes():
+    """A group of a long prefix with one of a short prefix and many own keys, and lone requests: far more own keys
+    than the call's sizes say."""
+    Shared(32, Sizes([0, 3, 5, 6], [4000, 40, 0], [3, 1, 20, 3900, 2000, 4010], 1, 16, 2, 128, 64), "f16").run()
+    Shared(33, Sizes([0, 2, 4], [900, 0], [70, 64, 900, 33], 30, 16, 2, 64, 16), "bf16").run()
+
+
 def test_streams_and_graphs():
     """Captured calls of their own workspaces replayed side by side, lengths changing between replays."""
     small, large = Sizes([0, 5, 12], [200, 90], [9] * 12, 1, 16, 2, 128, 16), of_form(("two+", "one"), 128)

@@ -16,6 +16,7 @@ slot and head may be strided in any order (a permuted view of
 from __future__ import annotations
 
 import ctypes
+import functools
 import struct
 import sys
 from typing import Optional, Tuple
@@ -232,6 +233,13 @@ def mx4_attend_workspace_bytes(n_requests: int, query_len: int, max_keys: int, s
     return int(_library().indexer_mx4_attend_workspace_bytes(*sizes))
 
 
+@functools.lru_cache(maxsize=1024)
+def _need_bytes(*sizes):
+    """Workspace of an attention call, which follows from its sizes alone (nine where requests share prefixes)."""
+    return (_lib.indexer_mx4_attend_workspace_bytes if len(sizes) == 7 else
+            _lib.indexer_mx4_attend_shared_workspace_bytes)(*sizes)
+
+
 def _attend(entry, q, k_data, k_scale, v_data, v_scale, block_table, seq_lens, query_len, max_seq_len, sm_scale,
             selected, max_keys, form, out, lse, with_lse, workspace, groups=None):
     torch = _torch
@@ -279,10 +287,9 @@ def _attend(entry, q, k_data, k_scale, v_data, v_scale, block_table, seq_lens, q
         return out, lse
     if workspace is None:
         if groups is None:
-            need = _lib.indexer_mx4_attend_workspace_bytes(requests, query_len, max_keys, selected, heads, kv, d)
+            need = _need_bytes(requests, query_len, max_keys, selected, heads, kv, d)
         else:
-            need = _lib.indexer_mx4_attend_shared_workspace_bytes(requests, query_len, max_seq_len, *groups[2:], heads, kv,
-                                                                  d)
+            need = _need_bytes(requests, query_len, max_seq_len, *groups[2:], heads, kv, d)
         if 0 < need < 2**63:  # sizes the library refuses have none: the call below names them
             workspace = q.new_empty(need, dtype=torch.uint8)
     blocks, size, *strides = pages

@@ -220,6 +220,17 @@ def test_pages_of_any_size_and_place():
         assert torch.equal(t._base[:, off + t.shape[1]:], base[:, off + t.shape[1]:])
 
 
+def test_forks_and_compaction_of_more_caches_than_a_launch_takes():
+    p = Pool(90, 9, 12, 4, seed=14, shapes=((4, 5), (4, 2, 16), (33,)) * 25, dtypes=(torch.uint8, torch.float16, torch.uint8) * 25)
+    p.grow([0, 1], 46, [46, 13])
+    p.fork([0, 1, 1, 0, 0], [2, 3, 4, 5, 8])
+    p.same()
+    p.grow(list(range(9)), 2)
+    p.free([0, 3, 8])
+    p.compact()
+    p.same()
+
+
 def test_a_cache_past_2_to_the_32_bytes():
     t = torch.zeros((70, 1 << 26), dtype=torch.uint8, device=DEV)
     t[68, 5], t[69, -1] = 3, 4

@@ -343,7 +343,7 @@ Mx4Plan plan_mx4_attend(int n_requests, int q_len, int64_t max_keys, bool select
 // 32 160 and 213, 64 293 and 407; 32 over 8192 38 and 31, 64 over 8192 47 and 46,
 // 128 over 8192 64 and 73.
 static Mx4Plan plan_prefix(int n_groups, int rows_of, int64_t all_rows, int keys, int n_heads, int n_kv, int head_dim,
-                           int most_shares) {
+                           int most_shares, double *time) {
     constexpr int kCus = 256;
     Mx4Plan p = plan_mx4_attend(n_groups, rows_of, keys, false, n_heads, n_kv, head_dim);
     const int64_t rows = (int64_t)n_groups * rows_of, n_m = (int64_t)rows_of * (n_heads / n_kv);
@@ -361,9 +361,10 @@ static Mx4Plan plan_prefix(int n_groups, int rows_of, int64_t all_rows, int keys
         const int64_t items = (n_groups * tiles < real ? n_groups * tiles : real) * n_kv;
         const double fill = (double)n_m / (double)(tiles * 256);
         const int step = prompt ? 64 : 32 * waves, steps = (keys + step - 1) / step;  // of a workgroup
+        const int slots = !prompt && head_dim == 192 ? 2 * kCus : kCus;  // workgroups of half as many waves, side by side
         for (int s = 1; s <= most_shares && s <= steps; ++s) {
             if (!one_launch((n_groups * tiles + 7) * n_kv * s, kMx4PromptThreads)) break;
-            const double rounds = (double)((items * s + kCus - 1) / kCus);
+            const double rounds = (double)((items * s + slots - 1) / slots);
             const double each = prompt ? 2.05 * (0.76 + 0.24 * fill) : 1.7;
             const double t = 10.0 + rounds * (double)((steps + s - 1) / s) * each * wide + s * part +
                              (double)((s + waves - 1) / waves) * 0.8 * wide;
@@ -374,7 +375,9 @@ static Mx4Plan plan_prefix(int n_groups, int rows_of, int64_t all_rows, int keys
             q.m_tiles = (int)tiles;
         }
     }
-    return best < HUGE_VAL ? sized(q, rows, n_heads, n_kv, head_dim) : sized(p, rows, n_heads, n_kv, head_dim);
+    if (best == HUGE_VAL) return sized(p, rows, n_heads, n_kv, head_dim);
+    *time = best;
+    return sized(q, rows, n_heads, n_kv, head_dim);
 }
 
 // About how long attention of `units` units of n_m rows to `keys` keys takes in
@@ -396,10 +399,10 @@ static double estimate(const Mx4Plan &p, int64_t units, int64_t rows, int64_t n_
         const double tiles = (double)units * (double)((n_m + 16 * p.mt - 1) / (16 * p.mt)) * (n_kv / p.hp) *
                              (double)((keys + 31) / 32);
         const double rate = tiles / (4 * kCus) * (p.hp == 2 ? 1.4 : p.mt == 1 ? 0.68 : 0.85);
-        const double chain = (double)((keys + 32 * waves - 1) / (32 * waves)) * (p.hp == 2 || p.mt == 2 ? 1.7 : 0.95);
-        t = 7.0 + (rate > chain ? rate : chain) * wide;
+        const double chain = (double)((keys + 32 * waves - 1) / (32 * waves)) * (p.hp == 2 || p.mt == 2 ? 1.7 : 1.3);
+        t = 6.3 + (rate > chain ? rate : chain) * wide;
     }
-    if (join && p.n_splits > 1) t += 4.5 + (double)rows * n_heads * (1.2e-3 + p.n_splits * head_dim * 8 / 4.5e6);
+    if (join && p.n_splits > 1) t += 3.3 + (double)rows * n_heads * (1.2e-3 + p.n_splits * head_dim * 8 / 4.5e6);
     return t;
 }
 
@@ -444,16 +447,17 @@ Mx4SharedPlan plan_mx4_shared(int n_requests, int q_len, int max_seq_len, int n_
             p.own.n_splits = kMx4MaxSplits / 4;
             p.own = sized(p.own, rows, n_heads, n_kv, head_dim);
         }
+        double first = 0.0;
         p.prefix = plan_prefix(n_groups, max_group * q_len, rows, prefix_keys, n_heads, n_kv, head_dim,
-                               kMx4MaxSplits - p.own.n_splits);
+                               kMx4MaxSplits - p.own.n_splits, &first);
         const int64_t group_rows = n_m * (((int64_t)n_requests + n_groups - 1) / n_groups);
+        if (first == 0.0)
+            first = estimate(p.prefix, n_groups, rows, group_rows, prefix_keys, n_heads, n_kv, head_dim, false) +
+                    (double)rows * n_heads * p.prefix.n_splits * head_dim * 8 / 4.5e6 +
+                    ceil(p.prefix.n_splits * 64.0 / mx4_wave_threads(head_dim, 1)) * 0.8 * head_dim / 128;
         const bool joined = !p.own.prompt && p.own.n_splits == 1;
-        const double apart =
-            estimate(p.prefix, n_groups, rows, group_rows, prefix_keys, n_heads, n_kv, head_dim, false) +
-            (double)rows * n_heads * p.prefix.n_splits * head_dim * 8 / 4.5e6 +
-            ceil(p.prefix.n_splits * 64.0 / mx4_wave_threads(head_dim, 1)) * 0.8 * head_dim / 128 +
-            estimate(p.own, n_requests, rows, n_m, own_keys, n_heads, n_kv, head_dim, true) +
-            (joined || p.own.n_splits > 1 ? 0.0 : 4.5 + (double)rows * n_heads * 1.2e-3);
+        const double apart = first + estimate(p.own, n_requests, rows, n_m, own_keys, n_heads, n_kv, head_dim, true) +
+                             (joined || p.own.n_splits > 1 ? 0.0 : 4.5 + (double)rows * n_heads * 1.2e-3);
         const Mx4Plan all = alone(max_seq_len);
         p.whole = all.fits && estimate(all, n_requests, rows, n_m, max_seq_len, n_heads, n_kv, head_dim, true) < apart;
         if (p.whole) {
@@ -461,7 +465,7 @@ Mx4SharedPlan plan_mx4_shared(int n_requests, int q_len, int max_seq_len, int n_
             p.prefix = Mx4Plan{};
         }
     }
-    p.finish = !p.own.prompt && p.own.n_splits == 1;
+    p.finish = p.own.n_splits == 1 && (!p.own.prompt || !p.prefix.n_splits);  // (tiles of 256 rows begin with nothing)
     const int own_shares = p.finish ? 0 : p.own.n_splits;
     p.shares = p.prefix.n_splits + own_shares;
     const size_t parts = (size_t)rows * n_heads * p.shares;

@@ -1305,7 +1305,7 @@ __global__ void __launch_bounds__(kMx4PromptThreads, 2) mx4_prompt_kernel(Mx4Att
         const int t = token_in(m), token = req * a.q_len + t, head = it.kv * a.group + m - t * a.group;
         const int64_t th = (int64_t)token * a.n_heads + head;
         const int64_t share = MODE >= kOwn ? th * a.shares + a.first_share + it.split : th * a.n_splits + it.split;
-        const bool partial = MODE >= kOwn || a.n_splits > 1;
+        const bool partial = MODE == kPrefix || (MODE == kOwn ? !a.finish : a.n_splits > 1);
         const float inv = partial ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {

@@ -130,8 +130,8 @@ Mx4Plan plan_mx4_attend(int n_requests, int q_len, int64_t max_keys, bool select
 
 // Requests that share prefixes: the prefixes' keys for all rows of a group of
 // requests, then each request's own keys, and a join of the two parts' shares,
-// by the second launch where it has all of a row's own keys in one workgroup,
-// else by a third.
+// by the second launch where it has all of a row's own keys in one workgroup
+// of waves (or there is nothing to join), else by a third.
 struct Mx4SharedPlan {
     Mx4Plan prefix, own;
     bool whole;  // no part of the prefix's own: its keys are few, and cost less than a launch

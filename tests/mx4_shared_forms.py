@@ -76,16 +76,16 @@ FORMS = {
                       192: (100, 1, 1500, 64, 8, 1, 1), 256: (100, 1, 3000, 8, 8, 1, 1)},
     ("one+", "pairs"): {64: (128, 1, 1500, 64, 8, 8, 8), 96: (128, 1, 3000, 8, 8, 8, 8), 128: (128, 1, 1500, 8, 8, 8, 8)},
     ("one+", "one+"): {192: (100, 1, 6000, 1500, 8, 1, 1)},
-    ("two", "one"): {64: (100, 4, 3000, 64, 1, 16, 8), 96: (200, 2, 1500, 8, 2, 16, 4), 128: (200, 4, 1500, 64, 1, 8, 4),
-                     192: (200, 1, 200, 8, 1, 32, 16), 256: (200, 4, 200, 8, 1, 16, 16)},
-    ("two", "pairs"): {64: (200, 4, 1500, 8, 1, 8, 8), 96: (100, 4, 800, 8, 1, 32, 16), 128: (128, 4, 800, 8, 2, 16, 8)},
-    ("two+", "one"): {64: (200, 4, 1500, 8, 1, 4, 4), 96: (100, 1, 6000, 8, 1, 1, 1), 128: (64, 1, 6000, 8, 1, 1, 1),
+    ("two", "one"): {64: (100, 4, 3000, 64, 1, 16, 8), 96: (200, 4, 3000, 8, 1, 8, 4), 128: (200, 4, 1500, 64, 1, 8, 4),
+                     192: (200, 4, 400, 8, 1, 16, 16), 256: (200, 4, 800, 8, 1, 8, 8)},
+    ("two", "pairs"): {64: (200, 4, 1500, 8, 1, 8, 8), 96: (200, 4, 800, 8, 1, 8, 8), 128: (200, 4, 800, 8, 1, 8, 8)},
+    ("two+", "one"): {64: (200, 1, 6000, 8, 1, 1, 1), 96: (100, 1, 6000, 8, 1, 1, 1), 128: (200, 1, 3000, 8, 1, 1, 1),
                       192: (200, 1, 1500, 8, 1, 1, 1), 256: (128, 4, 3000, 8, 1, 1, 1)},
     ("two+", "pairs groups"): {64: (128, 1, 800, 8, 1, 16, 16), 96: (200, 1, 400, 8, 1, 16, 16), 128: (128, 2, 400, 8, 1, 16, 16)},
-    ("two+", "two"): {64: (100, 32, 6000, 64, 2, 1, 1), 96: (128, 32, 6000, 32, 1, 1, 1), 128: (32, 100, 3000, 100, 1, 1, 1),
+    ("two+", "two"): {64: (24, 100, 12000, 100, 1, 1, 1), 96: (24, 100, 6000, 200, 1, 1, 1), 128: (24, 100, 6000, 200, 1, 1, 1),
                       192: (48, 100, 1500, 100, 1, 1, 1), 256: (24, 100, 1500, 100, 1, 1, 1)},
-    ("two+", "two+"): {128: (24, 100, 12000, 3000, 1, 1, 1), 192: (8, 100, 3000, 1500, 1, 4, 1), 256: (12, 100, 6000, 1500, 1, 2, 2)},
-    ("two+", "one+"): {96: (64, 1, 12000, 3000, 1, 1, 1), 192: (48, 2, 12000, 600, 1, 1, 1), 256: (48, 1, 12000, 600, 1, 1, 1)},
+    ("two+", "two+"): {128: (24, 100, 12000, 3000, 1, 1, 1), 192: (12, 100, 12000, 600, 1, 1, 1), 256: (12, 100, 6000, 1500, 1, 2, 2)},
+    ("two+", "one+"): {96: (100, 1, 12000, 3000, 1, 1, 1), 192: (48, 2, 12000, 600, 1, 1, 1), 256: (48, 1, 12000, 600, 1, 1, 1)},
     ("prompt", "one"): {64: (200, 4, 1500, 8, 2, 64, 16), 96: (128, 4, 800, 8, 1, 128, 32), 128: (200, 4, 1500, 8, 1, 64, 16)},
     ("prompt", "prompt"): {64: (64, 100, 12000, 100, 2, 8, 8), 96: (64, 100, 6000, 200, 1, 8, 8),
                            128: (128, 100, 6000, 100, 1, 4, 4)},
@@ -95,7 +95,8 @@ FORMS = {
     ("prompt+", "ahead"): {64: (128, 4, 12000, 3000, 1, 8, 2), 128: (200, 2, 12000, 3000, 1, 8, 1)},
     ("prompt+", "prompt"): {64: (200, 100, 6000, 100, 1, 8, 1), 96: (100, 100, 6000, 100, 1, 2, 1),
                             128: (100, 100, 6000, 100, 1, 2, 1)},
-    ("ahead", "one"): {64: (128, 1, 3000, 8, 64, 4, 4), 96: (200, 2, 3000, 64, 100, 2, 2), 128: (100, 1, 3000, 64, 50, 4, 4)},
+    ("prompt+", "prompt+"): {96: (100, 100, 12000, 1500, 1, 2, 1)},
+    ("ahead", "one"): {64: (128, 1, 3000, 8, 64, 4, 4), 96: (128, 1, 3000, 8, 64, 4, 4), 128: (100, 1, 3000, 64, 50, 4, 4)},
     ("ahead+", "one"): {64: (100, 2, 12000, 200, 50, 1, 1), 96: (200, 1, 6000, 8, 100, 1, 1), 128: (200, 1, 6000, 8, 100, 1, 1)},
     ("pairs", "pairs groups"): {64: (128, 2, 800, 8, 64, 16, 16), 96: (200, 2, 400, 8, 100, 16, 16),
                                 128: (200, 2, 400, 8, 100, 16, 16)},

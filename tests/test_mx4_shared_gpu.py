@@ -105,6 +105,33 @@ def test_every_form(names, d, kind):
     assert torch.isnan(out[:s.query]).any()
 
 
+@pytest.mark.parametrize("names,d,kind", [
+    (("one", "one"), 128, "f16"), (("one+", "one"), 64, "bf16"), (("one+", "pairs"), 96, "f16"), (("two", "one"), 128, "bf16"),
+    (("two", "pairs"), 64, "f16"), (("two+", "one"), 192, "bf16"), (("two+", "two"), 128, "f16"), (("two+", "two+"), 256, "f16"),
+    (("two+", "one+"), 192, "f16"), (("prompt", "one"), 96, "f16"), (("prompt", "prompt"), 128, "bf16"),
+    (("prompt+", "one"), 128, "f16"), (("prompt+", "prompt+"), 96, "bf16"), (("ahead", "one"), 128, "f16"),
+    (("ahead+", "one"), 64, "f16")], ids=str)
+def test_requests_that_end_inside_the_prefix(names, d, kind):
+    """With the prefix in a part of its own: requests that end inside it, that hold fewer keys than they have query rows
+    or none, and a first and a last one that are of no group."""
+    s = of_form(names, d)
+    rng, last = np.random.default_rng(41), len(s.own) - 1
+    starts = [min(max(x, 1), last) for x in s.starts]
+    own = list(s.own)
+    for g, prefix in enumerate(s.prefixes):
+        for r in range(starts[g], starts[g + 1]):
+            if r % 3 == 1:
+                own[r] = -int(rng.integers(1, prefix))
+            elif r % 7 == 3:
+                own[r] = -prefix + int(rng.integers(1, s.query + 1))
+    own[0], own[last] = 40, max(s.query, 33)
+    s = s._replace(starts=starts, own=own)
+    assert form_kind(taken(s)[0]) != "none"
+    case = Shared(42, s, kind)
+    case.rows = np.unique(np.concatenate([case.rows, rng.integers(0, (last + 1) * s.query, 20)]))
+    case.run(f"{names} {d}")
+
+
 SHAPES = [
     Sizes([0, 1], [1], [1], 1, 1, 1, 64, 1),
     Sizes([0, 3], [40], [1, 7, 30], 1, 8, 8, 128, 16),
@@ -259,10 +286,12 @@ def test_other_layouts(order):
 
 def test_given_outputs_and_no_lse():
     """Strided outputs, no lse, a workspace of the caller's; nothing else is written."""
-    case = Shared(12, of_form(("two+", "one"), 64), "bf16")
-    want = case.run()
-    room = torch.full((800, 5, 80), 5.0, dtype=torch.bfloat16, device=DEV)
-    need = li.mx4_attend_shared_workspace_bytes(200, 4, case.max_seq_len, 1, 200, 1500, 4, 4, 64)
+    s = of_form(("two+", "one"), 64)
+    case = Shared(12, s, "bf16")
+    want, requests = case.run(), len(s.own)
+    room = torch.full((requests * s.query, s.heads + 1, 80), 5.0, dtype=torch.bfloat16, device=DEV)
+    need = li.mx4_attend_shared_workspace_bytes(requests, s.query, case.max_seq_len, 1, requests, max(s.prefixes), s.heads,
+                                                s.kv, 64)
     assert need > 0
     workspace = torch.zeros(need + 256, dtype=torch.uint8, device=DEV)
     out, lse = li.mx4_attend_shared(*case.args(), case.max_seq_len, case.sm_scale, **case.groups(), out=room[:, 1:, 8:72],

@@ -4,8 +4,10 @@
 // A row (a token's head) is read once and written once, so this is
 // memory-bound: 4 bytes a value.  `lanes` neighbouring lanes hold a row, each
 // VEC pairs as one wide load of first and one of second values (for pairs of
-// neighbours two consecutive loads), so a rotation never leaves its lane and
-// the norm is a sum over `lanes` lanes by lane moves.  A wave takes a token (or
+// neighbours one of whole pairs from each half of the row), so a rotation never
+// leaves its lane and the norm is a sum over `lanes` lanes by lane moves (4096
+// tokens of 128 + 16 heads of 128: 49 us either way; neighbours as two consecutive
+// loads 62).  A wave takes a token (or
 // with few tokens some of its rows) and has kBatch steps of 64 / lanes rows on
 // the way; rows, weights, positions and frequencies are asked for together.
 //
@@ -90,11 +92,12 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(Rope a) {
     const int all = a.heads[0] + a.heads[1];
     const int end = (int64_t)blockIdx.x * kWaves + wave < a.n_tokens ? min(first + a.steps, (all + ROWS - 1) / ROWS) : first;
 
-    // the lane's pairs: i0 .. i0 + VEC, and where their values lie in a row
-    const int i0 = (lane & (LANES - 1)) * VEC;
-    const bool inside = i0 < a.head_dim / 2, turns = i0 < a.n_freq;
-    const int at0 = !inside ? 0 : NEIGHBOURS ? 2 * i0 : (turns ? i0 : i0 + a.n_freq);
-    const int at1 = !inside ? 0 : NEIGHBOURS ? 2 * i0 + VEC : (turns ? i0 + a.n_freq : i0 + a.head_dim / 2);
+    // the lane's pairs: i0 .. i0 + VEC, or of neighbours half of them from either
+    // half of the row (first0, first1), and where their values lie in a row
+    const int i0 = (lane & (LANES - 1)) * VEC, first0 = NEIGHBOURS ? i0 / 2 : i0, first1 = a.head_dim / 4 + i0 / 2;
+    const bool inside = i0 < a.head_dim / 2, turns = first0 < a.n_freq, turns1 = NEIGHBOURS ? first1 < a.n_freq : turns;
+    const int at0 = !inside ? 0 : (NEIGHBOURS || turns ? i0 : i0 + a.n_freq);
+    const int at1 = !inside ? 0 : (!NEIGHBOURS && turns ? i0 + a.n_freq : i0 + a.head_dim / 2);
 
     struct Row {
         words x0, x1;
@@ -160,8 +163,9 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(Rope a) {
     float c[VEC], s[VEC];
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
-        c[j] = turn[wave][0][turns ? i0 + j : j];
-        s[j] = turn[wave][1][turns ? i0 + j : j];
+        const int i = NEIGHBOURS && j >= VEC / 2 ? (turns1 ? first1 - VEC / 2 : 0) : (turns ? first0 : 0);
+        c[j] = turn[wave][0][i + j];
+        s[j] = turn[wave][1][i + j];
     }
 
     const int64_t q_osh = held(a.ysh[0]), k_osh = held(a.ysh[1]);
@@ -207,9 +211,10 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(Rope a) {
                     x[VEC + j] = x[VEC + j] * r * w[at1 + j];
                 }
             }
-            if (turns) {
+            if (turns || turns1) {
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) {
+                    if (NEIGHBOURS && !(j < VEC / 2 ? turns : turns1)) continue;
                     float &u = x[NEIGHBOURS ? 2 * j : j], &v = x[NEIGHBOURS ? 2 * j + 1 : VEC + j];
                     const float p = u * c[j] - v * s[j], q = v * c[j] + u * s[j];
                     u = p;

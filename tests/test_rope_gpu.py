@@ -60,6 +60,8 @@ def dev(a, dtype=None):
     (33, 16, 16, 80, 40, 3, False), (5, 7, 3, 72, 36, 2, False), (9, 4, 4, 72, 16, 4, True), (4, 1, 0, 256, 128, 4, False),
     (65, 6, 2, 96, 20, 1, False), (17, 12, 4, 192, 96, 1, True), (130, 2, 1, 32, 8, 2, True), (11, 33, 5, 64, 32, 1, False),
     (2, 9, 1, 248, 124, 1, True), (2, 3, 2, 248, 124, 1, False), (19, 8, 8, 40, 20, 1, False), (6, 200, 3, 128, 32, 1, False),
+    (3, 7, 2, 128, 16, 1, True), (3, 7, 2, 128, 32, 2, True), (3, 7, 2, 128, 48, 1, True), (5, 3, 1, 256, 72, 4, True),
+    (5, 3, 1, 72, 20, 1, True), (5, 3, 1, 40, 12, 2, True), (2, 2, 2, 8, 4, 1, True), (2, 2, 2, 16, 8, 1, True),
     (4100, 2, 1, 64, 32, 1, False), (4097, 9, 2, 48, 24, 3, True),
 ])
 def test_against_the_plain_form(kind, n, hq, hk, d, m, axes, interleaved):

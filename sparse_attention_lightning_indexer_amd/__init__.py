@@ -527,7 +527,8 @@ __all__ = [
     "score_topk_fused_decode", "score_topk_fused_decode_noalloc", "score_topk_fused_decode_blocks",
     "topk_blocks", "pool_keys", "score_topk_stream_prefill", "workspace_bytes", "load_library", "IndexerError",
     "EXPORTS", "MAX_K_TOP", "mx4_cache_write", "mx4_cache_read", "mx4_attend_selected", "mx4_attend_window",
-    "mx4_attend_workspace_bytes", "mx4_attend_shared", "mx4_attend_shared_workspace_bytes", "MX4_EXPORTS", "norm_rope", "ROPE_EXPORTS", "PageSet",
+    "mx4_attend_workspace_bytes", "mx4_attend_shared", "mx4_attend_shared_workspace_bytes", "MX4_EXPORTS",
+    "norm_rope", "ROPE_EXPORTS", "PageSet",
     "pages_copy", "pages_fork", "pages_grow", "pages_free", "pages_compact", "pages_compact_workspace_bytes",
     "PAGES_EXPORTS",
 ]

@@ -73,11 +73,15 @@ indexer_status indexer_pages_copy(const indexer_pages_copy_args *args);
  * where len is not a multiple of block_size a free page, with a copy of the
  * parent's last, partly filled page in every cache; the rest of its row is
  * -1, its seq_len len (at most n_cols * block_size).  Where no page is free
- * the child is left empty (row -1, seq_len 0).  What a child's row held is
- * overwritten: free it first.  No row is both a child and a parent.
+ * the child is left empty (row -1, seq_len 0).  Where the parent's last page is
+ * not of the pool, the child has none there either: the page of its turn stays
+ * free, and its last tokens are as little there as the parent's.  What a
+ * child's row held is overwritten: free it first.  No row is both a child and a
+ * parent.
  *
- *   fresh  i32 [n], out: the page a child got for its last tokens; -1 it
- *          needed none; -2 there was none; -3 the pair was skipped
+ *   fresh  i32 [n], out: the page a child got for its last tokens; -1 it got
+ *          none (it needed none, or its parent's is not of the pool); -2 no
+ *          page was free; -3 the pair was skipped
  *
  * arrays may be NULL (n_arrays 0): no page is copied.
  */

@@ -52,10 +52,10 @@ def fork(caches, refs, table, lens, parents, children, bs):
         row += [-1] * (cols - full)
         page = -1
         if rest:
-            page = free.pop(0)
-            refs[page] = 1
-            row[full] = page
+            turn = free.pop(0)
             if 0 <= table[p][full] < len(refs):
+                page = row[full] = turn
+                refs[page] = 1
                 for a in caches:
                     a[page] = a[table[p][full]]
         table[c], lens[c] = row, length

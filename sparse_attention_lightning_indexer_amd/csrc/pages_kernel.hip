@@ -224,7 +224,8 @@ __device__ __forceinline__ void fork_rows(const PageFork &a, unsigned group) {
     if (c >= t.n_cols) return;
     int page[kGroup];
 #pragma unroll
-    for (int k = 0; k < kGroup; ++k) page[k] = c < full_of[k] ? t.table[(int64_t)parent_of[k] * t.stride + c] : -1;
+    for (int k = 0; k < kGroup; ++k)
+        page[k] = c < full_of[k] || (c == full_of[k] && fresh_of[k] >= 0) ? t.table[(int64_t)parent_of[k] * t.stride + c] : -1;
     int held = -1, times = 0;
 #pragma unroll
     for (int k = 0; k < kGroup; ++k) {
@@ -237,8 +238,13 @@ __device__ __forceinline__ void fork_rows(const PageFork &a, unsigned group) {
                 times = 0;
             }
             ++times;
-        } else if (c == full_of[k]) {
-            mine = fresh_of[k] >= 0 ? fresh_of[k] : -1;
+        } else if (mine >= 0) {
+            mine = fresh_of[k];
+        } else if (c == full_of[k] && fresh_of[k] >= 0) {
+            // the parent's last page is none of the pool's, and the child has none either: the page
+            // stays free, whose bytes are another's (copies of it read the same entry and leave it)
+            t.refs[fresh_of[k]] = 0;
+            a.fresh[i0 + k] = -1;
         }
         t.table[(int64_t)child_of[k] * t.stride + c] = mine;
     }

@@ -135,9 +135,10 @@ def pages_copy(pages, source, target) -> None:
 def pages_fork(pages, refs, block_table, seq_lens, parents, children, block_size: int, fresh=None):
     """Requests children[i] (rows of the table) begin as requests parents[i]
     are: they share the parents' full pages and get a copy of the last, partly
-    filled one.  -> fresh i32 [n]: the page of the copy, -1 none needed, -2
-    none free (the child is empty), -3 skipped (a row that is not there, or a
-    child named before).  What a child held is overwritten: free it first.
+    filled one.  -> fresh i32 [n]: the page of the copy, -1 none needed (or the
+    parent's is not of the pool, then the child has none either), -2 none free
+    (the child is empty), -3 skipped (a row that is not there, or a child named
+    before).  What a child held is overwritten: free it first.
     pages None: no bytes are copied."""
     lib = _library()
     dev, n_pages = _refs(refs)

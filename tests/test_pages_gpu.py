@@ -368,3 +368,27 @@ def test_the_same_pages_every_time():
         p.grow(list(range(64)), 5)
         results.append((p.g_refs.clone(), p.g_table.clone()))
     assert all(torch.equal(a, b) for r in results[1:] for a, b in zip(r, results[0]))
+
+
+def test_a_child_of_a_row_without_its_last_page_has_none_either():
+    """A parent whose partly filled last page is none of the pool's hides its last tokens: the child takes no page, which
+    would show them bytes of whoever held it before.  The page of its turn stays free, later children get theirs."""
+    p = Pool(60, 40, 6, 4, seed=15, shapes=((4, 3),), dtypes=(torch.uint8,))
+    p.grow([0, 1, 2, 3, 4], 18, [18, 18, 18, 16, 2])
+    for row, column, page in ((0, 4, -1), (1, 4, 60), (4, 0, -2**31)):
+        p.refs[p.table[row][column]] -= 1
+        p.table[row][column] = page
+    p.put()
+    parents = [0, 2, 1, 3, 4, 2, 0, 0, 2, 1, 4]
+    got = li.pages_fork(p.set, p.g_refs, p.g_table, p.g_lens, ints(parents), ints(list(range(10, 21))), p.bs).tolist()
+    assert [f >= 0 for f in got] == [x == 2 for x in parents] and min(got) == -1
+    assert p.g_lens.tolist()[10:21] == [18, 18, 18, 16, 2, 18, 18, 18, 18, 18, 2]
+    table = p.g_table.tolist()
+    assert all(table[10 + i][4] == -1 for i, x in enumerate(parents) if x in (0, 1)) and table[14] == table[20] == [-1] * 6
+    assert got == plain.fork(p.caches, p.refs, p.table, p.lens, parents, list(range(10, 21)), p.bs)
+    p.same()
+    p.grow(list(range(10, 21)), 1)       # those children do not grow, as their parents would not
+    p.same()
+    p.free(list(range(40)))
+    p.same()
+    assert max(p.refs) == 0              # nothing is held without a request

@@ -392,3 +392,69 @@ def test_a_child_of_a_row_without_its_last_page_has_none_either():
     p.free(list(range(40)))
     p.same()
     assert max(p.refs) == 0              # nothing is held without a request
+
+
+def _long_list(rng, rows, n):
+    """Rows in any order, the same row on both sides of each 1024th entry, named again far behind, and padding."""
+    out = rng.permutation(rows)[:n].tolist()
+    out += [-1] * (n - len(out))
+    for at in range(1024, n, 1024):
+        out[at] = out[at - 1]
+    for at in range(7, n, 97):
+        out[at] = (-1, rows, 2**31 - 1, out[at // 2])[at % 4]
+    return out
+
+
+@pytest.mark.parametrize("n", [1023, 1024, 1025, 2500, 8192])
+def test_long_lists(n):
+    """Lists of more entries than the deciding workgroup looks at in one step, in tables as long as they may be."""
+    rows = 8192
+    p = Pool(3 * n, rows, 6, 4, seed=n, shapes=((3,), (4, 4)), dtypes=(torch.uint8, torch.float16))
+    rng = p.rng
+    members = _long_list(rng, rows, n)
+    p.grow(members, 24, rng.choice([0, 1, 3, 4, 5, 9], n).tolist())
+    p.same("some pages each")
+    p.grow(_long_list(rng, rows, n), 1)
+    p.same("one token each")
+    # parents and children in any order: full pages shared, a copy of the last one
+    order = rng.permutation(rows).tolist()
+    parents, children = order[:600], order[600:]
+    p.free(children)
+    p.same("children freed")
+    child = _long_list(rng, len(children), n)
+    child = [children[c] if 0 <= c < len(children) else c for c in child]
+    parent = [parents[i] for i in rng.integers(0, 600, n)]
+    for at in range(5, n, 61):
+        parent[at] = (-1, rows)[at % 2]
+    p.fork(parent, child)
+    p.same("forked")
+    p.free(_long_list(rng, rows, n))
+    p.same("freed")
+    p.compact()
+    p.same("moved together")
+
+
+@pytest.mark.parametrize("n,free", [(2500, 1030), (2500, 2047), (8192, 1024), (8192, 5000), (1025, 1024)])
+def test_long_lists_that_run_out_of_pages(n, free):
+    """The pages end behind the first 1024 entries: of those that grow by one page or by several, and of children."""
+    rows = 8192
+    p = Pool(free + 300, rows, 5, 4, seed=n + free, shapes=((5,),), dtypes=(torch.uint8,))
+    rng = p.rng
+    held = sorted(rng.permutation(free + 300)[:300].tolist())
+    for page in held:                       # pages in use anywhere in the pool
+        p.refs[page] = 1
+    p.put()
+    p.grow(_long_list(rng, rows, n), 4)
+    p.same("a page each")
+    p.free(list(range(rows)))
+    p.same("none")
+    p.grow(_long_list(rng, rows, n), 20, rng.choice([0, 2, 4, 7, 20], n, p=[.3, .5, .1, .05, .05]).tolist())
+    p.same("some pages each")
+    p.free(list(range(rows)))
+    order = rng.permutation(rows).tolist()
+    p.grow(order[:3], 7, [7, 4, 6])
+    child = [order[3 + c] if 0 <= c < rows - 3 else c for c in _long_list(rng, rows - 3, n)]
+    p.fork([order[i] for i in rng.choice(3, n, p=[.45, .1, .45])], child)
+    p.same("children")
+    p.compact()
+    p.same("moved together")

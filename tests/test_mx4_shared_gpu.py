@@ -448,3 +448,34 @@ def test_a_server_s_step():
             place, live = li.pages_compact(pages, refs, table)
             assert live.item() == (refs > 0).sum().item() and (table.max() < live).all()
             li.pages_fork(pages, refs, table, lens_, row(*[0] * 4), row(2, 4, 6, 8), bs)
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("names,d", [(("one+", "one"), 128), (("prompt+", "one"), 128), (("none", "ahead"), 64),
+                                     (("two+", "two"), 192), (("prompt+", "prompt+"), 96)], ids=str)
+def test_requests_whose_pages_are_all_gone(names, d, kind):
+    """Requests that name no page of the cache, one of them of no group, beside ones that do: outputs of exactly 0 and
+    lse of -inf, finite ones where some key is left; then with the prefix's pages gone, where own keys are all there is."""
+    s = of_form(names, d)
+    starts = list(s.starts)
+    starts[0] = 1                                   # the first request shares nothing
+    s = s._replace(starts=starts, own=[max(s.query, 40)] + list(s.own[1:]))
+    case = Shared(51, s, kind)
+    gone, requests = [0, 3], len(s.own)
+    if s.starts[1] < requests - 1:
+        gone.append(s.starts[1])                    # the first of another group or of none
+    first = {r: s.starts[g] for g in range(len(s.prefixes)) for r in range(s.starts[g], s.starts[g + 1])}
+    for r in gone:
+        case.table[r] = (-1, case.n_blocks, 2**31 - 1)[r % 3]
+    case.rows = np.unique(np.concatenate([case.rows] + [np.arange(r * s.query, r * s.query + min(s.query, 4)) for r in gone]))
+
+    def dead(out, lse, which):
+        for r in which:
+            at = slice(r * s.query, (r + 1) * s.query)
+            assert (out[at] == 0).all() and torch.isneginf(lse[at]).all(), r
+    out, lse = case.run(f"{names} {d} some gone")
+    dead(out, lse, [r for r in gone if first.get(r, r) in gone])
+    assert torch.isfinite(lse[s.query]).all()
+    case.table[1] = -5                              # the first group's prefix, and what its first request has of its own
+    out, lse = case.run(f"{names} {d} prefix gone")
+    dead(out, lse, [r for r in gone + [1] if first.get(r, r) in gone + [1]])

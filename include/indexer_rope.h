@@ -51,8 +51,9 @@ typedef enum {
  *
  * head_dim a multiple of 8 in [8, 256]; n_freq a multiple of 4 in
  * [0, head_dim / 2]; n_axes in [1, 4]; heads in [1, 1024] each; eps >= 0;
- * rotary_scale finite.  A launch holds fewer than 2^32 threads, 64 a token:
- * 2^26 tokens and more are INDEXER_EINVAL.  n_tokens = 0 enqueues nothing.
+ * rotary_scale finite.  A launch holds fewer than 2^32 threads, 256 for four
+ * tokens: more than 2^26 - 4 tokens are INDEXER_EINVAL.  n_tokens = 0 enqueues
+ * nothing.
  */
 typedef struct {
     const void *q;

@@ -107,4 +107,9 @@ indexer_status indexer_norm_rope(const indexer_norm_rope_args *args) {
     return (indexer_status)lidx::api_launch(lidx::launch_rope(a, p, (hipStream_t)g.stream), "norm and rotation launch");
 }
 
+// Whether a call of these sizes fits a launch, for the tests.  Not part of the interface.
+int32_t lidx_rope_fits(int32_t n_tokens, int32_t heads, int32_t head_dim, int32_t n_freq) {
+    return lidx::plan_rope(n_tokens, heads, head_dim, n_freq).fits;
+}
+
 }  // extern "C"

@@ -79,6 +79,18 @@ def test_refuses(lib, kw, status, msg):
     assert msg in lib.indexer_last_error()
 
 
+@pytest.mark.parametrize("heads,d,m", [(1, 8, 4), (2, 128, 64), (72, 128, 64), (2048, 256, 128), (32, 80, 40)])
+def test_the_most_tokens(lib, heads, d, m):
+    """2^26 - 4 tokens fit a launch of fewer than 2^32 threads, whatever a row is; the next ones are refused."""
+    fits = [lib.lidx_rope_fits(n, heads, d, m) for n in (1, 2**20, 2**26 - 5, 2**26 - 4, 2**26 - 3, 2**26, 2**31 - 1)]
+    assert fits == [1, 1, 1, 1, 0, 0, 0]
+    q, k = (heads, 0) if heads == 1 else (heads // 2, heads - heads // 2)
+    for n in (2**26 - 3, 2**26 - 1, 2**31 - 1):
+        assert call(lib, n=n, hq=q, hk=k, k=A if k else 0, d=d, m=m, qsh=256, ksh=256, qosh=256, kosh=256, qst=2**19,
+                    kst=2**19, qost=2**19, kost=2**19) == li.EINVAL
+        assert b"too large" in lib.indexer_last_error()
+
+
 def test_null_arguments(lib):
     assert lib.indexer_norm_rope(None) == li.EINVAL
     assert b"args is NULL" in lib.indexer_last_error()

@@ -387,14 +387,16 @@ def mx4_attend_shared(q, k_data, k_scale, v_data, v_scale, block_table, seq_lens
     requests begin with the same prefix: its keys are read once for a group.
 
     Requests group_starts[g] to group_starts[g + 1] - 1 (i32 [n_groups + 1],
-    ascending; None: all are one group, of at most max_group each) share their
-    first prefix_lens[g] (i32 [n_groups], at most max_prefix_len) positions,
-    whose pages the group's first request's row of block_table names; later
-    positions are read through each request's own row, as pages_fork makes
-    them.  The work is laid out for max_seq_len - max_prefix_len own keys:
-    requests of far more (of shorter prefixes, or of none) do better in a call
-    of their own.  Other arguments and results as in mx4_attend_window without a
-    window."""
+    ascending) share their first prefix_lens[g] (i32 [n_groups], at most
+    max_prefix_len) positions, whose pages the group's first request's row of
+    block_table names; later positions are read through each request's own row,
+    as pages_fork makes them.  max_group is the most requests of a group: results
+    of a group's requests past it are undefined, and None lays the work out for
+    groups of all requests, which is as right and slower where there are several.
+    group_starts None: all requests are one group, and max_group is not used.
+    The work is laid out for max_seq_len - max_prefix_len own keys: requests of
+    far more (of shorter prefixes, or of none) do better in a call of their own.
+    Other arguments and results as in mx4_attend_window without a window."""
     lib = _library()
     if not isinstance(q, _torch.Tensor):
         raise TypeError("q must be a torch.Tensor")

@@ -479,3 +479,14 @@ def test_requests_whose_pages_are_all_gone(names, d, kind):
     case.table[1] = -5                              # the first group's prefix, and what its first request has of its own
     out, lse = case.run(f"{names} {d} prefix gone")
     dead(out, lse, [r for r in gone + [1] if first.get(r, r) in gone + [1]])
+
+
+def test_the_most_requests_of_a_group_left_out():
+    """max_group None lays several groups out for all requests; with one group of all it is not used, whatever it is."""
+    case = Shared(52, Sizes([0, 3, 4, 9], [700, 33, 300], [9, 0, 40, 64, 5, 33, 7, 8, 1], 1, 16, 2, 128, 16), "bf16")
+    case.run("several groups", max_group=None)
+    case = Shared(53, Sizes([0, 6], [900], [9, 3, 40, 64, 5, 33], 1, 16, 2, 128, 16), "f16")
+    a = case.run("all")
+    for most in (0, 2, 6):
+        b = case.run(f"max_group={most}", group_starts=None, max_group=most)
+        assert all(torch.equal(x, y) for x, y in zip(a, b))

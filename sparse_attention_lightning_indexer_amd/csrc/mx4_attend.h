@@ -53,7 +53,8 @@
 // keys 9.5 us (f16: the latency of dependent loads and few tiles a wave).  What is
 // loaded ahead is used as loaded, in a later tile (scale bytes as bytes), and q is
 // known to have arrived before the loop: a value widened at once, or first used
-// in the loop, has the compiler wait there for every load on the way.
+// in the loop, has the compiler wait there for every load on the way
+// (windows of head dimension 192 and 256 apart, see below).
 //
 // Masked positions: their scores become -inf by selection, so K's NaN there
 // never spreads; V's blocks of NaN are replaced by zeros in the product, and
@@ -65,6 +66,8 @@
 #pragma once
 
 #include <math.h>
+
+#include <type_traits>
 
 #include "device_common.h"
 #include "mx4_internal.h"
@@ -495,9 +498,15 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
     // blocks (c * KS + s) / 4: at most NB of them
     constexpr int NB = KS % 4 == 0 ? KS / 4 : (KS == 2 ? 1 : 2);
     constexpr int ALIGN = KS % 4 == 0 ? 16 : (KS % 2 == 0 ? 8 : 4);
+    // Scales stay bytes until they are used: widening them at once would wait for them
+    // there.  Windows of head dimension 192 and 256 are quicker with words and without
+    // the wait for q below: full attention of 126 x 2 tokens over 4584 keys at 192 218 us
+    // for 247, 36 x 4 over 21189 at 256 201 for 223, 16 x 100 over 20088 at 256 2449 for
+    // 2559 (selected keys at 192 are 2% slower so in f16).
+    constexpr bool WIDEN = D >= 192 && MODE == kWindow;
     struct Raw {
         uint32_t k[KS], v[KS];
-        uint8_t sk[NB], sv[NB];  // bytes until they are used: widening them at once would wait for them there
+        typename std::conditional<WIDEN, uint32_t, uint8_t>::type sk[NB], sv[NB];
     };
     const int blk0 = ch * KS / 4;
     const uint64_t chunk = (uint64_t)((uint32_t)hsel * (uint32_t)a.pages.d_sh) + (uint32_t)(ch * KS * 4);
@@ -571,7 +580,7 @@ __global__ void __launch_bounds__((Shape<D, HP>::WAVES * 64), (waves_per_simd<D,
     // q, asked for before, has arrived when the first page's id has.  Said here,
     // else its first use, which is in the loop, waits there for all loads on the
     // way in every tile
-    wait_vmem_all_known();
+    if (!WIDEN) wait_vmem_all_known();
     if (any_tile) {
         locate(pos, page);
         if (SHARE) load_part();

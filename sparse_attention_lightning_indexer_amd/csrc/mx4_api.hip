@@ -242,11 +242,13 @@ static Mx4Plan sized(Mx4Plan p, int64_t rows, int n_heads, int n_kv, int head_di
 // and 256 rows a compute unit (1.8 us half full), rounds of one workgroup a
 // compute unit and 10 us, the keys shared out where that fills the last round
 // better, at the price of a second launch and of the shares' traffic; against
-// 0.79 us a SIMD for 32 keys and 32 rows of a wave, and 7 us a round.  Measured,
-// together and apart, 8 query heads a K/V head: 1024 tokens over 16384 keys 557
-// and 841 us, 512 tokens 297 and 403, 1000 under a window of 4096 154 and 217,
-// 1100 under one of 512 75 and 109, 128 under one of 1024 37 and 18, 256 over
-// 2048 52 and 39, 16 tokens of 32 requests over 4096 121 and 138.
+// 0.79 us a SIMD for 32 keys and 32 rows of a wave, and 7 us a round.  (Fit to
+// loops that waited for their loads: either form has since become up to 10%
+// quicker than its estimate.)  Measured as the loops are, back to back in a graph,
+// f16, together and apart, 64 query heads on 8 K/V heads of 128: 1024 tokens over
+// 16384 keys 487 and 795 us, 512 tokens 283 and 403, 1000 under a window of 4096
+// 145 and 219, 1100 under one of 512 69 and 107, 128 under one of 1024 34 and 18,
+// 256 over 2048 48 and 37, 16 tokens of 32 requests over 4096 109 and 123.
 //
 // Where a row's pairs of heads make a multiple of four and the rows fill the
 // chip, the four waves of a workgroup take the same keys of four pairs, instead
@@ -337,11 +339,11 @@ Mx4Plan plan_mx4_attend(int n_requests, int q_len, int64_t max_keys, bool select
 // workgroup, about one a compute unit (a share of a row costs the traffic of a
 // result there and back, and a round of loads in the launch that joins it).
 // Tiles of 256 rows that go through the keys together or waves with 32 rows of
-// their own, whichever is shorter by estimate.  Measured, 64 query heads on 8
-// K/V heads of 128, the whole call with one own key each, together and apart, of
-// their best shares: 8 requests over 131072 keys 125 and 70 us, 16 128 and 116,
-// 32 160 and 213, 64 293 and 407; 32 over 8192 38 and 31, 64 over 8192 47 and 46,
-// 128 over 8192 64 and 73.
+// their own, whichever is shorter by estimate.  Measured back to back in a graph,
+// f16, 64 query heads on 8 K/V heads of 128, the whole call with one own key each,
+// together and apart, of their best shares: 8 requests over 131072 keys 108 and 73
+// us, 16 115 and 119, 32 148 and 218, 64 269 and 419; 32 over 8192 38 and 32, 64
+// over 8192 44 and 47, 128 over 8192 62 and 72.
 static Mx4Plan plan_prefix(int n_groups, int rows_of, int64_t all_rows, int keys, int n_heads, int n_kv, int head_dim,
                            int most_shares, double *time) {
     constexpr int kCus = 256;
@@ -426,11 +428,14 @@ static Mx4Plan unless_joined(const Mx4Plan &p, int64_t units, int64_t rows, int6
 //
 // A short prefix, few requests, or requests of many rows (whose tiles a group
 // does not fill better) are not worth the launch of the prefix's part: then
-// each request reads the prefix's keys itself.  Measured with and without, 64
-// query heads on 8 K/V heads of 128, 32 own keys: 2 requests over 16384 shared
-// keys 21.0 and 16.1 us, 8 over 2048 18.1 and 13.4, over 16384 25.5 and 33.5, 32
-// over 1024 18.9 and 13.0, over 4096 23.9 and 29.7, over 16384 44 and 94, 128
-// over 512 22.6 and 20.8, over 4096 46 and 98.
+// each request reads the prefix's keys itself.  Measured so too with and without,
+// 32 own keys: 2 requests over 16384 shared keys 21.5 and 16.5 us, 8 over 2048
+// 17.7 and 13.1, over 16384 26.3 and 34.4, 32 over 1024 18.3 and 12.1, over 4096
+// 24.4 and 29.7, over 16384 45 and 96, 128 over 512 22.2 and 20.9, over 4096 46
+// and 96.  The rule knows of a request's own keys what the two longest lengths
+// say: where some have far more, they are read by as few workgroups as if they had
+// not (8 requests over 131072 shared keys with 32 of their own 79 us, one of no
+// group and 131072 keys 39 us by the window form, both in one call 751 us).
 Mx4SharedPlan plan_mx4_shared(int n_requests, int q_len, int max_seq_len, int n_groups, int max_group, int max_prefix,
                               int n_heads, int n_kv, int head_dim) {
     Mx4SharedPlan p{};
